@@ -55,9 +55,12 @@ extern "C" {
 #define BAKRON_EWAIT (-4)   /* a solve's bounded wait inside a leaf block gave up
                                (bakron_solve_status): its outputs are invalid */
 
-/* Element types. */
+/* Element types. The calls of the solve take F32 and F64; the 8-bit product
+ * takes F32, BF16 and F16. */
 #define BAKRON_F32 0
 #define BAKRON_F64 1
+#define BAKRON_BF16 2
+#define BAKRON_F16 3
 
 /* Scale modes of the quantizer (§3.1: one scale per row and/or column). */
 #define BAKRON_SCALE_NONE 0 /* s = 1 */
@@ -441,6 +444,42 @@ int bakron_gram(int dtype, int64_t N, int64_t d, const void *X, int64_t ldx,
                 const void *weights, double damp_rel, void *G, int64_t ldg, void *stream);
 int bakron_sample_sqnorms(int dtype, int64_t N, int64_t d, const void *X, int64_t ldx,
                           void *out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit product: what the solve's codes are for. A layer whose weight is
+ * s_i V_ij (V the codes, inside int8; s the row scales) is applied to T tokens
+ * held as int8 with a scale each:
+ *   Y[t][i] = sx[t] * sv[i] * sum_j Xq[t][j] * Vq[i][j].
+ *
+ * bakron_quantize_tokens makes the tokens: with x_j = X[t][j] * channel[j]
+ * (one float32 rounding; channel nullable = all 1; a layer solved with column
+ * scales passes them here),
+ *   sx[t] = max_j |x_j| / 127 (1 for an all-zero token),
+ *   Xq[t][j] = clamp(rint(x_j / sx[t]), -127, 127),
+ * in float32, the division correctly rounded, ties to even. A token that
+ * holds an infinity or a NaN gets a scale that is not finite and codes whose
+ * products with it are NaN.
+ *   xtype  BAKRON_F32, BAKRON_BF16 or BAKRON_F16.
+ *   X      T x n (ldx >= n); Xq out, T x n int8 (ldq >= n; columns past n are
+ *          not written); sx out, float32, length T.
+ *
+ * bakron_matmul_int8: Xq T x n (ldx), Vq m x n (ldv), int8 (any values,
+ * -128 included); sx float32 length T; sv float32 length m, or NULL (all 1).
+ *   ytype  the type of Y (T x m, ldy >= m): F32, BF16 or F16.
+ * The sums over j are exact (int32), for n <= 131071 (BAKRON_EINVAL beyond);
+ * the sum, its product with sx and that with sv are rounded to float32 in this
+ * order, then once to ytype. Rows that start at multiples of 16 bytes
+ * with n a multiple of 16 are read fastest; any alignment and stride works.
+ * Y must not overlap the inputs (BAKRON_EINVAL).
+ *
+ * Both are asynchronous and deterministic. T, m <= 2^31 - 1.
+ * ------------------------------------------------------------------------ */
+int bakron_quantize_tokens(int xtype, int64_t T, int64_t n, const void *X, int64_t ldx,
+                           const float *channel, int8_t *Xq, int64_t ldq, float *sx, void *stream);
+int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n,
+                       const int8_t *Xq, int64_t ldx, const float *sx,
+                       const int8_t *Vq, int64_t ldv, const float *sv,
+                       void *Y, int64_t ldy, void *stream);
 
 #ifdef __cplusplus
 }

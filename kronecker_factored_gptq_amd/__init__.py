@@ -17,16 +17,16 @@ from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-__all__ = ["F32", "F64", "SCALE_NONE", "SCALE_ROW", "SCALE_COL", "BakronError", "lib", "factor",
+__all__ = ["F32", "F64", "BF16", "F16", "SCALE_NONE", "SCALE_ROW", "SCALE_COL", "BakronError", "lib", "factor",
            "factor_batched",
            "solve", "solve_antidiag", "solve_noalloc", "factor_blockdiag", "solve_blockdiag",
            "loss_blockdiag", "solve_batched", "loss", "loss_batched", "row_scales", "row_scales_mse", "gram",
-           "sample_sqnorms", "kfac_factors", "shampoo_factors", "solve_schedule", "tile_size", "workspace_bytes"]
+           "sample_sqnorms", "kfac_factors", "shampoo_factors", "quantize_tokens", "matmul_int8", "solve_schedule", "tile_size", "workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libbakron.so")
 
-F32, F64 = 0, 1
+F32, F64, BF16, F16 = 0, 1, 2, 3
 SCALE_NONE, SCALE_ROW, SCALE_COL = 0, 1, 2
 OK, EINVAL, ENOTSPD, EHIP, EWAIT = 0, -1, -2, -3, -4
 
@@ -133,6 +133,11 @@ def lib() -> ctypes.CDLL:
     L.bakron_gram.restype = _int
     L.bakron_sample_sqnorms.argtypes = [_int, _i64, _i64, _vp, _i64, _vp, _vp]
     L.bakron_sample_sqnorms.restype = _int
+    L.bakron_quantize_tokens.argtypes = [_int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp]
+    L.bakron_quantize_tokens.restype = _int
+    L.bakron_matmul_int8.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                                     _i64, _vp]
+    L.bakron_matmul_int8.restype = _int
     _lib = L
     return L
 
@@ -745,6 +750,97 @@ def shampoo_factors(Xa: torch.Tensor, Xb: torch.Tensor, damp_rel: float = 0.0):
     """One-step Shampoo-style factors A = E[|b|^2 a a^T], B = E[|a|^2 b b^T]
     (§4.2, Appendix A.2)."""
     return gram(Xa, sample_sqnorms(Xb), damp_rel), gram(Xb, sample_sqnorms(Xa), damp_rel)
+
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _ft(dtype: torch.dtype, name: str) -> int:
+    """The element type code of the calls beside the solve."""
+    if dtype not in _FLOATS:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return _FLOATS[dtype]
+
+
+def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None) -> int:
+    """The leading dimension of a 2-D row-major input whose rows may be any
+    distance apart (at least their length)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride (row-major)")
+    if rows <= 1:
+        return max(cols, 1)
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} rows overlap (leading dimension below the row length)")
+    return max(int(t.stride(0)), 1)
+
+
+def _vector(t: Optional[torch.Tensor], n: int, name: str, dtype: torch.dtype = torch.float32) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of length {n}")
+
+
+def quantize_tokens(X: torch.Tensor, channel_scales: Optional[torch.Tensor] = None):
+    """Per-token int8 activations (bakron_quantize_tokens): with x = X[t] *
+    channel_scales (a float32 vector; the column scales of a layer solved with
+    SCALE_COL), sx[t] = max|x| / 127 (1 for an all-zero token) and
+    Xq[t] = clamp(rint(x / sx[t]), -127, 127). X is T x n in float32, bfloat16
+    or float16. Returns Xq (int8, T x n, rows starting at multiples of 16
+    bytes) and sx (float32, T). Asynchronous."""
+    dev = _check_device(X, channel_scales)
+    code = _ft(X.dtype, "X")
+    ldx = _matrix(X, "X")
+    T, n = X.shape
+    _vector(channel_scales, n, "channel_scales")
+    ldq = (n + 15) // 16 * 16
+    Xq = torch.empty((T, ldq), dtype=torch.int8, device=dev)
+    if ldq != n:
+        Xq = Xq[:, :n]
+    sx = torch.empty(T, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        rc = lib().bakron_quantize_tokens(code, T, n, _p(X), ldx, _p(channel_scales), _p(Xq), ldq,
+                                          _p(sx), _stream(dev))
+    if rc != OK:
+        raise BakronError(rc, "bakron_quantize_tokens")
+    return Xq, sx
+
+
+def matmul_int8(Xq: torch.Tensor, sx: torch.Tensor, Vq: torch.Tensor,
+                sv: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.float32,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[t][i] = sx[t] sv[i] sum_j Xq[t][j] Vq[i][j] (bakron_matmul_int8): the
+    tokens of ``quantize_tokens`` through a layer held as the solve's codes.
+    Xq is T x n and Vq m x n, int8 (``V.to(torch.int8)`` of codes inside
+    [-128, 127], made once); sx has length T; sv, the row scales, length m, or
+    None for 1 (column scales go to ``quantize_tokens``). The sums are exact
+    (n <= 131071). Y is T x m in ``out_dtype`` (float32, bfloat16 or float16),
+    or ``out`` and its type. Asynchronous."""
+    dev = _check_device(Xq, sx, Vq, sv, out)
+    ldx, ldv = _matrix(Xq, "Xq", torch.int8), _matrix(Vq, "Vq", torch.int8)
+    (T, n), m = Xq.shape, Vq.size(0)
+    if Vq.size(1) != n:
+        raise ValueError(f"Xq and Vq must have rows of one length, got {n} and {Vq.size(1)}")
+    _vector(sx, T, "sx")
+    _vector(sv, m, "sv")
+    code = _ft(out_dtype if out is None else out.dtype, "out_dtype")
+    if out is None:
+        out = torch.empty((T, m), dtype=out_dtype, device=dev)
+    else:
+        _check_out(out, (T, m), out.dtype, "out")
+    with torch.cuda.device(dev):
+        rc = lib().bakron_matmul_int8(code, T, m, n, _p(Xq), ldx, _p(sx), _p(Vq), ldv, _p(sv),
+                                      _p(out), _ld(out, "out"), _stream(dev))
+    if rc != OK:
+        raise BakronError(rc, "bakron_matmul_int8")
+    return out
 
 
 def debug_set_wait_polls(polls: int) -> int:

@@ -1,0 +1,88 @@
+// C ABI of the calls beside the solve (declared in include/bakron.h): the
+// 8-bit product of quantised tokens with a layer's codes. Host side only:
+// argument checks and the choice of types; nothing here touches data.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "bakron.h"
+#include "launch.hpp"
+#include "tile_product.hpp"
+
+namespace {
+
+using namespace bk;
+
+inline size_t type_size(int t) { return t == BAKRON_F32 ? 4 : t == BAKRON_BF16 || t == BAKRON_F16 ? 2 : 0; }
+inline bool type_ok(int t) { return type_size(t) != 0; }
+
+// whether a matrix of `rows` x `cols` elements of `es` bytes can be addressed
+inline bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es) {
+  if (rows == 0 || cols == 0) return true;
+  return p && ld >= cols && ld <= (INT64_MAX / 8) / rows && (uintptr_t)p % es == 0;
+}
+// whether two matrices' byte ranges intersect
+inline bool overlap(const void* a, int64_t arows, int64_t acols, int64_t lda, size_t ea,
+                    const void* b, int64_t brows, int64_t bcols, int64_t ldb, size_t eb) {
+  if (!a || !b || arows == 0 || acols == 0 || brows == 0 || bcols == 0) return false;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  const uintptr_t a1 = a0 + ((uintptr_t)(arows - 1) * (uintptr_t)lda + (uintptr_t)acols) * ea;
+  const uintptr_t b1 = b0 + ((uintptr_t)(brows - 1) * (uintptr_t)ldb + (uintptr_t)bcols) * eb;
+  return a0 < b1 && b0 < a1;
+}
+inline int status(hipError_t e) { return e == hipSuccess ? BAKRON_OK : BAKRON_EHIP; }
+
+// the largest n whose int8 sums fit int32: 128 * 128 * 131071 < 2^31
+constexpr int64_t kMaxInt8Sum = 131071;
+// the most tiles of 128 x 128 one launch covers
+inline bool tiles_ok(int64_t a, int64_t b) {
+  return ((a + 127) / 128) * ((b + 127) / 128) <= INT_MAX;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bakron_quantize_tokens(int xtype, int64_t T, int64_t n, const void* X, int64_t ldx,
+                           const float* channel, int8_t* Xq, int64_t ldq, float* sx, void* stream) {
+  if (!type_ok(xtype) || T < 0 || n < 0 || T > INT_MAX) return BAKRON_EINVAL;
+  if (T == 0) return BAKRON_OK;
+  if (!matrix_ok(X, T, n, ldx, type_size(xtype)) || !matrix_ok(Xq, T, n, ldq, 1)) return BAKRON_EINVAL;
+  if (!sx || (uintptr_t)sx % 4 || (uintptr_t)channel % 4) return BAKRON_EINVAL;
+  const size_t es = type_size(xtype);
+  if (overlap(Xq, T, n, ldq, 1, X, T, n, ldx, es) || overlap(Xq, T, n, ldq, 1, sx, 1, T, T, 4) ||
+      overlap(sx, 1, T, T, 4, X, T, n, ldx, es) || overlap(Xq, T, n, ldq, 1, channel, 1, n, n, 4) ||
+      overlap(sx, 1, T, T, 4, channel, 1, n, n, 4))
+    return BAKRON_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (xtype == BAKRON_F32)
+    return status(launch_quantize_tokens(T, n, (const float*)X, ldx, channel, Xq, ldq, sx, s));
+  if (xtype == BAKRON_BF16)
+    return status(launch_quantize_tokens(T, n, (const BF16*)X, ldx, channel, Xq, ldq, sx, s));
+  return status(launch_quantize_tokens(T, n, (const F16*)X, ldx, channel, Xq, ldq, sx, s));
+}
+
+int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n, const int8_t* Xq, int64_t ldx,
+                       const float* sx, const int8_t* Vq, int64_t ldv, const float* sv, void* Y,
+                       int64_t ldy, void* stream) {
+  if (!type_ok(ytype) || T < 0 || m < 0 || n < 0 || T > INT_MAX || m > INT_MAX || n > kMaxInt8Sum)
+    return BAKRON_EINVAL;
+  if (T == 0 || m == 0) return BAKRON_OK;
+  const size_t es = type_size(ytype);
+  if (!tiles_ok(T, m) || !matrix_ok(Xq, T, n, ldx, 1) || !matrix_ok(Vq, m, n, ldv, 1) ||
+      !matrix_ok(Y, T, m, ldy, es))
+    return BAKRON_EINVAL;
+  if (!sx || (uintptr_t)sx % 4 || (uintptr_t)sv % 4) return BAKRON_EINVAL;
+  if (overlap(Y, T, m, ldy, es, Xq, T, n, ldx, 1) || overlap(Y, T, m, ldy, es, Vq, m, n, ldv, 1) ||
+      overlap(Y, T, m, ldy, es, sx, 1, T, T, 4) || overlap(Y, T, m, ldy, es, sv, 1, m, m, 4))
+    return BAKRON_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (ytype == BAKRON_F32)
+    return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (float*)Y, ldy, s));
+  if (ytype == BAKRON_BF16)
+    return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (BF16*)Y, ldy, s));
+  return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (F16*)Y, ldy, s));
+}
+
+}  // extern "C"

@@ -271,4 +271,18 @@ template <typename R>
 hipError_t launch_sample_sqnorms(int64_t N, int64_t d, const R* X, int64_t ldx, R* out,
                                  hipStream_t s);
 
+// ---- 8-bit product (product_kernels.hip) ------------------------------------
+// Element types of the calls beside the solve: float, and these two (held as
+// their 16 bits; the kernels compute in float32).
+struct BF16;
+struct F16;
+template <typename X>
+hipError_t launch_quantize_tokens(int64_t T, int64_t n, const X* x, int64_t ldx, const float* c,
+                                  int8_t* q, int64_t ldq, float* s, hipStream_t st);
+// Y (T x m) = sx sv^T (.) (Xq Vq^T), sv nullable (all 1).
+template <typename O>
+hipError_t launch_matmul_int8(int64_t T, int64_t m, int64_t n, const int8_t* Xq, int64_t ldx,
+                              const float* sx, const int8_t* Vq, int64_t ldv, const float* sv, O* Y,
+                              int64_t ldy, hipStream_t s);
+
 }  // namespace bk

@@ -1,0 +1,321 @@
+// The tiled matrix product behind the int8 product, its input gradient and the
+// cross entropy:
+//   D[r][c] = sum over pairs p of sum_k R_p[r][k] C_p[c][k]
+// of two operands whose rows run along k (both k-contiguous), on 16x16 MFMA.
+//
+// Everything about the layout is counted in bytes, so one template serves
+// int8 (64 k per instruction), bfloat16 and float16 (32 k): each takes 64
+// bytes of k per operand row and instruction, lane l holding 16 bytes of row
+// l % 16, and both operands are given the same k per lane, so the order of k
+// inside an instruction does not matter. The result's lane l, register i holds
+// D[4 * (l / 16) + i][l % 16].
+//
+// Pairs of planes: a float32 operand is held as bfloat16 planes x = x1 + x2 +
+// x3 (exact, 8 bits each, split_bf16), and a product is the sum over the pairs
+// of planes whose terms reach the result's precision, all added into the same
+// float32 accumulators (PlanePairs). A bfloat16, float16 or int8 product is
+// the single pair (0, 0).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace bk {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+struct MmaI8 {
+  typedef v4i acc_t;
+  static constexpr int kElem = 1;
+  __device__ static inline acc_t mma(v4i a, v4i b, acc_t c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+  }
+};
+struct MmaBF16 {
+  typedef f32x4 acc_t;
+  static constexpr int kElem = 2;
+  __device__ static inline acc_t mma(v4i a, v4i b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
+                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  }
+};
+struct MmaF16 {
+  typedef f32x4 acc_t;
+  static constexpr int kElem = 2;
+  __device__ static inline acc_t mma(v4i a, v4i b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
+                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
+};
+
+// One operand: `rows` rows of `kbytes` bytes, `ld` bytes apart, in planes
+// `plane` bytes apart.
+struct TileOperand {
+  const char* p;
+  int64_t ld, plane, rows;
+};
+
+// The plane pairs of a product, smallest terms last.
+struct PlanePairs {
+  int n;
+  unsigned char r[6], c[6];
+};
+
+// The largest row stride (and row length, in bytes) the direct loads take: the
+// 32-bit offsets inside a tile of 256 rows stay below 2^31.
+constexpr int64_t kTileMaxLd = (int64_t)1 << 22;
+constexpr int kStepBytes = 128;  // bytes of k per row and pipeline step
+
+// Whether the direct loads (TileProduct::run) can take an operand.
+inline bool tile_direct(const TileOperand& o, int64_t kbytes) {
+  return (uintptr_t)o.p % 16 == 0 && o.ld % 16 == 0 && o.plane % 16 == 0 && kbytes % 16 == 0 &&
+         o.ld <= kTileMaxLd && kbytes <= kTileMaxLd;
+}
+
+// The block of tiles that workgroup b of `nr` x `nc` works on. Workgroups go
+// to the 8 XCDs in turn, so each XCD is given a contiguous run of the tile
+// order, and the order walks groups of 8 c-tiles r-tile by r-tile: the tiles
+// that run together on an XCD share operand rows in its L2.
+__device__ inline void tile_of(unsigned b, unsigned nr, unsigned nc, int& tr, int& tc) {
+  const unsigned total = nr * nc, q = total / 8, rem = total % 8;
+  const unsigned x = b % 8, i = b / 8;
+  const unsigned t = x * q + (x < rem ? x : rem) + i;
+  const unsigned group = t / (8 * nr), first = group * 8;
+  const unsigned width = nc - first < 8 ? nc - first : 8;
+  const unsigned in = t - first * nr;
+  tr = (int)(in / width);
+  tc = (int)(first + in % width);
+}
+
+template <class M, int BR, int BC, int WR, int WC, int STAGES>
+struct TileProduct {
+  typedef typename M::acc_t acc_t;
+  static constexpr int kWaves = WR * WC;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int FR = BR / WR / 16, FC = BC / WC / 16;
+  static constexpr int kStage = (BR + BC) * kStepBytes;
+  static constexpr int kLds = STAGES * kStage;
+  static constexpr int LR = BR * kStepBytes / 1024 / kWaves;  // wave loads per step
+  static constexpr int LC = BC * kStepBytes / 1024 / kWaves;
+  static_assert(LR * kWaves * 1024 == BR * kStepBytes && LC * kWaves * 1024 == BC * kStepBytes,
+                "a step's bytes divide over the waves");
+  static_assert(kWaves % 2 == 0, "the chunk order of a wave's loads does not depend on the load");
+
+  acc_t acc[FR][FC];
+
+  __device__ inline int wave_r() const { return (threadIdx.x >> 6) / WC * (FR * 16); }
+  __device__ inline int wave_c() const { return (threadIdx.x >> 6) % WC * (FC * 16); }
+
+  // LDS holds each operand's rows 128 bytes apart; 16-byte chunk q of row r
+  // lies at position q ^ ((r / 2) % 8), so that the 16 rows a fragment reads
+  // at one q fall on different banks. The loads write LDS in lane order, so
+  // each lane fetches the chunk that belongs at its place.
+  __device__ static inline int chunk_at(int row, int pos) { return pos ^ ((row >> 1) & 7); }
+
+  // One step's compute from LDS.
+  __device__ inline void compute(const char* lds) {
+    const int lane = threadIdx.x & 63;
+    const int r16 = lane & 15, q = lane >> 4;
+    const char* lr = lds + (wave_r() + r16) * kStepBytes;
+    const char* lc = lds + BR * kStepBytes + (wave_c() + r16) * kStepBytes;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int off = chunk_at(r16, kk * 4 + q) * 16;
+      v4i fr[FR], fc[FC];
+#pragma unroll
+      for (int i = 0; i < FR; ++i) fr[i] = *(const v4i*)(lr + i * 16 * kStepBytes + off);
+#pragma unroll
+      for (int j = 0; j < FC; ++j) fc[j] = *(const v4i*)(lc + j * 16 * kStepBytes + off);
+#pragma unroll
+      for (int j = 0; j < FC; ++j)
+#pragma unroll
+        for (int i = 0; i < FR; ++i) acc[i][j] = M::mma(fr[i], fc[j], acc[i][j]);
+    }
+  }
+
+  __device__ inline void zero() {
+#pragma unroll
+    for (int i = 0; i < FR; ++i)
+#pragma unroll
+      for (int j = 0; j < FC; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
+  }
+
+  // 64 lanes x 16 bytes from global memory straight into LDS at `lds` + 16 *
+  // lane. The LDS address is a number, so the compiler ties no LDS read to
+  // these loads: the waits are the ones written in run().
+  __device__ static inline void load_lds(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
+                                         unsigned lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (__attribute__((address_space(3))) void*)(uintptr_t)lds, 16, voff, soff, 0, 0);
+  }
+  __device__ static inline __amdgpu_buffer_rsrc_t make_rsrc(const char* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, bytes, 0x00020000);
+  }
+
+  // D's tile at (r0, c0), operands 16-byte aligned with ld a multiple of 16
+  // (at most kTileMaxLd) and kbytes a multiple of 16. Rows past an operand's
+  // last are read as its last (their results are not for storing); chunks past
+  // kbytes get an offset past the buffer's end and read as zero.
+  __device__ inline void run(const TileOperand& R, const TileOperand& C, int64_t kbytes,
+                             const PlanePairs& pairs, int64_t r0, int64_t c0, char* lds) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rows = R.rows - r0 < BR ? (int)(R.rows - r0) : BR;
+    const int cols = C.rows - c0 < BC ? (int)(C.rows - c0) : BC;
+    const int ldr = (int)R.ld, ldc = (int)C.ld;
+    const char* pr = R.p + r0 * R.ld;
+    const char* pc = C.p + c0 * C.ld;
+    const int rbytes = (rows - 1) * ldr + (int)kbytes, cbytes = (cols - 1) * ldc + (int)kbytes;
+    const int row8 = lane >> 3;
+    const int chunk = chunk_at((wave & 1) * 8 + row8, lane & 7);
+    int vr[LR], vc[LC];
+#pragma unroll
+    for (int j = 0; j < LR; ++j) {
+      const int r = (j * kWaves + wave) * 8 + row8;
+      vr[j] = (r < rows ? r : rows - 1) * ldr + chunk * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < LC; ++j) {
+      const int r = (j * kWaves + wave) * 8 + row8;
+      vc[j] = (r < cols ? r : cols - 1) * ldc + chunk * 16;
+    }
+    const unsigned lbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+
+    const int ksteps = (int)((kbytes + kStepBytes - 1) / kStepBytes);
+    const int total = ksteps * pairs.n;
+    const bool past = chunk * 16 + (int64_t)(ksteps - 1) * kStepBytes >= kbytes;
+    int lk = 0, lp = 0, lbuf = 0;  // the next step to load: k step, pair, buffer
+    __amdgpu_buffer_rsrc_t rr = make_rsrc(pr + pairs.r[0] * R.plane, rbytes);
+    __amdgpu_buffer_rsrc_t rc = make_rsrc(pc + pairs.c[0] * C.plane, cbytes);
+    auto load = [&]() {
+      const int soff = lk * kStepBytes;
+      const unsigned lb = lbase + lbuf * kStage + wave * 1024;
+      const bool cut = past && lk == ksteps - 1;
+#pragma unroll
+      for (int j = 0; j < LR; ++j)
+        load_lds(rr, cut ? (int)0x80000000 : vr[j], soff, lb + j * kWaves * 1024);
+#pragma unroll
+      for (int j = 0; j < LC; ++j)
+        load_lds(rc, cut ? (int)0x80000000 : vc[j], soff,
+                 lb + BR * kStepBytes + j * kWaves * 1024);
+      lbuf = lbuf + 1 == STAGES ? 0 : lbuf + 1;
+      if (++lk == ksteps && lp + 1 < pairs.n) {
+        lk = 0;
+        ++lp;
+        rr = make_rsrc(pr + pairs.r[lp] * R.plane, rbytes);
+        rc = make_rsrc(pc + pairs.c[lp] * C.plane, cbytes);
+      }
+    };
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+      if (s < total) load();
+    int buf = 0;
+    for (int s = 0; s < total; ++s) {
+      // this step's bytes have landed (the steps after it may be in flight),
+      // and every wave is done with the buffer that the next load fills
+      if (s + STAGES - 1 <= total)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((STAGES - 2) * (LR + LC))
+                     : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (s + STAGES - 1 < total) load();
+      compute(lds + buf * kStage);
+      buf = buf + 1 == STAGES ? 0 : buf + 1;
+    }
+  }
+
+  // The same for operands of any alignment, stride and k (M::kElem-sized
+  // elements): a step is read to registers while the one before is computed,
+  // partial chunks element by element, and then written to LDS.
+  __device__ static inline v4i load_any(const char* row, int64_t k, int64_t kbytes) {
+    v4i v = {0, 0, 0, 0};
+    if (k + 16 <= kbytes) {
+      __builtin_memcpy(&v, row + k, 16);
+    } else {
+      unsigned w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 16; e += M::kElem)
+        if (k + e < kbytes) {
+          unsigned x;
+          if (M::kElem == 1)
+            x = *(const unsigned char*)(row + k + e);
+          else
+            x = *(const unsigned short*)(row + k + e);
+          w[e / 4] |= x << (8 * (e % 4));
+        }
+      v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    }
+    return v;
+  }
+
+  __device__ inline void run_any(const TileOperand& R, const TileOperand& C, int64_t kbytes,
+                                 int64_t r0, int64_t c0, char* lds) {
+    const int tid = threadIdx.x;
+    const int64_t rows = R.rows - r0 < BR ? R.rows - r0 : BR;
+    const int64_t cols = C.rows - c0 < BC ? C.rows - c0 : BC;
+    constexpr int NR = BR * 8 / kThreads, NC = BC * 8 / kThreads;
+    v4i vr[NR], vc[NC];
+    auto gload = [&](int64_t k) {
+#pragma unroll
+      for (int u = 0; u < NR; ++u) {
+        const int e = u * kThreads + tid, r = e >> 3;
+        vr[u] = load_any(R.p + (r0 + (r < rows ? r : rows - 1)) * R.ld, k + (e & 7) * 16, kbytes);
+      }
+#pragma unroll
+      for (int u = 0; u < NC; ++u) {
+        const int e = u * kThreads + tid, r = e >> 3;
+        vc[u] = load_any(C.p + (c0 + (r < cols ? r : cols - 1)) * C.ld, k + (e & 7) * 16, kbytes);
+      }
+    };
+    auto sstore = [&](char* b) {
+#pragma unroll
+      for (int u = 0; u < NR; ++u) {
+        const int e = u * kThreads + tid, r = e >> 3;
+        *(v4i*)(b + r * kStepBytes + chunk_at(r, e & 7) * 16) = vr[u];
+      }
+#pragma unroll
+      for (int u = 0; u < NC; ++u) {
+        const int e = u * kThreads + tid, r = e >> 3;
+        *(v4i*)(b + (BR + r) * kStepBytes + chunk_at(r, e & 7) * 16) = vc[u];
+      }
+    };
+    const int ksteps = (int)((kbytes + kStepBytes - 1) / kStepBytes);
+    if (ksteps > 0) {
+      gload(0);
+      sstore(lds);
+    }
+    __syncthreads();
+    for (int s = 0; s < ksteps; ++s) {
+      if (s + 1 < ksteps) gload((int64_t)(s + 1) * kStepBytes);
+      compute(lds + (s & 1) * kStage);
+      if (s + 1 < ksteps) sstore(lds + ((s + 1) & 1) * kStage);
+      __syncthreads();
+    }
+  }
+};
+
+// ---- element types ----------------------------------------------------------
+struct BF16 {
+  unsigned short v;
+};
+struct F16 {
+  _Float16 v;
+};
+__device__ inline float to_f32(float x) { return x; }
+__device__ inline float to_f32(BF16 x) { return __uint_as_float((unsigned)x.v << 16); }
+__device__ inline float to_f32(F16 x) { return (float)x.v; }
+
+// Round to nearest even; a NaN stays a NaN.
+template <typename T> __device__ inline T from_f32(float x);
+template <> __device__ inline float from_f32<float>(float x) { return x; }
+template <> __device__ inline BF16 from_f32<BF16>(float x) {
+  const __bf16 b = (__bf16)x;
+  return BF16{__builtin_bit_cast(unsigned short, b)};
+}
+template <> __device__ inline F16 from_f32<F16>(float x) { return F16{(_Float16)x}; }
+
+}  // namespace bk

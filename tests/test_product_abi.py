@@ -1,0 +1,98 @@
+"""Refusals of the 8-bit product, through the C ABI and the binding (no GPU:
+every call here fails its checks or has nothing to do)."""
+import ctypes
+
+import pytest
+import torch
+
+import kronecker_factored_gptq_amd as bk
+
+
+def at(k):
+    """An address that is never dereferenced."""
+    return ctypes.c_void_p(0x100000 * k)
+
+
+def _quantize(**kw):
+    a = dict(t=bk.F32, T=3, n=4, X=at(1), ldx=4, c=None, q=at(2), ldq=4, s=at(3))
+    a.update(kw)
+    return bk.lib().bakron_quantize_tokens(a["t"], a["T"], a["n"], a["X"], a["ldx"], a["c"], a["q"], a["ldq"],
+                                           a["s"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(t=bk.F64), dict(t=9), dict(t=-1), dict(T=-1), dict(n=-1), dict(T=1 << 31), dict(X=None), dict(q=None),
+    dict(s=None), dict(ldx=3), dict(ldq=3), dict(ldx=1 << 62), dict(X=ctypes.c_void_p(0x100002)),
+    dict(s=ctypes.c_void_p(0x300002)), dict(c=ctypes.c_void_p(0x400001)),
+    # outputs over inputs, or over each other
+    dict(q=at(1)), dict(s=at(1)), dict(s=at(2)), dict(c=at(3)),
+])
+def test_quantize_tokens_rejects_bad_arguments(bad):
+    assert _quantize(**bad) == bk.EINVAL
+
+
+def test_quantize_tokens_empty():
+    assert _quantize(T=0, X=None, q=None, s=None) == bk.OK
+
+
+def _matmul(**kw):
+    a = dict(t=bk.F32, T=3, m=5, n=4, X=at(1), ldx=4, sx=at(2), V=at(3), ldv=4, sv=at(4), Y=at(5), ldy=5)
+    a.update(kw)
+    return bk.lib().bakron_matmul_int8(a["t"], a["T"], a["m"], a["n"], a["X"], a["ldx"], a["sx"], a["V"], a["ldv"],
+                                       a["sv"], a["Y"], a["ldy"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(t=bk.F64), dict(t=4), dict(T=-1), dict(m=-1), dict(n=-1), dict(T=1 << 31), dict(m=1 << 31),
+    dict(n=131072, ldx=131072, ldv=131072), dict(X=None), dict(V=None), dict(Y=None), dict(sx=None),
+    dict(ldx=3), dict(ldv=3), dict(ldy=4), dict(ldv=1 << 62), dict(Y=ctypes.c_void_p(0x500002)),
+    dict(sx=ctypes.c_void_p(0x200001)), dict(sv=ctypes.c_void_p(0x400002)),
+    dict(t=bk.BF16, Y=ctypes.c_void_p(0x500001)),
+    # more tiles than a launch holds
+    dict(T=(1 << 31) - 1, m=(1 << 31) - 1, ldy=(1 << 31) - 1),
+    # the output over an input
+    dict(Y=at(1)), dict(Y=at(2)), dict(Y=at(3)), dict(Y=at(4)),
+])
+def test_matmul_int8_rejects_bad_arguments(bad):
+    assert _matmul(**bad) == bk.EINVAL
+
+
+def test_matmul_int8_empty():
+    assert _matmul(T=0, X=None, sx=None, Y=None) == bk.OK
+    assert _matmul(m=0, V=None, sv=None, Y=None) == bk.OK
+
+
+def test_binding_refuses_cpu_tensors():
+    x = torch.zeros(2, 4)
+    q = torch.zeros(2, 4, dtype=torch.int8)
+    with pytest.raises(ValueError, match="GPU"):
+        bk.quantize_tokens(x)
+    with pytest.raises(ValueError, match="GPU"):
+        bk.matmul_int8(q, x[:, 0].contiguous(), q)
+
+
+@pytest.fixture
+def as_if_gpu(monkeypatch):
+    """The binding's own checks, on CPU tensors (nothing is launched: each call
+    raises before it reaches the library)."""
+    monkeypatch.setattr(bk, "_check_device", lambda *ts: torch.device("cpu"))
+
+
+def test_binding_checks(as_if_gpu):
+    x, q = torch.zeros(3, 4), torch.zeros(3, 4, dtype=torch.int8)
+    s = torch.ones(3)
+    for bad in (lambda: bk.quantize_tokens(x.double()), lambda: bk.quantize_tokens(x, torch.ones(4).double()),
+                lambda: bk.matmul_int8(x, s, q), lambda: bk.matmul_int8(q, s, q.to(torch.int32)),
+                lambda: bk.matmul_int8(q, s.double(), q), lambda: bk.matmul_int8(q, s, q, s.half()),
+                lambda: bk.matmul_int8(q, s, q, out_dtype=torch.float64)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: bk.quantize_tokens(x[0]), lambda: bk.quantize_tokens(x.t()),
+                lambda: bk.quantize_tokens(x, torch.ones(3)), lambda: bk.quantize_tokens(x, torch.ones(8)[::2]),
+                lambda: bk.quantize_tokens(torch.zeros(1, 4).expand(3, 4)),
+                lambda: bk.matmul_int8(q.t(), s, q), lambda: bk.matmul_int8(q, s[:2], q),
+                lambda: bk.matmul_int8(q, s, q[:, :3]), lambda: bk.matmul_int8(q, s, q, torch.ones(4)),
+                lambda: bk.matmul_int8(q, s, q, out=torch.zeros(3, 4)),
+                lambda: bk.matmul_int8(q, s, q, out=torch.zeros(3, 6)[:, ::2])):
+        with pytest.raises(ValueError):
+            bad()
