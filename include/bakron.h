@@ -481,6 +481,28 @@ int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n,
                        const int8_t *Vq, int64_t ldv, const float *sv,
                        void *Y, int64_t ldy, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Input gradient of the 8-bit product, the tokens' rounding passed straight
+ * through (output-side samples of earlier layers come back through layers
+ * that are codes already):
+ *   dX[t][j] = channel[j] * sum_i G[t][i] * sv[i] * Vq[i][j].
+ *
+ *   gtype  the type of G (T x m, ldg >= m) and of dX (T x n, ldx >= n): F32,
+ *          BF16 or F16. Vq m x n int8 (ldv >= n); sv float32 length m and
+ *          channel float32 length n, each nullable (all 1).
+ * G[t][i] sv[i] is rounded to float32 and then kept with 8 bits for BF16 (an
+ * error of 2^-9 to 2^-8 a term, as the output's own), 16 for F16, all 24 for
+ * F32; products are exact, sums float32, one rounding to gtype.
+ * dX must not overlap the inputs (BAKRON_EINVAL). m, n <= 2^20. Asynchronous,
+ * deterministic.
+ * ------------------------------------------------------------------------ */
+size_t bakron_matmul_int8_grad_workspace_bytes(int gtype, int64_t T, int64_t m, int64_t n);
+int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n,
+                            const void *G, int64_t ldg, const int8_t *Vq, int64_t ldv,
+                            const float *sv, const float *channel,
+                            void *dX, int64_t ldx,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,7 +21,8 @@ __all__ = ["F32", "F64", "BF16", "F16", "SCALE_NONE", "SCALE_ROW", "SCALE_COL", 
            "factor_batched",
            "solve", "solve_antidiag", "solve_noalloc", "factor_blockdiag", "solve_blockdiag",
            "loss_blockdiag", "solve_batched", "loss", "loss_batched", "row_scales", "row_scales_mse", "gram",
-           "sample_sqnorms", "kfac_factors", "shampoo_factors", "quantize_tokens", "matmul_int8", "solve_schedule", "tile_size", "workspace_bytes"]
+           "sample_sqnorms", "kfac_factors", "shampoo_factors", "quantize_tokens", "matmul_int8",
+           "matmul_int8_grad", "solve_schedule", "tile_size", "workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libbakron.so")
@@ -138,6 +139,11 @@ def lib() -> ctypes.CDLL:
     L.bakron_matmul_int8.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
                                      _i64, _vp]
     L.bakron_matmul_int8.restype = _int
+    L.bakron_matmul_int8_grad_workspace_bytes.argtypes = [_int, _i64, _i64, _i64]
+    L.bakron_matmul_int8_grad_workspace_bytes.restype = _sz
+    L.bakron_matmul_int8_grad.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                          _vp, _i64, _vp, _sz, _vp]
+    L.bakron_matmul_int8_grad.restype = _int
     _lib = L
     return L
 
@@ -840,6 +846,38 @@ def matmul_int8(Xq: torch.Tensor, sx: torch.Tensor, Vq: torch.Tensor,
                                       _p(out), _ld(out, "out"), _stream(dev))
     if rc != OK:
         raise BakronError(rc, "bakron_matmul_int8")
+    return out
+
+
+def matmul_int8_grad(G: torch.Tensor, Vq: torch.Tensor, sv: Optional[torch.Tensor] = None,
+                     channel_scales: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The input gradient of a layer held as codes (bakron_matmul_int8_grad):
+    dX[t][j] = channel_scales[j] sum_i G[t][i] sv[i] Vq[i][j], with the rounding
+    of the tokens passed straight through. G is T x m in float32, bfloat16 or
+    float16 and dX, T x n, of its type; sv (length m) and channel_scales
+    (length n) are float32, None for 1. Asynchronous."""
+    dev = _check_device(G, Vq, sv, channel_scales, workspace, out)
+    code = _ft(G.dtype, "G")
+    ldg, ldv = _matrix(G, "G"), _matrix(Vq, "Vq", torch.int8)
+    (T, m), n = G.shape, Vq.size(1)
+    if Vq.size(0) != m:
+        raise ValueError(f"G must have a column for each row of Vq, got {m} and {Vq.size(0)}")
+    _vector(sv, m, "sv")
+    _vector(channel_scales, n, "channel_scales")
+    if out is None:
+        out = torch.empty((T, n), dtype=G.dtype, device=dev)
+    else:
+        _check_out(out, (T, n), G.dtype, "out")
+    L = lib()
+    ws = _workspace(L.bakron_matmul_int8_grad_workspace_bytes(code, T, m, n), dev, workspace)
+    with torch.cuda.device(dev):
+        rc = L.bakron_matmul_int8_grad(code, T, m, n, _p(G), ldg, _p(Vq), ldv, _p(sv),
+                                       _p(channel_scales), _p(out), _ld(out, "out"), _p(ws),
+                                       ws.numel() * ws.element_size(), _stream(dev))
+    if rc != OK:
+        raise BakronError(rc, "bakron_matmul_int8_grad")
     return out
 
 

@@ -40,6 +40,17 @@ inline bool tiles_ok(int64_t a, int64_t b) {
   return ((a + 127) / 128) * ((b + 127) / 128) <= INT_MAX;
 }
 
+constexpr size_t kAlign = 256;
+
+// Sizes of the input gradient: rows of planes short enough for the tile
+// product's 32-bit offsets, and a grid of 64 x 64 transposes.
+constexpr int64_t kMaxPlaneCols = (int64_t)1 << 20;
+inline int grad_planes(int t) { return t == BAKRON_F32 ? 3 : t == BAKRON_BF16 ? 1 : 2; }
+inline bool grad_sizes_ok(int t, int64_t T, int64_t m, int64_t n) {
+  return type_ok(t) && T >= 0 && m >= 0 && n >= 0 && T <= INT_MAX && m <= kMaxPlaneCols &&
+         n <= kMaxPlaneCols && T * (m + 64) <= ((int64_t)1 << 41);
+}
+
 }  // namespace
 
 extern "C" {
@@ -83,6 +94,39 @@ int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n, const int8_t*
   if (ytype == BAKRON_BF16)
     return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (BF16*)Y, ldy, s));
   return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (F16*)Y, ldy, s));
+}
+
+size_t bakron_matmul_int8_grad_workspace_bytes(int gtype, int64_t T, int64_t m, int64_t n) {
+  if (!grad_sizes_ok(gtype, T, m, n)) return 0;
+  return matmul_int8_grad_bytes(grad_planes(gtype), T, m, n) + kAlign;
+}
+
+int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n, const void* G, int64_t ldg,
+                            const int8_t* Vq, int64_t ldv, const float* sv, const float* channel,
+                            void* dX, int64_t ldx, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (!grad_sizes_ok(gtype, T, m, n)) return BAKRON_EINVAL;
+  if (T == 0 || n == 0) return BAKRON_OK;
+  const size_t es = type_size(gtype);
+  if (!tiles_ok(T, n) || !matrix_ok(G, T, m, ldg, es) || !matrix_ok(Vq, m, n, ldv, 1) ||
+      !matrix_ok(dX, T, n, ldx, es))
+    return BAKRON_EINVAL;
+  if ((uintptr_t)sv % 4 || (uintptr_t)channel % 4) return BAKRON_EINVAL;
+  if (!workspace || (uintptr_t)workspace % kAlign ||
+      workspace_bytes < matmul_int8_grad_bytes(grad_planes(gtype), T, m, n))
+    return BAKRON_EINVAL;
+  if (overlap(dX, T, n, ldx, es, G, T, m, ldg, es) || overlap(dX, T, n, ldx, es, Vq, m, n, ldv, 1) ||
+      overlap(dX, T, n, ldx, es, sv, 1, m, m, 4) || overlap(dX, T, n, ldx, es, channel, 1, n, n, 4))
+    return BAKRON_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (gtype == BAKRON_F32)
+    return status(launch_matmul_int8_grad(T, m, n, (const float*)G, ldg, Vq, ldv, sv, channel,
+                                          (float*)dX, ldx, workspace, s));
+  if (gtype == BAKRON_BF16)
+    return status(launch_matmul_int8_grad(T, m, n, (const BF16*)G, ldg, Vq, ldv, sv, channel,
+                                          (BF16*)dX, ldx, workspace, s));
+  return status(launch_matmul_int8_grad(T, m, n, (const F16*)G, ldg, Vq, ldv, sv, channel, (F16*)dX,
+                                        ldx, workspace, s));
 }
 
 }  // extern "C"

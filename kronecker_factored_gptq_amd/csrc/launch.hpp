@@ -285,4 +285,38 @@ hipError_t launch_matmul_int8(int64_t T, int64_t m, int64_t n, const int8_t* Xq,
                               const float* sx, const int8_t* Vq, int64_t ldv, const float* sv, O* Y,
                               int64_t ldy, hipStream_t s);
 
+// ---- operands and products of 16-bit planes (plane_kernels.hip) ------------
+// A matrix held as planes for the 16-bit matrix instructions (tile_product.hpp):
+// word k of row r of plane p at w + p * plane + r * ld (bytes), the columns
+// past `cols` up to a multiple of kPlaneCols zero.
+constexpr int64_t kPlaneCols = 64;  // 128 bytes: every row starts on a line
+inline int64_t plane_ld(int64_t cols) { return (cols + kPlaneCols - 1) / kPlaneCols * kPlaneCols * 2; }
+struct Planes {
+  char* w;
+  int64_t ld, plane;
+};
+// out = planes (KIND, a Split) of X (rows x cols) times col_scale (nullable).
+template <typename X, int KIND>
+hipError_t launch_planes(int64_t rows, int64_t cols, const X* x, int64_t ldx,
+                         const float* col_scale, Planes out, hipStream_t s);
+// out = planes of the transpose of X (rows x cols): cols x rows.
+template <typename X, int KIND>
+hipError_t launch_planes_t(int64_t rows, int64_t cols, const X* x, int64_t ldx, Planes out,
+                           hipStream_t s);
+// Y[c][r] = row_scale[r] * sum over the plane pairs of R[r][k] C[c][k], k < K:
+// R rows r < M, C rows c < N (row_scale nullable). F16: the planes' type.
+template <typename O, bool F16P>
+hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C, int npairs,
+                                const unsigned char* pr, const unsigned char* pc,
+                                const float* row_scale, O* Y, int64_t ldy, hipStream_t s);
+
+// dX (T x n) = channel (.) ((G sv) Vq); sv and channel nullable. ws holds
+// matmul_int8_grad_bytes(planes of G's type: float 3, BF16 1, F16 2).
+size_t matmul_int8_grad_bytes(int planes, int64_t T, int64_t m, int64_t n);
+template <typename G>
+hipError_t launch_matmul_int8_grad(int64_t T, int64_t m, int64_t n, const G* g, int64_t ldg,
+                                   const int8_t* Vq, int64_t ldv, const float* sv,
+                                   const float* channel, G* dX, int64_t ldx, void* ws,
+                                   hipStream_t s);
+
 }  // namespace bk

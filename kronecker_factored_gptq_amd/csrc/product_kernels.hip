@@ -6,59 +6,6 @@
 
 namespace bk {
 
-namespace {
-
-// Four consecutive outputs as one store.
-template <typename O> struct Vec4;
-template <> struct Vec4<float> {
-  typedef float type __attribute__((ext_vector_type(4)));
-};
-template <> struct Vec4<BF16> {
-  typedef unsigned short type __attribute__((ext_vector_type(4)));
-};
-template <> struct Vec4<F16> {
-  typedef unsigned short type __attribute__((ext_vector_type(4)));
-};
-// whether every group of four columns of Y starts at a multiple of its size
-template <typename O>
-inline bool vec4_ok(const O* y, int64_t ld) {
-  return (uintptr_t)y % (4 * sizeof(O)) == 0 && ld % 4 == 0;
-}
-
-// A tile's results to Y[c][r .. r + 3] (row stride ldy): f(value, i, j, e) of
-// each accumulator element, rounded to O. `vec`: vec4_ok.
-template <class TP, typename O, typename F>
-__device__ inline void store_tile(const TP& tp, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
-                                  O* __restrict__ Y, int64_t ldy, bool vec, F f) {
-  const int lane = threadIdx.x & 63;
-  const int64_t rb = r0 + tp.wave_r() + 4 * (lane >> 4), cb = c0 + tp.wave_c() + (lane & 15);
-  if (vec && r0 + tp.wave_r() + TP::FR * 16 <= rows) {
-#pragma unroll
-    for (int j = 0; j < TP::FC; ++j) {
-      if (cb + j * 16 >= cols) continue;
-      O* p = Y + (cb + j * 16) * ldy + rb;
-#pragma unroll
-      for (int i = 0; i < TP::FR; ++i) {
-        O t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = from_f32<O>(f(tp.acc[i][j][e], i, j, e));
-        *(typename Vec4<O>::type*)(p + i * 16) = __builtin_bit_cast(typename Vec4<O>::type, t);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < TP::FC; ++j)
-#pragma unroll
-      for (int i = 0; i < TP::FR; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (cb + j * 16 < cols && rb + i * 16 + e < rows)
-            Y[(cb + j * 16) * ldy + rb + i * 16 + e] = from_f32<O>(f(tp.acc[i][j][e], i, j, e));
-  }
-}
-
-}  // namespace
-
 // ---------------------------------------------------------------------------
 // Tokens to int8: x = X[t][j] * c[j] in float32, s = max_j |x| / 127 (1 for an
 // all-zero token), q = clamp(rint(x / s), -127, 127), the division correctly

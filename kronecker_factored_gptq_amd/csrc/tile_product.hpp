@@ -318,4 +318,89 @@ template <> __device__ inline BF16 from_f32<BF16>(float x) {
 }
 template <> __device__ inline F16 from_f32<F16>(float x) { return F16{(_Float16)x}; }
 
+// Four consecutive outputs as one store.
+template <typename O> struct Vec4;
+template <> struct Vec4<float> {
+  typedef float type __attribute__((ext_vector_type(4)));
+};
+template <> struct Vec4<BF16> {
+  typedef unsigned short type __attribute__((ext_vector_type(4)));
+};
+template <> struct Vec4<F16> {
+  typedef unsigned short type __attribute__((ext_vector_type(4)));
+};
+// whether every group of four columns of Y starts at a multiple of its size
+template <typename O>
+inline bool vec4_ok(const O* y, int64_t ld) {
+  return (uintptr_t)y % (4 * sizeof(O)) == 0 && ld % 4 == 0;
+}
+
+// A tile's results to Y[c][r .. r + 3] (row stride ldy): f(value, i, j, e) of
+// each accumulator element, rounded to O. `vec`: vec4_ok.
+template <class TP, typename O, typename F>
+__device__ inline void store_tile(const TP& tp, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
+                                  O* __restrict__ Y, int64_t ldy, bool vec, F f) {
+  const int lane = threadIdx.x & 63;
+  const int64_t rb = r0 + tp.wave_r() + 4 * (lane >> 4), cb = c0 + tp.wave_c() + (lane & 15);
+  if (vec && r0 + tp.wave_r() + TP::FR * 16 <= rows) {
+#pragma unroll
+    for (int j = 0; j < TP::FC; ++j) {
+      if (cb + j * 16 >= cols) continue;
+      O* p = Y + (cb + j * 16) * ldy + rb;
+#pragma unroll
+      for (int i = 0; i < TP::FR; ++i) {
+        O t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = from_f32<O>(f(tp.acc[i][j][e], i, j, e));
+        *(typename Vec4<O>::type*)(p + i * 16) = __builtin_bit_cast(typename Vec4<O>::type, t);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < TP::FC; ++j)
+#pragma unroll
+      for (int i = 0; i < TP::FR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (cb + j * 16 < cols && rb + i * 16 + e < rows)
+            Y[(cb + j * 16) * ldy + rb + i * 16 + e] = from_f32<O>(f(tp.acc[i][j][e], i, j, e));
+  }
+}
+
+// ---- planes -----------------------------------------------------------------
+// How a matrix is held for the 16-bit instructions: a float32 value as one, two
+// or three bfloat16 planes, or as float16. Two planes lose at most 2^-16 of the
+// value, three keep all 24 bits.
+enum Split { kBF16x1, kBF16x2, kBF16x3, kF16x1 };
+constexpr int kPlanes[] = {1, 2, 3, 1};
+
+// The planes' 16-bit words of x. The first ones are truncated, so that each
+// rest is exact and no finite x overflows; an infinity or a NaN stands in the
+// first plane alone.
+template <int KIND>
+__device__ inline void split16(float x, unsigned short* w) {
+  if (KIND == kF16x1) {
+    w[0] = __builtin_bit_cast(unsigned short, (_Float16)x);
+  } else if (KIND == kBF16x1) {
+    w[0] = from_f32<BF16>(x).v;
+  } else {
+    const unsigned u = __float_as_uint(x);
+    if ((u & 0x7f800000u) == 0x7f800000u) {
+      w[0] = from_f32<BF16>(x).v;
+      w[1] = 0;
+      if (KIND == kBF16x3) w[2] = 0;
+      return;
+    }
+    w[0] = (unsigned short)(u >> 16);
+    const float r = x - __uint_as_float(u & 0xffff0000u);
+    if (KIND == kBF16x2) {
+      w[1] = from_f32<BF16>(r).v;
+    } else {
+      const unsigned v = __float_as_uint(r);
+      w[1] = (unsigned short)(v >> 16);
+      w[2] = from_f32<BF16>(r - __uint_as_float(v & 0xffff0000u)).v;
+    }
+  }
+}
+
 }  // namespace bk

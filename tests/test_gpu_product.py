@@ -1,12 +1,16 @@
-"""The 8-bit product (bakron_quantize_tokens, bakron_matmul_int8) against plain
-64-bit arithmetic.
+"""The 8-bit product (bakron_quantize_tokens, bakron_matmul_int8) and its input
+gradient (bakron_matmul_int8_grad) against plain 64-bit arithmetic.
 
 Tolerances, counted in the roundings of the definitions. Quantisation: the
 scale is one float32 division, the codes are whole numbers and equal. Product:
 the int32 sum is exact; its conversion to float32 and the two scale products
 round once each, and the output once, so |Y - Y64| <= (3 eps32 (1 + 2 eps32) +
 eps_out) |Y64| with eps half a step (2^-24; bf16 2^-8, fp16 2^-11 relative to
-the value), plus the smallest subnormal of a float16 output."""
+the value), plus the smallest subnormal of a float16 output. Gradient: with S
+the sum of the terms' absolute values, each term carries the rounding of G sv
+(2^-24) and what its planes drop (2^-8 bf16, 2^-16 fp16, nothing for float32,
+whose 24 bits are all kept), the at most 3 m float32 additions 2^-24 of S each,
+the channel factor 2^-24 and the output half a step of its type."""
 import numpy as np
 import pytest
 import torch
@@ -162,3 +166,104 @@ def test_matmul_int8_empty(gpu_lib):
     assert bk.matmul_int8(torch.empty(3, 8, **e), torch.ones(3, device="cuda"), torch.empty(0, 8, **e)).shape == (3, 0)
     Y = bk.matmul_int8(torch.empty(3, 0, **e), torch.ones(3, device="cuda"), torch.empty(5, 0, **e))
     assert Y.shape == (3, 5) and (Y == 0).all()
+
+
+KEPT = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -16}
+
+
+def check_grad(bk, G, V, sv, c, t, out=None):
+    D = bk.matmul_int8_grad(G.cuda(), V.cuda(), None if sv is None else sv.cuda(),
+                            None if c is None else c.cuda(), out=out)
+    m = G.shape[1]
+    g = G.double() if sv is None else G.double() * sv.double()
+    f = 1.0 if c is None else c.double()
+    ref, S = (g @ V.double()) * f, (g.abs() @ V.double().abs()) * f
+    assert D.dtype == TYPES[t]
+    tol = S * (KEPT[t] + (3 * m + 4) * E32) * (1 + 2.0 ** -6) + ref.abs() * half_step(TYPES[t])
+    tol += {"f32": 0.0, "bf16": 0.0, "f16": 2.0 ** -25}[t] + 1e-40
+    got = D.cpu().double()
+    # float16 ends at 65504 = 2^16 - 2^5 and the rounding of anything from 2^16 - 2^4 on is infinity: a
+    # result may be infinite where its value, moved by its tolerance, reaches that (float32 and bfloat16
+    # end at 2^128, out of these inputs' reach)
+    over = torch.isinf(got) & (got.sign() == ref.sign()) & (ref.abs() + tol >= 65520) & (t == "f16")
+    err = torch.where(over, 0.0, (got - ref).abs())
+    assert (err <= tol).all(), (err / tol).max()
+    return D
+
+
+@pytest.mark.parametrize("T,m,n", [(1, 1, 1), (1, 4096, 300), (3, 17, 65), (33, 200, 1000), (129, 64, 130),
+                                   (300, 1003, 511), (1, 70, 4096), (2600, 300, 2100)])
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_matmul_int8_grad(gpu_lib, T, m, n, t):
+    g = torch.Generator().manual_seed(T + 3 * m + 7 * n)
+    G = torch.randn(T, m, generator=g).to(TYPES[t])
+    sv, c = torch.exp(torch.randn(m, generator=g)), torch.exp(torch.randn(n, generator=g))
+    V = int8(m, n, g)
+    check_grad(gpu_lib, G, V, sv, c, t)
+    check_grad(gpu_lib, G, V, None, None, t)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_matmul_int8_grad_strides(gpu_lib, t):
+    """Slices of wider buffers, unaligned; a strided output whose other columns
+    stay; gradients of very different sizes in one row."""
+    g = torch.Generator().manual_seed(7)
+    base = torch.randn(40, 101, generator=g) * 10.0 ** torch.randint(-3, 3, (40, 101), generator=g)
+    G, V = base.to(TYPES[t])[:, 3:80], int8(77, 133, g)[:, 1:121]
+    sv = torch.rand(77, generator=g) + 0.5
+    wide = torch.full((40, 131), 9.0, dtype=TYPES[t], device="cuda")
+    check_grad(gpu_lib, G, V, sv, None, t, out=wide[:, 5:125])
+    assert (wide[:, :5] == 9).all() and (wide[:, 125:] == 9).all()
+
+
+def test_matmul_int8_grad_edge_values(gpu_lib):
+    """No rows, no outputs, no inputs; infinities and NaN stay in their rows."""
+    bk, e = gpu_lib, dict(dtype=torch.int8, device="cuda")
+    assert bk.matmul_int8_grad(torch.empty(0, 4, device="cuda"), torch.empty(4, 6, **e)).shape == (0, 6)
+    assert bk.matmul_int8_grad(torch.empty(3, 4, device="cuda"), torch.empty(4, 0, **e)).shape == (3, 0)
+    D = bk.matmul_int8_grad(torch.empty(3, 0, device="cuda"), torch.empty(0, 6, **e))
+    assert D.shape == (3, 6) and (D == 0).all()
+    for t in TYPES.values():
+        G = torch.ones(4, 9, device="cuda", dtype=t)
+        G[1, 3], G[2, 8] = float("inf"), float("nan")
+        D = bk.matmul_int8_grad(G, torch.ones(9, 20, **e))
+        assert (D[1] == float("inf")).all() and torch.isnan(D[2]).all() and (D[[0, 3]] == 9).all()
+    # the largest floats are kept, not rounded up to infinity
+    G = torch.full((1, 1), 3.4e38, device="cuda")
+    assert bk.matmul_int8_grad(G, torch.ones(1, 1, **e)).item() == G.item()
+
+
+def test_grad_is_the_products_derivative(gpu_lib):
+    """Differences of the layer's outputs: where the tokens are whole numbers of
+    steps the rounding is exact, and one step h of x[t][j] moves sum(G Y) by
+    h dX[t][j]."""
+    bk = gpu_lib
+    g = torch.Generator().manual_seed(11)
+    T, m, n = 3, 50, 40
+    X = torch.randint(-100, 101, (T, n), generator=g).float() / 64
+    X[:, 0] = 127.0 / 64  # fixes every token's scale at 1/64
+    V, sv = int8(m, n, g, -8, 7), torch.rand(m, generator=g) + 0.5
+    c = 2.0 ** torch.randint(-1, 2, (n,), generator=g).float()
+    c[0] = 1.0
+    X[:, 1:] = X[:, 1:] / 2  # stays below the first column under the channel factors
+    X = torch.round(X * 64 * c) / 64 / c
+    G = torch.randn(T, m, generator=g)
+
+    def value(x):
+        q, s = bk.quantize_tokens(x.cuda(), c.cuda())
+        assert (s == 1.0 / 64).all()
+        return (G.double() * bk.matmul_int8(q, s, V.cuda(), sv.cuda()).cpu().double()).sum()
+
+    D = bk.matmul_int8_grad(G.cuda(), V.cuda(), sv.cuda(), c.cuda()).cpu().double()
+    for t, j in ((0, 1), (1, 17), (2, 39), (0, 20)):
+        h = 1.0 / 64 / float(c[j])
+        up, down = X.clone(), X.clone()
+        up[t, j] += h
+        down[t, j] -= h
+        slope = (value(up) - value(down)) / (2 * h)
+        # each Y is off by 3 roundings of 2^-24 of itself, the slope by their sum over 2 h
+        size = 2 * 3 * E32 * (G[t].abs().double() * (V.double().abs() @ (X[t].double() * c.double()).abs())
+                              * sv.double()).sum()
+        scale = size * 1.1 / h + 1e-6 * D[t, j].abs() + 200 * E32 * (G[t].abs().double() * sv.double()
+                                                                      * V[:, j].abs().double()).sum() * float(c[j])
+        assert abs(slope - D[t, j]) <= scale, (t, j)

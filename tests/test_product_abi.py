@@ -62,6 +62,34 @@ def test_matmul_int8_empty():
     assert _matmul(m=0, V=None, sv=None, Y=None) == bk.OK
 
 
+def _grad(**kw):
+    a = dict(t=bk.F32, T=3, m=5, n=4, G=at(1), ldg=5, V=at(2), ldv=4, sv=at(3), c=at(4), D=at(5), ldx=4, ws=at(6),
+             wsb=1 << 40)
+    a.update(kw)
+    return bk.lib().bakron_matmul_int8_grad(a["t"], a["T"], a["m"], a["n"], a["G"], a["ldg"], a["V"], a["ldv"],
+                                            a["sv"], a["c"], a["D"], a["ldx"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(t=bk.F64), dict(t=4), dict(T=-1), dict(m=-1), dict(n=-1), dict(T=1 << 31), dict(G=None), dict(V=None),
+    dict(D=None), dict(ldg=4), dict(ldv=3), dict(ldx=3), dict(m=(1 << 20) + 1, ldg=1 << 21),
+    dict(n=(1 << 20) + 1, ldv=1 << 21, ldx=1 << 21), dict(G=ctypes.c_void_p(0x100002)),
+    dict(D=ctypes.c_void_p(0x500002)), dict(sv=ctypes.c_void_p(0x300002)), dict(c=ctypes.c_void_p(0x400002)),
+    dict(ws=None), dict(wsb=1000), dict(ws=ctypes.c_void_p(0x600008)),
+    dict(D=at(1)), dict(D=at(2)), dict(D=at(3)), dict(D=at(4)),
+])
+def test_matmul_int8_grad_rejects_bad_arguments(bad):
+    assert _grad(**bad) == bk.EINVAL
+
+
+def test_matmul_int8_grad_empty_and_workspace():
+    assert _grad(T=0, G=None, D=None, ws=None) == bk.OK
+    assert _grad(n=0, V=None, c=None, D=None, ws=None) == bk.OK
+    q = bk.lib().bakron_matmul_int8_grad_workspace_bytes
+    assert 0 < q(bk.BF16, 64, 64, 64) < q(bk.F16, 64, 64, 64) < q(bk.F32, 64, 64, 64) < q(bk.F32, 64, 200, 64)
+    assert q(bk.F64, 64, 64, 64) == q(bk.F32, -1, 64, 64) == q(bk.F32, 64, 1 << 21, 64) == 0
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 4)
     q = torch.zeros(2, 4, dtype=torch.int8)
@@ -84,7 +112,10 @@ def test_binding_checks(as_if_gpu):
     for bad in (lambda: bk.quantize_tokens(x.double()), lambda: bk.quantize_tokens(x, torch.ones(4).double()),
                 lambda: bk.matmul_int8(x, s, q), lambda: bk.matmul_int8(q, s, q.to(torch.int32)),
                 lambda: bk.matmul_int8(q, s.double(), q), lambda: bk.matmul_int8(q, s, q, s.half()),
-                lambda: bk.matmul_int8(q, s, q, out_dtype=torch.float64)):
+                lambda: bk.matmul_int8(q, s, q, out_dtype=torch.float64),
+                lambda: bk.matmul_int8_grad(x.double(), q), lambda: bk.matmul_int8_grad(x[:, :3], x),
+                lambda: bk.matmul_int8_grad(x[:, :3], q, s.double()),
+                lambda: bk.matmul_int8_grad(x[:, :3], q, out=torch.zeros(3, 4).half())):
         with pytest.raises(TypeError):
             bad()
     for bad in (lambda: bk.quantize_tokens(x[0]), lambda: bk.quantize_tokens(x.t()),
@@ -93,6 +124,10 @@ def test_binding_checks(as_if_gpu):
                 lambda: bk.matmul_int8(q.t(), s, q), lambda: bk.matmul_int8(q, s[:2], q),
                 lambda: bk.matmul_int8(q, s, q[:, :3]), lambda: bk.matmul_int8(q, s, q, torch.ones(4)),
                 lambda: bk.matmul_int8(q, s, q, out=torch.zeros(3, 4)),
+                lambda: bk.matmul_int8_grad(x, q), lambda: bk.matmul_int8_grad(x[:, :3], q, torch.ones(4)),
+                lambda: bk.matmul_int8_grad(x[:, :3], q, s, torch.ones(3)),
+                lambda: bk.matmul_int8_grad(x[:, :3], q, s, out=torch.zeros(3, 3)),
+                lambda: bk.matmul_int8_grad(x[:, :3], q, workspace=torch.zeros(9, dtype=torch.uint8)),
                 lambda: bk.matmul_int8(q, s, q, out=torch.zeros(3, 6)[:, ::2])):
         with pytest.raises(ValueError):
             bad()
