@@ -56,7 +56,7 @@ extern "C" {
                                (bakron_solve_status): its outputs are invalid */
 
 /* Element types. The calls of the solve take F32 and F64; the 8-bit product
- * takes F32, BF16 and F16. */
+ * and the cross entropy take F32, BF16 and F16. */
 #define BAKRON_F32 0
 #define BAKRON_F64 1
 #define BAKRON_BF16 2
@@ -502,6 +502,52 @@ int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n,
                             const float *sv, const float *channel,
                             void *dX, int64_t ldx,
                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Softmax cross entropy over a vocabulary, the logits z = X W^T never stored:
+ * the loss that the output-side samples of bakron_gram are gradients of, and
+ * that a quantised model is judged by.
+ *
+ * bakron_cross_entropy: for every token t
+ *   lse[t]  = log sum_v exp(z[t][v]),
+ *   loss[t] = lse[t] - z[t][targets[t]].
+ *   xtype   the type of X (T x d, ldx >= d; the hidden states) and W (V x d,
+ *           ldw >= d; the output layer): F32, BF16 or F16.
+ *   targets int64, length T. A target outside [0, V) (-100 by custom) marks a
+ *           token without one: its loss is 0, its lse still written.
+ *   loss, lse  out, float32, length T.
+ * Products are exact (for F32 to 2^-21 of each term), sums and exponentials
+ * float32. Logits of -inf add nothing; a token with a logit of +inf or NaN gets
+ * NaN (its loss is 0 all the same without a target). For F32 an infinity in X or
+ * W makes the logits it enters NaN.
+ *
+ * bakron_cross_entropy_grad: with g[t] the gradient of loss[t] (1 / T or 1 /
+ * (number of targets) for a mean) and lse as the forward call gave it,
+ *   D[t][v] = exp(z[t][v] - lse[t]) - [v = targets[t]], 0 without a target,
+ *   dX[t]   = g[t] sum_v D[t][v] W[v]    (T x d, lddx >= d; nullable),
+ *   dW[v]   = sum_t g[t] D[t][v] X[t]    (V x d, lddw >= d; nullable),
+ * both of xtype. The logits are formed again by pieces of the vocabulary whose
+ * D is held in the workspace: in bfloat16 for BF16 (an error of 2^-9 to 2^-8 a
+ * term, as the outputs' own), in float16 scaled by 2^14 for F16, with all of
+ * float32's bits for F32; sums are float32. A token without a target takes no
+ * part, whatever its X, lse or g hold. T = 0 gives dW = 0.
+ *
+ * Outputs must not overlap the inputs or each other (BAKRON_EINVAL). V >= 1;
+ * T, d <= 2^20. Rows that start at multiples of 16 bytes with d a multiple of
+ * 8 are read fastest (BF16, F16); any alignment and stride works.
+ * Asynchronous, deterministic.
+ * ------------------------------------------------------------------------ */
+size_t bakron_cross_entropy_workspace_bytes(int xtype, int64_t T, int64_t d, int64_t V);
+int bakron_cross_entropy(int xtype, int64_t T, int64_t d, int64_t V,
+                         const void *X, int64_t ldx, const void *W, int64_t ldw,
+                         const int64_t *targets, float *loss, float *lse,
+                         void *workspace, size_t workspace_bytes, void *stream);
+size_t bakron_cross_entropy_grad_workspace_bytes(int xtype, int64_t T, int64_t d, int64_t V);
+int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
+                              const void *X, int64_t ldx, const void *W, int64_t ldw,
+                              const int64_t *targets, const float *lse, const float *g,
+                              void *dX, int64_t lddx, void *dW, int64_t lddw,
+                              void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

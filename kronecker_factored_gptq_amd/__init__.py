@@ -22,7 +22,7 @@ __all__ = ["F32", "F64", "BF16", "F16", "SCALE_NONE", "SCALE_ROW", "SCALE_COL", 
            "solve", "solve_antidiag", "solve_noalloc", "factor_blockdiag", "solve_blockdiag",
            "loss_blockdiag", "solve_batched", "loss", "loss_batched", "row_scales", "row_scales_mse", "gram",
            "sample_sqnorms", "kfac_factors", "shampoo_factors", "quantize_tokens", "matmul_int8",
-           "matmul_int8_grad", "solve_schedule", "tile_size", "workspace_bytes"]
+           "matmul_int8_grad", "cross_entropy", "cross_entropy_grad", "solve_schedule", "tile_size", "workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libbakron.so")
@@ -144,6 +144,16 @@ def lib() -> ctypes.CDLL:
     L.bakron_matmul_int8_grad.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
                                           _vp, _i64, _vp, _sz, _vp]
     L.bakron_matmul_int8_grad.restype = _int
+    for name in ("bakron_cross_entropy_workspace_bytes", "bakron_cross_entropy_grad_workspace_bytes"):
+        f = getattr(L, name)
+        f.argtypes = [_int, _i64, _i64, _i64]
+        f.restype = _sz
+    L.bakron_cross_entropy.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                       _vp, _sz, _vp]
+    L.bakron_cross_entropy.restype = _int
+    L.bakron_cross_entropy_grad.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                            _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
+    L.bakron_cross_entropy_grad.restype = _int
     _lib = L
     return L
 
@@ -879,6 +889,66 @@ def matmul_int8_grad(G: torch.Tensor, Vq: torch.Tensor, sv: Optional[torch.Tenso
     if rc != OK:
         raise BakronError(rc, "bakron_matmul_int8_grad")
     return out
+
+
+def _entropy_args(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor):
+    """(type code, ldx, ldw, T, d, V) of the cross entropy's operands."""
+    code = _ft(X.dtype, "X")
+    ldx, ldw = _matrix(X, "X"), _matrix(W, "W", X.dtype)
+    (T, d), V = X.shape, W.size(0)
+    if W.size(1) != d:
+        raise ValueError(f"X and W must have rows of one length, got {d} and {W.size(1)}")
+    if V < 1:
+        raise ValueError("W must have a row")
+    _vector(targets, T, "targets", torch.int64)
+    return code, ldx, ldw, T, d, V
+
+
+def cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
+                  workspace: Optional[torch.Tensor] = None):
+    """Softmax cross entropy of hidden states X (T x d) under the output layer W
+    (V x d), one loss per token, the logits X W^T never stored
+    (bakron_cross_entropy). X and W are float32, bfloat16 or float16 (one type);
+    targets is int64, and one outside [0, V) (-100 by custom) marks a token
+    without a target, whose loss is 0. Returns loss and lse = log sum exp of the
+    logits, float32 vectors of length T. Asynchronous."""
+    dev = _check_device(X, W, targets, workspace)
+    code, ldx, ldw, T, d, V = _entropy_args(X, W, targets)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    L = lib()
+    ws = _workspace(L.bakron_cross_entropy_workspace_bytes(code, T, d, V), dev, workspace)
+    with torch.cuda.device(dev):
+        rc = L.bakron_cross_entropy(code, T, d, V, _p(X), ldx, _p(W), ldw, _p(targets), _p(loss),
+                                    _p(lse), _p(ws), ws.numel() * ws.element_size(), _stream(dev))
+    if rc != OK:
+        raise BakronError(rc, "bakron_cross_entropy")
+    return loss, lse
+
+
+def cross_entropy_grad(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                       g: torch.Tensor, need_dX: bool = True, need_dW: bool = True,
+                       workspace: Optional[torch.Tensor] = None):
+    """The gradient of sum_t g[t] loss[t] of ``cross_entropy`` with respect to X
+    and W (bakron_cross_entropy_grad), of their type: (dX, dW), None where not
+    needed. lse is the forward call's, g a float32 vector of length T (1 / (number of
+    targets) for their mean). The rows of dX are the output-side samples of the
+    layer below (``gram`` takes them in float32). Asynchronous."""
+    dev = _check_device(X, W, targets, lse, g, workspace)
+    code, ldx, ldw, T, d, V = _entropy_args(X, W, targets)
+    _vector(lse, T, "lse")
+    _vector(g, T, "g")
+    dX = torch.empty((T, d), dtype=X.dtype, device=dev) if need_dX else None
+    dW = torch.empty((V, d), dtype=X.dtype, device=dev) if need_dW else None
+    L = lib()
+    ws = _workspace(L.bakron_cross_entropy_grad_workspace_bytes(code, T, d, V), dev, workspace)
+    with torch.cuda.device(dev):
+        rc = L.bakron_cross_entropy_grad(code, T, d, V, _p(X), ldx, _p(W), ldw, _p(targets), _p(lse),
+                                         _p(g), _p(dX), max(d, 1), _p(dW), max(d, 1), _p(ws),
+                                         ws.numel() * ws.element_size(), _stream(dev))
+    if rc != OK:
+        raise BakronError(rc, "bakron_cross_entropy_grad")
+    return dX, dW
 
 
 def debug_set_wait_polls(polls: int) -> int:

@@ -1,10 +1,12 @@
 // C ABI of the calls beside the solve (declared in include/bakron.h): the
-// 8-bit product of quantised tokens with a layer's codes. Host side only:
-// argument checks and the choice of types; nothing here touches data.
+// 8-bit product of quantised tokens with a layer's codes, and the cross entropy
+// over a vocabulary. Host side only: argument checks and the choice of types;
+// nothing here touches data.
 #include <hip/hip_runtime.h>
 
 #include <climits>
 #include <cstdint>
+#include <initializer_list>
 
 #include "bakron.h"
 #include "launch.hpp"
@@ -49,6 +51,11 @@ inline int grad_planes(int t) { return t == BAKRON_F32 ? 3 : t == BAKRON_BF16 ? 
 inline bool grad_sizes_ok(int t, int64_t T, int64_t m, int64_t n) {
   return type_ok(t) && T >= 0 && m >= 0 && n >= 0 && T <= INT_MAX && m <= kMaxPlaneCols &&
          n <= kMaxPlaneCols && T * (m + 64) <= ((int64_t)1 << 41);
+}
+
+inline bool entropy_sizes_ok(int t, int64_t T, int64_t d, int64_t V) {
+  return type_ok(t) && T >= 0 && d >= 0 && V >= 1 && T <= kMaxPlaneCols && d <= kMaxPlaneCols &&
+         V <= INT_MAX && tiles_ok(T, V) && tiles_ok(d, V);
 }
 
 }  // namespace
@@ -127,6 +134,83 @@ int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n, const vo
                                           (BF16*)dX, ldx, workspace, s));
   return status(launch_matmul_int8_grad(T, m, n, (const F16*)G, ldg, Vq, ldv, sv, channel, (F16*)dX,
                                         ldx, workspace, s));
+}
+
+size_t bakron_cross_entropy_workspace_bytes(int xtype, int64_t T, int64_t d, int64_t V) {
+  if (!entropy_sizes_ok(xtype, T, d, V)) return 0;
+  return entropy_bytes((int)type_size(xtype), T, d, V) + kAlign;
+}
+
+int bakron_cross_entropy(int xtype, int64_t T, int64_t d, int64_t V, const void* X, int64_t ldx,
+                         const void* W, int64_t ldw, const int64_t* targets, float* loss,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!entropy_sizes_ok(xtype, T, d, V)) return BAKRON_EINVAL;
+  if (T == 0) return BAKRON_OK;
+  const size_t es = type_size(xtype);
+  if (!matrix_ok(X, T, d, ldx, es) || !matrix_ok(W, V, d, ldw, es)) return BAKRON_EINVAL;
+  if (!targets || !loss || !lse || (uintptr_t)targets % 8 || (uintptr_t)loss % 4 || (uintptr_t)lse % 4)
+    return BAKRON_EINVAL;
+  if (!workspace || (uintptr_t)workspace % kAlign ||
+      workspace_bytes < entropy_bytes((int)es, T, d, V))
+    return BAKRON_EINVAL;
+  for (const float* o : {loss, lse})
+    if (overlap(o, 1, T, T, 4, X, T, d, ldx, es) || overlap(o, 1, T, T, 4, W, V, d, ldw, es) ||
+        overlap(o, 1, T, T, 4, targets, 1, T, T, 8))
+      return BAKRON_EINVAL;
+  if (overlap(loss, 1, T, T, 4, lse, 1, T, T, 4)) return BAKRON_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (xtype == BAKRON_F32)
+    return status(launch_entropy(T, d, V, (const float*)X, ldx, (const float*)W, ldw, targets, loss,
+                                 lse, workspace, s));
+  if (xtype == BAKRON_BF16)
+    return status(launch_entropy(T, d, V, (const BF16*)X, ldx, (const BF16*)W, ldw, targets, loss,
+                                 lse, workspace, s));
+  return status(launch_entropy(T, d, V, (const F16*)X, ldx, (const F16*)W, ldw, targets, loss, lse,
+                               workspace, s));
+}
+
+size_t bakron_cross_entropy_grad_workspace_bytes(int xtype, int64_t T, int64_t d, int64_t V) {
+  if (!entropy_sizes_ok(xtype, T, d, V)) return 0;
+  return entropy_grad_bytes((int)type_size(xtype), T, d, V) + kAlign;
+}
+
+int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V, const void* X,
+                              int64_t ldx, const void* W, int64_t ldw, const int64_t* targets,
+                              const float* lse, const float* g, void* dX, int64_t lddx, void* dW,
+                              int64_t lddw, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!entropy_sizes_ok(xtype, T, d, V)) return BAKRON_EINVAL;
+  if (d == 0 || (!dX && !dW) || (T == 0 && !dW)) return BAKRON_OK;
+  const size_t es = type_size(xtype);
+  if (!matrix_ok(X, T, d, ldx, es) || !matrix_ok(W, V, d, ldw, es)) return BAKRON_EINVAL;
+  if ((dX && !matrix_ok(dX, T, d, lddx, es)) || (dW && !matrix_ok(dW, V, d, lddw, es)))
+    return BAKRON_EINVAL;
+  if (T > 0 && (!targets || !lse || !g || (uintptr_t)targets % 8 || (uintptr_t)lse % 4 ||
+                (uintptr_t)g % 4))
+    return BAKRON_EINVAL;
+  if (!workspace || (uintptr_t)workspace % kAlign ||
+      workspace_bytes < entropy_grad_bytes((int)es, T, d, V))
+    return BAKRON_EINVAL;
+  const struct {
+    const void* p;
+    int64_t rows, ld;
+  } outs[2] = {{dX, T, lddx}, {dW, V, lddw}};
+  for (const auto& o : outs)
+    if (overlap(o.p, o.rows, d, o.ld, es, X, T, d, ldx, es) ||
+        overlap(o.p, o.rows, d, o.ld, es, W, V, d, ldw, es) ||
+        overlap(o.p, o.rows, d, o.ld, es, targets, 1, T, T, 8) ||
+        overlap(o.p, o.rows, d, o.ld, es, lse, 1, T, T, 4) ||
+        overlap(o.p, o.rows, d, o.ld, es, g, 1, T, T, 4))
+      return BAKRON_EINVAL;
+  if (overlap(dX, T, d, lddx, es, dW, V, d, lddw, es)) return BAKRON_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (xtype == BAKRON_F32)
+    return status(launch_entropy_grad(T, d, V, (const float*)X, ldx, (const float*)W, ldw, targets,
+                                      lse, g, (float*)dX, lddx, (float*)dW, lddw, workspace, s));
+  if (xtype == BAKRON_BF16)
+    return status(launch_entropy_grad(T, d, V, (const BF16*)X, ldx, (const BF16*)W, ldw, targets,
+                                      lse, g, (BF16*)dX, lddx, (BF16*)dW, lddw, workspace, s));
+  return status(launch_entropy_grad(T, d, V, (const F16*)X, ldx, (const F16*)W, ldw, targets, lse, g,
+                                    (F16*)dX, lddx, (F16*)dW, lddw, workspace, s));
 }
 
 }  // extern "C"

@@ -1,0 +1,468 @@
+// Softmax cross entropy over a large vocabulary on gfx950, the logits z = X W^T
+// never stored, and its gradient.
+//
+// Forward: a tiled product (tile_product.hpp; rows = vocabulary, columns =
+// tokens) whose epilogue keeps, per token and wave, the largest logit m and
+// sum exp(z - m) of its rows, and the target's logit; a second kernel joins
+// these to lse and the loss.
+//
+// Gradient: with D[t][v] = exp(z - lse_t) - [v = y_t] (0 for a token without a
+// target), dX = g (.) (D W) and dW = D^T (g (.) X). The vocabulary goes by in
+// pieces: a piece's logits are formed again, D is written as 16-bit planes in
+// both orders, and the two products are formed from it; dX is summed over the
+// pieces in float32.
+//
+// float32 operands are three bfloat16 planes each (exact), and a product the six
+// pairs of planes whose terms reach float32's precision.
+#include "launch.hpp"
+#include "tile_product.hpp"
+
+namespace bk {
+
+namespace {
+
+template <typename X> struct Kind;
+template <> struct Kind<float> {
+  typedef MmaBF16 mma;
+  static constexpr int split = kBF16x3;
+  static constexpr bool f16 = false;
+};
+template <> struct Kind<BF16> {
+  typedef MmaBF16 mma;
+  static constexpr int split = kBF16x1;
+  static constexpr bool f16 = false;
+};
+template <> struct Kind<F16> {
+  typedef MmaF16 mma;
+  static constexpr int split = kF16x1;
+  static constexpr bool f16 = true;
+};
+
+// What D is multiplied by before it becomes 16-bit planes: float16 reaches down
+// to 2^-24, and probabilities of a large vocabulary well below; 2^14 brings
+// them up, |D| <= 1 staying far from its largest value. bfloat16 has float32's
+// range.
+template <typename X> constexpr float dscale() { return Kind<X>::f16 ? 16384.0f : 1.0f; }
+
+template <typename X> inline PlanePairs pairs_of() {
+  if (kPlanes[Kind<X>::split] == 3) return {6, {0, 0, 1, 0, 2, 1}, {0, 1, 0, 2, 0, 1}};
+  return {1, {0}, {0}};
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ inline float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+struct MaxSum {
+  float m, s;
+};
+// The sums of two sets of terms, each relative to its largest; an empty set has
+// m = -inf, s = 0.
+__device__ inline MaxSum join(MaxSum a, MaxSum b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -__builtin_inff()) return {m, a.s + b.s};
+  return {m, a.s * exp_of(a.m - m) + b.s * exp_of(b.m - m)};
+}
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+// parts[(part0 + tile * WR + wave row) * T + t], and zy[t] from the wave that
+// holds row y[t]; W's rows are the vocabulary's from v0 on.
+template <class M, int BR, int BC, int WR, int WC, bool ANY>
+__global__ __launch_bounds__(64 * WR * WC) void entropy_kernel(
+    TileOperand W, TileOperand X, int64_t kbytes, PlanePairs pairs, const int64_t* __restrict__ y,
+    int64_t v0, MaxSum* __restrict__ parts, int64_t part0, float* __restrict__ zy, unsigned nr,
+    unsigned nc) {
+  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  extern __shared__ char lds[];
+  int tr, tc;
+  tile_of(blockIdx.x, nr, nc, tr, tc);
+  const int64_t r0 = (int64_t)tr * BR, c0 = (int64_t)tc * BC;
+  TP tp;
+  tp.zero();
+  if (ANY)
+    tp.run_any(W, X, kbytes, r0, c0, lds);
+  else
+    tp.run(W, X, kbytes, pairs, r0, c0, lds);
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int64_t rb = r0 + tp.wave_r(), T = X.rows;
+  // rows of this lane's that are W's: 16 i + 4 q + e < left
+  const int left = (int)(W.rows - rb < TP::FR * 16 ? W.rows - rb : TP::FR * 16) - 4 * q;
+  const int64_t part = part0 + (int64_t)tr * WR + (threadIdx.x >> 6) / WC;
+#pragma unroll
+  for (int j = 0; j < TP::FC; ++j) {
+    const int64_t t = c0 + tp.wave_c() + j * 16 + (lane & 15);
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < TP::FR; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (16 * i + e < left) m = fmaxf(m, tp.acc[i][j][e]);
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    // a set of -inf alone sums to 0 (and one with a NaN to NaN)
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TP::FR; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (16 * i + e < left) s += exp_of(tp.acc[i][j][e] - base);
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (t < T) {
+      if (q == 0) parts[part * T + t] = {m, s};
+      const int64_t yt = y[t];  // the target among this lane's rows
+      const int64_t at = yt < 0 ? -1 : yt - v0 - rb - 4 * q;
+#pragma unroll
+      for (int i = 0; i < TP::FR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * i + e == at && at < left) zy[t] = tp.acc[i][j][e];
+    }
+  }
+}
+
+// 16 tokens per workgroup, 16 threads to each, the parts in a fixed order.
+__global__ __launch_bounds__(256) void entropy_join_kernel(
+    int64_t T, int64_t V, int64_t nparts, const MaxSum* __restrict__ parts,
+    const float* __restrict__ zy, const int64_t* __restrict__ y, float* __restrict__ loss,
+    float* __restrict__ lse) {
+  __shared__ MaxSum red[16][16];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t t = (int64_t)blockIdx.x * 16 + tx;
+  MaxSum a = {-__builtin_inff(), 0.0f};
+  if (t < T)
+    for (int64_t p = ty; p < nparts; p += 16) a = join(a, parts[p * T + t]);
+  red[ty][tx] = a;
+  __syncthreads();
+  if (ty == 0 && t < T) {
+    for (int k = 1; k < 16; ++k) a = join(a, red[k][tx]);
+    const float l = a.m + logf(a.s);
+    lse[t] = l;
+    loss[t] = y[t] >= 0 && y[t] < V ? l - zy[t] : 0.0f;
+  }
+}
+
+// w[t] = g[t] for a token with a target, else 0; top = max |w|; rel = w / top
+// (0 where top is 0). One workgroup. The maximum is taken over bits, in which a
+// NaN is larger than infinity.
+__global__ __launch_bounds__(1024) void entropy_weights_kernel(
+    int64_t T, int64_t V, const int64_t* __restrict__ y, const float* __restrict__ g,
+    float* __restrict__ w, float* __restrict__ rel, float* __restrict__ top) {
+  __shared__ unsigned red[16];
+  unsigned m = 0;
+  for (int64_t t = threadIdx.x; t < T; t += 1024) {
+    const float v = y[t] >= 0 && y[t] < V ? g[t] : 0.0f;
+    w[t] = v;
+    const unsigned a = __float_as_uint(v) & 0x7fffffffu;
+    m = a > m ? a : m;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const unsigned u = __shfl_xor(m, o, 64);
+    m = u > m ? u : m;
+  }
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  for (int k = 0; k < 16; ++k) m = red[k] > m ? red[k] : m;
+  const float mx = __uint_as_float(m);
+  if (threadIdx.x == 0) *top = mx;
+  for (int64_t t = threadIdx.x; t < T; t += 1024) rel[t] = m == 0 ? 0.0f : w[t] / mx;
+}
+
+// D's planes of a piece, in both orders (each nullable): P rows are tokens, Pt
+// rows the piece's. Written up to the planes' padding, with zeros there.
+template <class M, int KIND, int BR, int BC, int WR, int WC, bool ANY>
+__global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
+    TileOperand W, TileOperand X, int64_t kbytes, PlanePairs pairs, const int64_t* __restrict__ y,
+    int64_t V, int64_t v0, const float* __restrict__ lse, float scale, Planes P, Planes Pt,
+    unsigned nr, unsigned nc) {
+  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  constexpr int NP = kPlanes[KIND];
+  extern __shared__ char lds[];
+  int tr, tc;
+  tile_of(blockIdx.x, nr, nc, tr, tc);
+  const int64_t r0 = (int64_t)tr * BR, c0 = (int64_t)tc * BC;
+  TP tp;
+  tp.zero();
+  if (ANY)
+    tp.run_any(W, X, kbytes, r0, c0, lds);
+  else
+    tp.run(W, X, kbytes, pairs, r0, c0, lds);
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int64_t T = X.rows;
+#pragma unroll
+  for (int j = 0; j < TP::FC; ++j) {
+    const int64_t t = c0 + tp.wave_c() + j * 16 + (lane & 15);
+    const int64_t yt = t < T ? y[t] : -1;
+    const bool has = yt >= 0 && yt < V;
+    const float l = t < T ? lse[t] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < TP::FR; ++i) {
+      const int64_t r = r0 + tp.wave_r() + i * 16 + 4 * q;
+      unsigned short w[NP][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = exp_of(tp.acc[i][j][e] - l);
+        if (v0 + r + e == yt) v -= 1.0f;
+        v = has && r + e < W.rows ? v * scale : 0.0f;
+        unsigned short k[NP];
+        split16<KIND>(v, k);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) w[p][e] = k[p];
+      }
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        if (P.w && t < T && r * 2 < P.ld)
+          *(uint2*)(P.w + p * P.plane + t * P.ld + r * 2) = __builtin_bit_cast(uint2, w[p]);
+        if (Pt.w && t * 2 < Pt.ld) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e < W.rows)
+              *(unsigned short*)(Pt.w + p * Pt.plane + (r + e) * Pt.ld + t * 2) = w[p][e];
+        }
+      }
+    }
+  }
+}
+
+template <class M, int BR, int BC, int WR, int WC, bool ANY>
+static hipError_t start_entropy(const TileOperand& W, const TileOperand& X, int64_t kbytes,
+                                const PlanePairs& pairs, const int64_t* y, int64_t v0,
+                                MaxSum* parts, int64_t& part0, float* zy, hipStream_t s) {
+  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  auto* k = entropy_kernel<M, BR, BC, WR, WC, ANY>;
+  if (TP::kLds > 65536) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, TP::kLds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t nr = (W.rows + BR - 1) / BR, nc = (X.rows + BC - 1) / BC;
+  hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc)), dim3(TP::kThreads), TP::kLds, s, W, X, kbytes,
+                     pairs, y, v0, parts, part0, zy, (unsigned)nr, (unsigned)nc);
+  part0 += nr * WR;
+  return hipGetLastError();
+}
+
+template <class M, int KIND, int BR, int BC, int WR, int WC, bool ANY>
+static hipError_t start_entropy_diff(const TileOperand& W, const TileOperand& X, int64_t kbytes,
+                                     const PlanePairs& pairs, const int64_t* y, int64_t V,
+                                     int64_t v0, const float* lse, float scale, Planes P,
+                                     Planes Pt, hipStream_t s) {
+  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  auto* k = entropy_diff_kernel<M, KIND, BR, BC, WR, WC, ANY>;
+  if (TP::kLds > 65536) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, TP::kLds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t nr = (W.rows + BR - 1) / BR, nc = (X.rows + BC - 1) / BC;
+  hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc)), dim3(TP::kThreads), TP::kLds, s, W, X, kbytes,
+                     pairs, y, V, v0, lse, scale, P, Pt, (unsigned)nr, (unsigned)nc);
+  return hipGetLastError();
+}
+
+// ---- workspaces -------------------------------------------------------------
+// Rows of W whose planes (float32 operands) are held at once: 512 MiB of them.
+static int64_t plane_piece(int64_t d, int64_t V) {
+  const int64_t per = 3 * plane_ld(d);
+  int64_t p = per ? ((int64_t)512 << 20) / per / 256 * 256 : V;
+  if (p < 256) p = 256;
+  return p < V ? p : V;
+}
+// Columns of D held at once: 256 MiB in each order, small enough for the
+// last-level cache to serve the products that read them.
+static int64_t diff_piece(int es, int64_t T, int64_t d, int64_t V) {
+  const int64_t per = 2 * T * (es == 4 ? 3 : 1);
+  int64_t p = per ? ((int64_t)256 << 20) / per / 256 * 256 : V;
+  if (p < 256) p = 256;
+  if (p > ((int64_t)1 << 20)) p = (int64_t)1 << 20;  // rows the direct loads can step over
+  if (es == 4 && p > plane_piece(d, V)) p = plane_piece(d, V);
+  return p < V ? p : V;
+}
+
+// Offsets into the workspaces.
+struct EntropyLayout {
+  size_t parts, zy, xp, wp, total;
+};
+static EntropyLayout entropy_layout(int es, int64_t T, int64_t d, int64_t V) {
+  EntropyLayout L;
+  L.parts = 0;
+  // two waves of rows in each tile, of at least 128 rows
+  const int64_t nparts = 2 * ((V + 127) / 128) + 2 * ((V + 255) / 256);
+  L.zy = L.parts + up256((size_t)(nparts * T) * sizeof(MaxSum));
+  L.xp = L.zy + up256((size_t)T * 4);
+  L.wp = L.xp + (es == 4 ? (size_t)(3 * T * plane_ld(d)) : 0);
+  L.total = L.wp + (es == 4 ? (size_t)(3 * plane_piece(d, V) * plane_ld(d)) : 0);
+  return L;
+}
+size_t entropy_bytes(int es, int64_t T, int64_t d, int64_t V) {
+  return entropy_layout(es, T, d, V).total;
+}
+
+struct GradLayout {
+  size_t w, rel, top, xp, xt, wp, wt, p, pt, acc, total;
+  int64_t piece, ldacc;
+};
+static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
+  GradLayout L;
+  const int64_t np = es == 4 ? 3 : 1;
+  L.piece = diff_piece(es, T, d, V);
+  L.ldacc = (d + 3) / 4 * 4;
+  L.w = 0;
+  L.rel = L.w + up256((size_t)T * 4);
+  L.top = L.rel + up256((size_t)T * 4);
+  L.xp = L.top + 256;
+  L.xt = L.xp + (es == 4 ? (size_t)(3 * T * plane_ld(d)) : 0);
+  L.wp = L.xt + (size_t)(np * d * plane_ld(T));
+  L.wt = L.wp + (es == 4 ? (size_t)(3 * L.piece * plane_ld(d)) : 0);
+  L.p = L.wt + (size_t)(np * d * plane_ld(L.piece));
+  L.pt = L.p + (size_t)(np * T * plane_ld(L.piece));
+  L.acc = L.pt + (size_t)(np * L.piece * plane_ld(T));
+  L.total = L.acc + (L.piece < V ? up256((size_t)(T * L.ldacc) * 4) : 0);
+  return L;
+}
+size_t entropy_grad_bytes(int es, int64_t T, int64_t d, int64_t V) {
+  return grad_layout(es, T, d, V).total;
+}
+
+// ---- calls --------------------------------------------------------------------
+template <typename X>
+hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t ldx, const X* w,
+                          int64_t ldw, const int64_t* y, float* loss, float* lse, void* ws,
+                          hipStream_t s) {
+  typedef Kind<X> K;
+  typedef typename K::mma M;
+  if (T <= 0) return hipSuccess;
+  const EntropyLayout L = entropy_layout(sizeof(X), T, d, V);
+  char* b = (char*)ws;
+  MaxSum* parts = (MaxSum*)(b + L.parts);
+  float* zy = (float*)(b + L.zy);
+  const PlanePairs pairs = pairs_of<X>();
+  int64_t nparts = 0;
+  hipError_t e;
+  constexpr bool split = sizeof(X) == 4;
+  TileOperand xo = {(const char*)x, ldx * (int64_t)sizeof(X), 0, T};
+  int64_t kbytes = d * (int64_t)sizeof(X), piece = V;
+  if (split) {
+    const Planes p = {b + L.xp, plane_ld(d), T * plane_ld(d)};
+    if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, p, s)) != hipSuccess) return e;
+    xo = {p.w, p.ld, p.plane, T};
+    kbytes = (d + 7) / 8 * 16;
+    piece = plane_piece(d, V);
+  }
+  for (int64_t v0 = 0; v0 < V; v0 += piece) {
+    const int64_t rows = V - v0 < piece ? V - v0 : piece;
+    TileOperand wo = {(const char*)(w + v0 * ldw), ldw * (int64_t)sizeof(X), 0, rows};
+    if (split) {
+      const Planes p = {b + L.wp, plane_ld(d), rows * plane_ld(d)};
+      if ((e = launch_planes<X, K::split>(rows, d, w + v0 * ldw, ldw, nullptr, p, s)) != hipSuccess)
+        return e;
+      wo = {p.w, p.ld, p.plane, rows};
+    }
+    if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
+      e = start_entropy<M, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
+    else if (((rows + 255) / 256) * ((T + 255) / 256) >= 192)
+      e = start_entropy<M, 256, 256, 2, 4, false>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
+    else
+      e = start_entropy<M, 128, 128, 2, 2, false>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(entropy_join_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, s, T, V,
+                     nparts, parts, zy, y, loss, lse);
+  return hipGetLastError();
+}
+
+template <typename X>
+hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int64_t ldx, const X* w,
+                               int64_t ldw, const int64_t* y, const float* lse, const float* g,
+                               X* dX, int64_t lddx, X* dW, int64_t lddw, void* ws, hipStream_t s) {
+  typedef Kind<X> K;
+  typedef typename K::mma M;
+  if (T <= 0) {  // no tokens: dW is zero, an empty sum
+    const Planes none = {(char*)ws, 0, 0};
+    const PlaneEpilogue ep = {nullptr, nullptr, nullptr, 1.0f, nullptr, 0};
+    return dW ? launch_plane_product<X, K::f16>(d, V, 0, none, none, pairs_of<X>(), ep, dW, lddw, s)
+              : hipSuccess;
+  }
+  const GradLayout L = grad_layout(sizeof(X), T, d, V);
+  char* b = (char*)ws;
+  float *wt = (float*)(b + L.w), *rel = (float*)(b + L.rel), *top = (float*)(b + L.top);
+  const PlanePairs pairs = pairs_of<X>();
+  constexpr bool split = sizeof(X) == 4;
+  constexpr int64_t es = sizeof(X);
+  hipLaunchKernelGGL(entropy_weights_kernel, dim3(1), dim3(1024), 0, s, T, V, y, g, wt, rel, top);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  TileOperand xo = {(const char*)x, ldx * es, 0, T};
+  int64_t kbytes = d * es;
+  if (split) {
+    const Planes p = {b + L.xp, plane_ld(d), T * plane_ld(d)};
+    if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, p, s)) != hipSuccess) return e;
+    xo = {p.w, p.ld, p.plane, T};
+    kbytes = (d + 7) / 8 * 16;
+  }
+  const Planes xt = {b + L.xt, plane_ld(T), d * plane_ld(T)};
+  if (dW && (e = launch_planes_t<X, K::split>(T, d, x, ldx, rel, xt, s)) != hipSuccess) return e;
+  float* acc = (float*)(b + L.acc);
+  for (int64_t v0 = 0; v0 < V; v0 += L.piece) {
+    const int64_t rows = V - v0 < L.piece ? V - v0 : L.piece;
+    const X* wv = w + v0 * ldw;
+    TileOperand wo = {(const char*)wv, ldw * es, 0, rows};
+    if (split) {
+      const Planes p = {b + L.wp, plane_ld(d), rows * plane_ld(d)};
+      if ((e = launch_planes<X, K::split>(rows, d, wv, ldw, nullptr, p, s)) != hipSuccess) return e;
+      wo = {p.w, p.ld, p.plane, rows};
+    }
+    const Planes P = {dX ? b + L.p : nullptr, plane_ld(rows), T * plane_ld(rows)};
+    const Planes Pt = {dW ? b + L.pt : nullptr, plane_ld(T), rows * plane_ld(T)};
+    if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
+      e = start_entropy_diff<M, K::split, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, V, v0, lse,
+                                                                dscale<X>(), P, Pt, s);
+    else if (((rows + 255) / 256) * ((T + 255) / 256) >= 192)
+      e = start_entropy_diff<M, K::split, 256, 256, 2, 4, false>(wo, xo, kbytes, pairs, y, V, v0,
+                                                                 lse, dscale<X>(), P, Pt, s);
+    else
+      e = start_entropy_diff<M, K::split, 128, 128, 2, 2, false>(wo, xo, kbytes, pairs, y, V, v0,
+                                                                 lse, dscale<X>(), P, Pt, s);
+    if (e != hipSuccess) return e;
+    if (dX) {
+      const Planes wtp = {b + L.wt, plane_ld(rows), d * plane_ld(rows)};
+      if ((e = launch_planes_t<X, K::split>(rows, d, wv, ldw, nullptr, wtp, s)) != hipSuccess)
+        return e;
+      const bool last = v0 + rows == V;
+      const float* prev = v0 > 0 ? acc : nullptr;
+      if (last) {
+        const PlaneEpilogue ep = {nullptr, wt, nullptr, 1.0f / dscale<X>(), prev, L.ldacc};
+        e = launch_plane_product<X, K::f16>(d, T, rows, wtp, P, pairs, ep, dX, lddx, s);
+      } else {
+        const PlaneEpilogue ep = {nullptr, nullptr, nullptr, 1.0f, prev, L.ldacc};
+        e = launch_plane_product<float, K::f16>(d, T, rows, wtp, P, pairs, ep, acc, L.ldacc, s);
+      }
+      if (e != hipSuccess) return e;
+    }
+    if (dW) {
+      const PlaneEpilogue ep = {nullptr, nullptr, top, 1.0f / dscale<X>(), nullptr, 0};
+      e = launch_plane_product<X, K::f16>(d, rows, T, xt, Pt, pairs, ep, dW + v0 * lddw, lddw, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+#define BK_INST(X)                                                                             \
+  template hipError_t launch_entropy<X>(int64_t, int64_t, int64_t, const X*, int64_t,          \
+                                        const X*, int64_t, const int64_t*, float*, float*,     \
+                                        void*, hipStream_t);                                   \
+  template hipError_t launch_entropy_grad<X>(int64_t, int64_t, int64_t, const X*, int64_t,     \
+                                             const X*, int64_t, const int64_t*, const float*,  \
+                                             const float*, X*, int64_t, X*, int64_t, void*,    \
+                                             hipStream_t);
+BK_INST(float)
+BK_INST(BF16)
+BK_INST(F16)
+#undef BK_INST
+
+}  // namespace bk

@@ -299,16 +299,31 @@ struct Planes {
 template <typename X, int KIND>
 hipError_t launch_planes(int64_t rows, int64_t cols, const X* x, int64_t ldx,
                          const float* col_scale, Planes out, hipStream_t s);
-// out = planes of the transpose of X (rows x cols): cols x rows.
+// out = planes of the transpose of X (rows x cols) times row_scale (nullable; a
+// row whose scale is 0 gives 0 whatever it holds): cols x rows.
 template <typename X, int KIND>
-hipError_t launch_planes_t(int64_t rows, int64_t cols, const X* x, int64_t ldx, Planes out,
-                           hipStream_t s);
-// Y[c][r] = row_scale[r] * sum over the plane pairs of R[r][k] C[c][k], k < K:
-// R rows r < M, C rows c < N (row_scale nullable). F16: the planes' type.
+hipError_t launch_planes_t(int64_t rows, int64_t cols, const X* x, int64_t ldx,
+                           const float* row_scale, Planes out, hipStream_t s);
+// The plane pairs of a product: planes r[i] and c[i] of its two operands.
+struct PlanePairs {
+  int n;
+  unsigned char r[6], c[6];
+};
+// Y[c][r] = (sum + prev[c][r]) * row_scale[r] * alpha * beta * col_scale[c];
+// every pointer nullable. prev has rows of whole groups of four, 16-byte
+// aligned, and may be Y.
+struct PlaneEpilogue {
+  const float *row_scale, *col_scale, *alpha;
+  float beta;
+  const float* prev;
+  int64_t ldprev;
+};
+// The sum over the plane pairs of R[r][k] C[c][k], k < K, for R's rows r < M and
+// C's rows c < N. F16P: the planes are float16 (else bfloat16).
 template <typename O, bool F16P>
-hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C, int npairs,
-                                const unsigned char* pr, const unsigned char* pc,
-                                const float* row_scale, O* Y, int64_t ldy, hipStream_t s);
+hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C,
+                                const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,
+                                int64_t ldy, hipStream_t s);
 
 // dX (T x n) = channel (.) ((G sv) Vq); sv and channel nullable. ws holds
 // matmul_int8_grad_bytes(planes of G's type: float 3, BF16 1, F16 2).
@@ -318,5 +333,19 @@ hipError_t launch_matmul_int8_grad(int64_t T, int64_t m, int64_t n, const G* g, 
                                    const int8_t* Vq, int64_t ldv, const float* sv,
                                    const float* channel, G* dX, int64_t ldx, void* ws,
                                    hipStream_t s);
+
+// ---- cross entropy (entropy_kernels.hip) ------------------------------------
+// Workspace bytes; `es` is the element size of X and W (4: three planes each).
+size_t entropy_bytes(int es, int64_t T, int64_t d, int64_t V);
+size_t entropy_grad_bytes(int es, int64_t T, int64_t d, int64_t V);
+template <typename X>
+hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t ldx, const X* w,
+                          int64_t ldw, const int64_t* y, float* loss, float* lse, void* ws,
+                          hipStream_t s);
+// dX (T x d) and dW (V x d), each nullable.
+template <typename X>
+hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int64_t ldx, const X* w,
+                               int64_t ldw, const int64_t* y, const float* lse, const float* g,
+                               X* dX, int64_t lddx, X* dW, int64_t lddw, void* ws, hipStream_t s);
 
 }  // namespace bk

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
 template <typename X, int KIND>
 __global__ __launch_bounds__(256) void planes_t_kernel(int64_t rows, int64_t cols,
                                                        const X* __restrict__ x, int64_t ldx,
-                                                       Planes out) {
+                                                       const float* __restrict__ rs, Planes out) {
   constexpr int NP = kPlanes[KIND];
   __shared__ float tile[64][65];
   const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
@@ -49,7 +49,9 @@ __global__ __launch_bounds__(256) void planes_t_kernel(int64_t rows, int64_t col
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
     const int64_t r = r0 + u * 4 + ty, c = c0 + tx;
-    tile[u * 4 + ty][tx] = r < rows && c < cols ? to_f32(x[r * ldx + c]) : 0.0f;
+    float v = r < rows && c < cols ? to_f32(x[r * ldx + c]) : 0.0f;
+    if (rs && r < rows) v = rs[r] == 0.0f ? 0.0f : v * rs[r];
+    tile[u * 4 + ty][tx] = v;
   }
   __syncthreads();
 #pragma unroll
@@ -73,9 +75,8 @@ __global__ __launch_bounds__(256) void planes_t_kernel(int64_t rows, int64_t col
 
 template <class M, typename O, int BR, int BC, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
-    TileOperand R, TileOperand C, int64_t kbytes, PlanePairs pairs,
-    const float* __restrict__ row_scale, O* __restrict__ Y, int64_t ldy, bool vec, unsigned nr,
-    unsigned nc) {
+    TileOperand R, TileOperand C, int64_t kbytes, PlanePairs pairs, PlaneEpilogue ep,
+    O* __restrict__ Y, int64_t ldy, bool vec, unsigned nr, unsigned nc) {
   typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
   extern __shared__ char lds[];
   int tr, tc;
@@ -84,27 +85,46 @@ __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
   TP tp;
   tp.zero();
   tp.run(R, C, kbytes, pairs, r0, c0, lds);
-  float sr[TP::FR][4];
+  const int lane = threadIdx.x & 63;
+  const int64_t rb = r0 + tp.wave_r() + 4 * (lane >> 4), cb = c0 + tp.wave_c() + (lane & 15);
+  const float all = (ep.alpha ? *ep.alpha : 1.0f) * ep.beta;
+  float sr[TP::FR][4], sc[TP::FC];
 #pragma unroll
   for (int i = 0; i < TP::FR; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sr[i][e] = 1.0f;
-  if (row_scale) {
+    for (int e = 0; e < 4; ++e) sr[i][e] = all;
+  if (ep.row_scale) {
 #pragma unroll
     for (int i = 0; i < TP::FR; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t r = r0 + tp.wave_r() + i * 16 + 4 * ((threadIdx.x & 63) >> 4) + e;
-        sr[i][e] = row_scale[r < R.rows ? r : R.rows - 1];
+        const int64_t r = rb + i * 16 + e;
+        sr[i][e] = ep.row_scale[r < R.rows ? r : R.rows - 1] * all;
       }
   }
+#pragma unroll
+  for (int j = 0; j < TP::FC; ++j) {
+    const int64_t c = cb + j * 16;
+    sc[j] = ep.col_scale ? ep.col_scale[c < C.rows ? c : C.rows - 1] : 1.0f;
+  }
+  if (ep.prev) {  // rows of whole groups of four: its columns are padded
+#pragma unroll
+    for (int j = 0; j < TP::FC; ++j) {
+      const int64_t c = cb + j * 16;
+      if (c >= C.rows) continue;
+#pragma unroll
+      for (int i = 0; i < TP::FR; ++i)
+        if (rb + i * 16 < R.rows)
+          tp.acc[i][j] += *(const f32x4*)(ep.prev + c * ep.ldprev + rb + i * 16);
+    }
+  }
   store_tile(tp, r0, c0, R.rows, C.rows, Y, ldy, vec,
-             [&](float a, int i, int, int e) { return a * sr[i][e]; });
+             [&](float a, int i, int j, int e) { return a * sr[i][e] * sc[j]; });
 }
 
 template <class M, typename O, int BR, int BC, int WR, int WC>
 static hipError_t start_plane_product(const TileOperand& R, const TileOperand& C, int64_t kbytes,
-                                      const PlanePairs& pairs, const float* row_scale, O* Y,
+                                      const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,
                                       int64_t ldy, hipStream_t s) {
   typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
   auto* k = plane_product_kernel<M, O, BR, BC, WR, WC>;
@@ -115,27 +135,22 @@ static hipError_t start_plane_product(const TileOperand& R, const TileOperand& C
   }
   const int64_t nr = (R.rows + BR - 1) / BR, nc = (C.rows + BC - 1) / BC;
   hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc)), dim3(TP::kThreads), TP::kLds, s, R, C, kbytes,
-                     pairs, row_scale, Y, ldy, vec4_ok(Y, ldy), (unsigned)nr, (unsigned)nc);
+                     pairs, ep, Y, ldy, vec4_ok(Y, ldy), (unsigned)nr, (unsigned)nc);
   return hipGetLastError();
 }
 
 template <typename O, bool F16P>
-hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C, int npairs,
-                                const unsigned char* pr, const unsigned char* pc,
-                                const float* row_scale, O* Y, int64_t ldy, hipStream_t s) {
+hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C,
+                                const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,
+                                int64_t ldy, hipStream_t s) {
   typedef typename std::conditional<F16P, MmaF16, MmaBF16>::type Mma;
   if (M <= 0 || N <= 0) return hipSuccess;
   const TileOperand r = {R.w, R.ld, R.plane, M}, c = {C.w, C.ld, C.plane, N};
-  PlanePairs pairs = {npairs, {0}, {0}};
-  for (int i = 0; i < npairs; ++i) {
-    pairs.r[i] = pr[i];
-    pairs.c[i] = pc[i];
-  }
   const int64_t kbytes = (K + 7) / 8 * 16;  // whole 16-byte chunks: the planes' padding is zero
   const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
   if (big >= 192)
-    return start_plane_product<Mma, O, 256, 256, 2, 4>(r, c, kbytes, pairs, row_scale, Y, ldy, s);
-  return start_plane_product<Mma, O, 128, 128, 2, 2>(r, c, kbytes, pairs, row_scale, Y, ldy, s);
+    return start_plane_product<Mma, O, 256, 256, 2, 4>(r, c, kbytes, pairs, ep, Y, ldy, s);
+  return start_plane_product<Mma, O, 128, 128, 2, 2>(r, c, kbytes, pairs, ep, Y, ldy, s);
 }
 
 template <typename X, int KIND>
@@ -149,12 +164,12 @@ hipError_t launch_planes(int64_t rows, int64_t cols, const X* x, int64_t ldx,
 }
 
 template <typename X, int KIND>
-hipError_t launch_planes_t(int64_t rows, int64_t cols, const X* x, int64_t ldx, Planes out,
-                           hipStream_t s) {
+hipError_t launch_planes_t(int64_t rows, int64_t cols, const X* x, int64_t ldx,
+                           const float* row_scale, Planes out, hipStream_t s) {
   if (rows <= 0 || cols <= 0) return hipSuccess;
   hipLaunchKernelGGL((planes_t_kernel<X, KIND>),
                      dim3((unsigned)((rows + 63) / 64), (unsigned)((cols + 63) / 64)), dim3(256), 0,
-                     s, rows, cols, x, ldx, out);
+                     s, rows, cols, x, ldx, row_scale, out);
   return hipGetLastError();
 }
 
@@ -184,13 +199,32 @@ hipError_t launch_matmul_int8_grad(int64_t T, int64_t m, int64_t n, const G* g, 
   if (T <= 0 || n <= 0) return hipSuccess;
   const int64_t ld = plane_ld(m);
   const Planes v = {(char*)ws, ld, 0}, gp = {(char*)ws + n * ld, ld, T * ld};
-  hipError_t e = launch_planes_t<I8, kBF16x1>(m, n, (const I8*)Vq, ldv, v, s);
+  hipError_t e = launch_planes_t<I8, kBF16x1>(m, n, (const I8*)Vq, ldv, nullptr, v, s);
   if (e != hipSuccess) return e;
   if ((e = launch_planes<G, kind>(T, m, g, ldg, sv, gp, s)) != hipSuccess) return e;
-  const unsigned char pr[3] = {0, 0, 0}, pc[3] = {0, 1, 2};
-  return launch_plane_product<G, false>(n, T, m, v, gp, kPlanes[kind], pr, pc, channel, dX, ldx, s);
+  const PlanePairs pairs = {kPlanes[kind], {0, 0, 0}, {0, 1, 2}};
+  const PlaneEpilogue ep = {channel, nullptr, nullptr, 1.0f, nullptr, 0};
+  return launch_plane_product<G, false>(n, T, m, v, gp, pairs, ep, dX, ldx, s);
 }
 
+#define BK_INST_P(X, KIND)                                                                  \
+  template hipError_t launch_planes<X, KIND>(int64_t, int64_t, const X*, int64_t,           \
+                                             const float*, Planes, hipStream_t);            \
+  template hipError_t launch_planes_t<X, KIND>(int64_t, int64_t, const X*, int64_t,         \
+                                               const float*, Planes, hipStream_t);
+BK_INST_P(float, kBF16x3)
+BK_INST_P(BF16, kBF16x1)
+BK_INST_P(F16, kF16x1)
+#undef BK_INST_P
+#define BK_INST_Y(O, F)                                                                     \
+  template hipError_t launch_plane_product<O, F>(int64_t, int64_t, int64_t, Planes, Planes, \
+                                                 const PlanePairs&, const PlaneEpilogue&,   \
+                                                 O*, int64_t, hipStream_t);
+BK_INST_Y(float, false)
+BK_INST_Y(float, true)
+BK_INST_Y(BF16, false)
+BK_INST_Y(F16, true)
+#undef BK_INST_Y
 #define BK_INST(G)                                                                            \
   template hipError_t launch_matmul_int8_grad<G>(int64_t, int64_t, int64_t, const G*,         \
                                                  int64_t, const int8_t*, int64_t,             \

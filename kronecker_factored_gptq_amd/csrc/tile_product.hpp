@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "launch.hpp"
+
 namespace bk {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -56,12 +58,6 @@ struct MmaF16 {
 struct TileOperand {
   const char* p;
   int64_t ld, plane, rows;
-};
-
-// The plane pairs of a product, smallest terms last.
-struct PlanePairs {
-  int n;
-  unsigned char r[6], c[6];
 };
 
 // The largest row stride (and row length, in bytes) the direct loads take: the
