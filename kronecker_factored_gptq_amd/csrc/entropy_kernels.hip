@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_kernel(
     TileOperand W, TileOperand X, int64_t kbytes, PlanePairs pairs, const int64_t* __restrict__ y,
     int64_t v0, MaxSum* __restrict__ parts, int64_t part0, float* __restrict__ zy, unsigned nr,
     unsigned nc) {
-  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  typedef TileProduct<M, BR, BC, WR, WC> TP;
   extern __shared__ char lds[];
   int tr, tc;
   tile_of(blockIdx.x, nr, nc, tr, tc);
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
     TileOperand W, TileOperand X, int64_t kbytes, PlanePairs pairs, const int64_t* __restrict__ y,
     int64_t V, int64_t v0, const float* __restrict__ lse, float scale, Planes P, Planes Pt,
     unsigned nr, unsigned nc) {
-  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  typedef TileProduct<M, BR, BC, WR, WC> TP;
   constexpr int NP = kPlanes[KIND];
   extern __shared__ char lds[];
   int tr, tc;
@@ -232,7 +232,7 @@ template <class M, int BR, int BC, int WR, int WC, bool ANY>
 static hipError_t start_entropy(const TileOperand& W, const TileOperand& X, int64_t kbytes,
                                 const PlanePairs& pairs, const int64_t* y, int64_t v0,
                                 MaxSum* parts, int64_t& part0, float* zy, hipStream_t s) {
-  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  typedef TileProduct<M, BR, BC, WR, WC> TP;
   auto* k = entropy_kernel<M, BR, BC, WR, WC, ANY>;
   if (TP::kLds > 65536) {
     const hipError_t e =
@@ -251,7 +251,7 @@ static hipError_t start_entropy_diff(const TileOperand& W, const TileOperand& X,
                                      const PlanePairs& pairs, const int64_t* y, int64_t V,
                                      int64_t v0, const float* lse, float scale, Planes P,
                                      Planes Pt, hipStream_t s) {
-  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  typedef TileProduct<M, BR, BC, WR, WC> TP;
   auto* k = entropy_diff_kernel<M, KIND, BR, BC, WR, WC, ANY>;
   if (TP::kLds > 65536) {
     const hipError_t e =

@@ -77,7 +77,7 @@ template <class M, typename O, int BR, int BC, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
     TileOperand R, TileOperand C, int64_t kbytes, PlanePairs pairs, PlaneEpilogue ep,
     O* __restrict__ Y, int64_t ldy, bool vec, unsigned nr, unsigned nc) {
-  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  typedef TileProduct<M, BR, BC, WR, WC> TP;
   extern __shared__ char lds[];
   int tr, tc;
   tile_of(blockIdx.x, nr, nc, tr, tc);
@@ -126,7 +126,7 @@ template <class M, typename O, int BR, int BC, int WR, int WC>
 static hipError_t start_plane_product(const TileOperand& R, const TileOperand& C, int64_t kbytes,
                                       const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,
                                       int64_t ldy, hipStream_t s) {
-  typedef TileProduct<M, BR, BC, WR, WC, 2> TP;
+  typedef TileProduct<M, BR, BC, WR, WC> TP;
   auto* k = plane_product_kernel<M, O, BR, BC, WR, WC>;
   if (TP::kLds > 65536) {
     const hipError_t e =

@@ -68,12 +68,12 @@ hipError_t launch_quantize_tokens(int64_t T, int64_t n, const X* x, int64_t ldx,
 // to the output's type. The tile's rows are channels and its columns tokens,
 // so a lane's four accumulators are four consecutive outputs of one token.
 // ---------------------------------------------------------------------------
-template <typename O, int BR, int BC, int WR, int WC, int STAGES, bool ANY>
+template <typename O, int BR, int BC, int WR, int WC, bool ANY>
 __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
     TileOperand V, TileOperand Xq, int64_t n, const float* __restrict__ sx,
     const float* __restrict__ sv, O* __restrict__ Y, int64_t ldy, bool vec, unsigned nr,
     unsigned nc) {
-  typedef TileProduct<MmaI8, BR, BC, WR, WC, STAGES> TP;
+  typedef TileProduct<MmaI8, BR, BC, WR, WC> TP;
   extern __shared__ char lds[];
   int tr, tc;
   tile_of(blockIdx.x, nr, nc, tr, tc);
@@ -110,13 +110,13 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
              [&](int a, int i, int j, int e) { return (float)a * st[j] * sr[i][e]; });
 }
 
-template <typename O, int BR, int BC, int WR, int WC, int STAGES, bool ANY>
+template <typename O, int BR, int BC, int WR, int WC, bool ANY>
 static hipError_t start_matmul_int8(const TileOperand& V, const TileOperand& X, int64_t n,
                                     const float* sx, const float* sv, O* Y, int64_t ldy,
                                     hipStream_t s) {
-  typedef TileProduct<MmaI8, BR, BC, WR, WC, STAGES> TP;
-  auto* k = matmul_int8_kernel<O, BR, BC, WR, WC, STAGES, ANY>;
-  constexpr int lds = ANY ? 2 * TP::kStage : TP::kLds;
+  typedef TileProduct<MmaI8, BR, BC, WR, WC> TP;
+  auto* k = matmul_int8_kernel<O, BR, BC, WR, WC, ANY>;
+  constexpr int lds = TP::kLds;
   if (lds > 65536) {
     const hipError_t e =
         hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -135,11 +135,11 @@ hipError_t launch_matmul_int8(int64_t T, int64_t m, int64_t n, const int8_t* Xq,
   if (T <= 0 || m <= 0) return hipSuccess;
   const TileOperand V = {(const char*)Vq, ldv, 0, m}, X = {(const char*)Xq, ldx, 0, T};
   const bool direct = tile_direct(V, n) && tile_direct(X, n);
-  if (!direct) return start_matmul_int8<O, 128, 128, 2, 2, 2, true>(V, X, n, sx, sv, Y, ldy, s);
+  if (!direct) return start_matmul_int8<O, 128, 128, 2, 2, true>(V, X, n, sx, sv, Y, ldy, s);
   const int64_t big = ((m + 255) / 256) * ((T + 255) / 256);
   if (big >= 192)
-    return start_matmul_int8<O, 256, 256, 2, 4, 2, false>(V, X, n, sx, sv, Y, ldy, s);
-  return start_matmul_int8<O, 128, 128, 2, 2, 2, false>(V, X, n, sx, sv, Y, ldy, s);
+    return start_matmul_int8<O, 256, 256, 2, 4, false>(V, X, n, sx, sv, Y, ldy, s);
+  return start_matmul_int8<O, 128, 128, 2, 2, false>(V, X, n, sx, sv, Y, ldy, s);
 }
 
 #define BK_INST_Q(X)                                                                        \

@@ -86,50 +86,107 @@ __device__ inline void tile_of(unsigned b, unsigned nr, unsigned nc, int& tr, in
   tc = (int)(first + in % width);
 }
 
-template <class M, int BR, int BC, int WR, int WC, int STAGES>
+// How an operand lies in memory and in LDS: its rows along k (kbytes of k in
+// each), or k-major (k its rows, `ld` apart, its tile's rows side by side).
+template <class M, int BR, int BC, int WR, int WC, bool RK = false, bool CK = false>
 struct TileProduct {
   typedef typename M::acc_t acc_t;
   static constexpr int kWaves = WR * WC;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int FR = BR / WR / 16, FC = BC / WC / 16;
-  static constexpr int kStage = (BR + BC) * kStepBytes;
-  static constexpr int kLds = STAGES * kStage;
+  // LDS is a ring of five slots, each one step of one operand: step s of R in
+  // slot 2 s mod 5, of C in the next. With two whole steps' slots (four) every
+  // load would have to land before the next goes out; the fifth keeps the next
+  // step but one of R in flight meanwhile, and the memory path busy.
+  static constexpr int kSlot = BR * kStepBytes;
+  static constexpr int kLds = 5 * kSlot;
+  static_assert(BR == BC, "one slot size");
   static constexpr int LR = BR * kStepBytes / 1024 / kWaves;  // wave loads per step
   static constexpr int LC = BC * kStepBytes / 1024 / kWaves;
   static_assert(LR * kWaves * 1024 == BR * kStepBytes && LC * kWaves * 1024 == BC * kStepBytes,
                 "a step's bytes divide over the waves");
   static_assert(kWaves % 2 == 0, "the chunk order of a wave's loads does not depend on the load");
+  static_assert(!(RK || CK) || M::kElem == 2, "the transposing reads are of 16-bit elements");
 
   acc_t acc[FR][FC];
+  // both operands for one instruction's k (64 bytes of it)
+  struct Frags {
+    v4i r[FR], c[FC];
+  };
 
   __device__ inline int wave_r() const { return (threadIdx.x >> 6) / WC * (FR * 16); }
   __device__ inline int wave_c() const { return (threadIdx.x >> 6) % WC * (FC * 16); }
 
-  // LDS holds each operand's rows 128 bytes apart; 16-byte chunk q of row r
-  // lies at position q ^ ((r / 2) % 8), so that the 16 rows a fragment reads
-  // at one q fall on different banks. The loads write LDS in lane order, so
-  // each lane fetches the chunk that belongs at its place.
+  // LDS holds a k-contiguous operand's rows 128 bytes apart; 16-byte chunk q of
+  // row r lies at position q ^ ((r / 2) % 8), so that the 16 rows a fragment
+  // reads at one q fall on different banks.
   __device__ static inline int chunk_at(int row, int pos) { return pos ^ ((row >> 1) & 7); }
 
-  // One step's compute from LDS.
-  __device__ inline void compute(const char* lds) {
-    const int lane = threadIdx.x & 63;
-    const int r16 = lane & 15, q = lane >> 4;
-    const char* lr = lds + (wave_r() + r16) * kStepBytes;
-    const char* lc = lds + BR * kStepBytes + (wave_c() + r16) * kStepBytes;
+  // A k-major operand lies k by k, 2 B bytes each. Of a transposing read, four
+  // lanes take 32 bytes of one k, 16 lanes four k, and the next 16 lanes k that
+  // are 8 further; the 32-byte block b of k lies at b ^ swap_at(k), so that 32
+  // lanes cover 256 bytes of banks once.
+  __device__ static inline int swap_at(int k) { return (k & 3) | ((k >> 1) & 4); }
+
+  // Fragment i of the operand whose wave's rows start at row0.
+  template <bool K, int B>
+  __device__ static inline v4i read_one(const char* lds, int row0, int kk, int i) {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+    if (!K)
+      return *(const v4i*)(lds + (row0 + i * 16 + r16) * kStepBytes +
+                           chunk_at(r16, kk * 4 + q) * 16);
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    const int k = 8 * q + (r16 >> 2);  // and 4 further, of 32 kk on
+    const char* a = lds + (kk * 32 + k) * (2 * B) + ((row0 / 16 + i) ^ swap_at(k)) * 32 +
+                    (r16 & 3) * 8;
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(a + 8 * B));
+    const int2 x = __builtin_bit_cast(int2, lo), y = __builtin_bit_cast(int2, hi);
+    return v4i{x.x, x.y, y.x, y.y};
+  }
+  __device__ inline void read(Frags& f, const char* lr, const char* lc, int kk, int g) const {
+    if (g < FC)
+      f.c[g] = read_one<CK, BC>(lc, wave_c(), kk, g);
+    else
+      f.r[g - FC] = read_one<RK, BR>(lr, wave_r(), kk, g - FC);
+  }
+  __device__ inline void read(Frags& f, const char* lr, const char* lc, int kk) const {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int off = chunk_at(r16, kk * 4 + q) * 16;
-      v4i fr[FR], fc[FC];
+    for (int g = 0; g < FR + FC; ++g) read(f, lr, lc, kk, g);
+  }
+  __device__ inline void multiply(const Frags& f, int g) {
+    const int i = g / FC, j = g % FC;
+    acc[i][j] = M::mma(f.r[i], f.c[j], acc[i][j]);
+  }
+  __device__ inline void multiply(const Frags& f) {
 #pragma unroll
-      for (int i = 0; i < FR; ++i) fr[i] = *(const v4i*)(lr + i * 16 * kStepBytes + off);
+    for (int g = 0; g < FR * FC; ++g) multiply(f, g);
+  }
+  // Multiplies `f` while `next` is read, and LOADS wave loads (load(u)) go out.
+  // The order is fixed here: all waves issue their loads at once after a
+  // barrier, and in a row they would keep the matrix units waiting for the
+  // address units; so each goes out with one read and two multiplications.
+  template <int LOADS, typename F>
+  __device__ inline void half_step(const Frags& f, Frags& next, const char* lr, const char* lc,
+                                   int kk, F load) {
+    constexpr int kMma = FR * FC, kReads = FR + FC;
+    constexpr int kPer = kMma >= 2 * kReads ? 2 : 1;
+    int g = 0;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < FC; ++j) fc[j] = *(const v4i*)(lc + j * 16 * kStepBytes + off);
+    for (int u = 0; u < kReads || u < LOADS; ++u) {
+      if (u < kReads) read(next, lr, lc, kk, u);
+      if (u < LOADS) load(u);
 #pragma unroll
-      for (int j = 0; j < FC; ++j)
-#pragma unroll
-        for (int i = 0; i < FR; ++i) acc[i][j] = M::mma(fr[i], fc[j], acc[i][j]);
+      for (int e = 0; e < kPer; ++e, ++g)
+        if (g < kMma) multiply(f, g);
+      __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int e = 0; e < kMma; ++e)
+      if (e >= g) multiply(f, e);
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   __device__ inline void zero() {
@@ -147,81 +204,163 @@ struct TileProduct {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rsrc, (__attribute__((address_space(3))) void*)(uintptr_t)lds, 16, voff, soff, 0, 0);
   }
-  __device__ static inline __amdgpu_buffer_rsrc_t make_rsrc(const char* p, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, bytes, 0x00020000);
+
+  // One operand's loads: a lane's byte offsets for each of a step's NL wave
+  // loads. LDS is written in lane order, so each lane fetches the chunk that
+  // belongs at its place. Rows past the operand's last are read as its last
+  // (their results are not for storing); chunks past the end of k get an
+  // offset past the buffer's end and read as zero, and so do a k-major operand's
+  // chunks past its rows.
+  template <bool K, int B, int NL>
+  struct Loader {
+    const char* p;
+    int64_t plane;
+    int bytes, step;  // of the buffer; from one k step to the next
+    int off[NL];
+    int krow;       // k-major: this lane's k of the first load
+    bool past;      // this lane's chunk is past the end in the last k step
+    int ksteps, k, pair, npairs;  // the next step to load
+    unsigned lds, slot;           // this wave's place in slot 0; the next slot
+    const unsigned char* planes;
+    __amdgpu_buffer_rsrc_t rsrc;
+
+    __device__ inline void init(const TileOperand& o, int64_t row0, int64_t kbytes, int npairs_,
+                                const unsigned char* planes_, unsigned lds_, unsigned slot_) {
+      const int lane = threadIdx.x & 63;
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      const int rows = o.rows - row0 < B ? (int)(o.rows - row0) : B, ld = (int)o.ld;
+      plane = o.plane;
+      ksteps = (int)((kbytes + kStepBytes - 1) / kStepBytes);
+      npairs = npairs_;
+      planes = planes_;
+      lds = lds_ + wave * 1024;
+      slot = slot_;
+      k = pair = 0;
+      if (!K) {
+        p = o.p + row0 * o.ld;
+        bytes = (rows - 1) * ld + (int)kbytes;
+        step = kStepBytes;
+        const int row8 = lane >> 3, chunk = chunk_at((wave & 1) * 8 + row8, lane & 7);
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+          const int r = (j * kWaves + wave) * 8 + row8;
+          off[j] = (r < rows ? r : rows - 1) * ld + chunk * 16;
+        }
+        past = chunk * 16 + (ksteps - 1) * kStepBytes >= (int)kbytes;
+      } else {
+        p = o.p + row0 * 2;
+        const int kn = (int)(kbytes / 2);
+        bytes = (kn - 1) * ld + rows * 2;
+        step = 64 * ld;
+        constexpr int per = B / 8;  // chunks of a k; kLanesK k in a wave load
+        constexpr int lanes_k = 64 / per;
+        krow = lane / per;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+          const int kr = (j * kWaves + wave) * lanes_k + krow, pos = lane % per;
+          const int chunk = ((pos >> 1) ^ swap_at(kr)) * 2 + (pos & 1);
+          off[j] = chunk * 8 < rows ? kr * ld + chunk * 16 : (int)0x80000000;
+        }
+        krow += wave * lanes_k + (ksteps - 1) * 64 - kn;  // >= 0: past the last k
+      }
+      select(planes[0]);
+    }
+    __device__ inline void select(int pl) {
+      rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p + pl * plane), 0, bytes,
+                                               0x00020000);
+    }
+    __device__ inline void load(int j) const {
+      const bool last = k == ksteps - 1;
+      bool cut = last && past;
+      if (K) cut = last && krow + j * kWaves * (64 / (B / 8)) >= 0;
+      load_lds(rsrc, cut ? (int)0x80000000 : off[j], k * step,
+               lds + slot * kSlot + j * kWaves * 1024);
+    }
+    __device__ inline void advance() {
+      slot = slot >= 3 ? slot - 3 : slot + 2;
+      if (++k == ksteps && pair + 1 < npairs) {
+        k = 0;
+        select(planes[++pair]);
+      }
+    }
+  };
+
+  template <int N> __device__ static inline void wait_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
   }
 
-  // D's tile at (r0, c0), operands 16-byte aligned with ld a multiple of 16
-  // (at most kTileMaxLd) and kbytes a multiple of 16. Rows past an operand's
-  // last are read as its last (their results are not for storing); chunks past
-  // kbytes get an offset past the buffer's end and read as zero.
+  // D's tile at (r0, c0); operands as tile_direct wants them, kbytes of k.
   __device__ inline void run(const TileOperand& R, const TileOperand& C, int64_t kbytes,
                              const PlanePairs& pairs, int64_t r0, int64_t c0, char* lds) {
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rows = R.rows - r0 < BR ? (int)(R.rows - r0) : BR;
-    const int cols = C.rows - c0 < BC ? (int)(C.rows - c0) : BC;
-    const int ldr = (int)R.ld, ldc = (int)C.ld;
-    const char* pr = R.p + r0 * R.ld;
-    const char* pc = C.p + c0 * C.ld;
-    const int rbytes = (rows - 1) * ldr + (int)kbytes, cbytes = (cols - 1) * ldc + (int)kbytes;
-    const int row8 = lane >> 3;
-    const int chunk = chunk_at((wave & 1) * 8 + row8, lane & 7);
-    int vr[LR], vc[LC];
+    const int total = (int)((kbytes + kStepBytes - 1) / kStepBytes) * pairs.n;
+    if (total == 0) return;
+    const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+    Loader<RK, BR, LR> lr;
+    Loader<CK, BC, LC> lc;
+    lr.init(R, r0, kbytes, pairs.n, pairs.r, base, 0);
+    lc.init(C, c0, kbytes, pairs.n, pairs.c, base, 1);
+    auto load_r = [&]() {
 #pragma unroll
-    for (int j = 0; j < LR; ++j) {
-      const int r = (j * kWaves + wave) * 8 + row8;
-      vr[j] = (r < rows ? r : rows - 1) * ldr + chunk * 16;
-    }
-#pragma unroll
-    for (int j = 0; j < LC; ++j) {
-      const int r = (j * kWaves + wave) * 8 + row8;
-      vc[j] = (r < cols ? r : cols - 1) * ldc + chunk * 16;
-    }
-    const unsigned lbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-
-    const int ksteps = (int)((kbytes + kStepBytes - 1) / kStepBytes);
-    const int total = ksteps * pairs.n;
-    const bool past = chunk * 16 + (int64_t)(ksteps - 1) * kStepBytes >= kbytes;
-    int lk = 0, lp = 0, lbuf = 0;  // the next step to load: k step, pair, buffer
-    __amdgpu_buffer_rsrc_t rr = make_rsrc(pr + pairs.r[0] * R.plane, rbytes);
-    __amdgpu_buffer_rsrc_t rc = make_rsrc(pc + pairs.c[0] * C.plane, cbytes);
-    auto load = [&]() {
-      const int soff = lk * kStepBytes;
-      const unsigned lb = lbase + lbuf * kStage + wave * 1024;
-      const bool cut = past && lk == ksteps - 1;
-#pragma unroll
-      for (int j = 0; j < LR; ++j)
-        load_lds(rr, cut ? (int)0x80000000 : vr[j], soff, lb + j * kWaves * 1024);
-#pragma unroll
-      for (int j = 0; j < LC; ++j)
-        load_lds(rc, cut ? (int)0x80000000 : vc[j], soff,
-                 lb + BR * kStepBytes + j * kWaves * 1024);
-      lbuf = lbuf + 1 == STAGES ? 0 : lbuf + 1;
-      if (++lk == ksteps && lp + 1 < pairs.n) {
-        lk = 0;
-        ++lp;
-        rr = make_rsrc(pr + pairs.r[lp] * R.plane, rbytes);
-        rc = make_rsrc(pc + pairs.c[lp] * C.plane, cbytes);
-      }
+      for (int u = 0; u < LR; ++u) lr.load(u);
+      lr.advance();
     };
-
+    auto load_c = [&]() {
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-      if (s < total) load();
-    int buf = 0;
-    for (int s = 0; s < total; ++s) {
-      // this step's bytes have landed (the steps after it may be in flight),
-      // and every wave is done with the buffer that the next load fills
-      if (s + STAGES - 1 <= total)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((STAGES - 2) * (LR + LC))
-                     : "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      if (s + STAGES - 1 < total) load();
-      compute(lds + buf * kStage);
-      buf = buf + 1 == STAGES ? 0 : buf + 1;
+      for (int u = 0; u < LC; ++u) lc.load(u);
+      lc.advance();
+    };
+    auto none = [](int) {};
+
+    load_r();
+    load_c();
+    if (total > 1) {
+      load_r();
+      load_c();
     }
+    if (total > 2) load_r();
+    if (total > 2)
+      wait_barrier<2 * LR + LC>();
+    else
+      wait_barrier<0>();
+    // A step's second half is multiplied while the next step's first half is
+    // read from LDS, and its first half while its second half is read; in
+    // between, when all waves have read the step, its slots are loaded anew: with C
+    // of the next step but one and R of the one after.
+    unsigned slot = 0;  // of this step's R
+    const char *pr = lds, *pc = lds + kSlot;
+    auto next_slots = [&]() {
+      slot = slot >= 3 ? slot - 3 : slot + 2;
+      pr = lds + slot * kSlot;
+      pc = slot == 4 ? lds : pr + kSlot;
+    };
+    Frags a, b;
+    read(a, pr, pc, 0);
+    int s = 0;
+    for (; s < total - 3; ++s) {
+      half_step<0>(a, b, pr, pc, 1, none);
+      wait_barrier<LR>();  // the next step has landed, R of the one after may be in flight
+      next_slots();
+      half_step<LR + LC>(b, a, pr, pc, 0, [&](int u) {
+        if (u < LC)
+          lc.load(u);
+        else
+          lr.load(u - LC);
+      });
+      lc.advance();
+      lr.advance();
+    }
+    for (; s < total - 1; ++s) {
+      half_step<0>(a, b, pr, pc, 1, none);
+      if (s == total - 3)
+        wait_barrier<LR>();
+      else
+        wait_barrier<0>();
+      next_slots();
+      if (s == total - 3) load_c();  // the last step's
+      half_step<0>(b, a, pr, pc, 0, none);
+    }
+    half_step<0>(a, b, pr, pc, 1, none);
+    multiply(b);
   }
 
   // The same for operands of any alignment, stride and k (M::kElem-sized
@@ -287,8 +426,13 @@ struct TileProduct {
     __syncthreads();
     for (int s = 0; s < ksteps; ++s) {
       if (s + 1 < ksteps) gload((int64_t)(s + 1) * kStepBytes);
-      compute(lds + (s & 1) * kStage);
-      if (s + 1 < ksteps) sstore(lds + ((s + 1) & 1) * kStage);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        Frags f;
+        read(f, lds + (s & 1) * 2 * kSlot, lds + ((s & 1) * 2 + 1) * kSlot, kk);
+        multiply(f);
+      }
+      if (s + 1 < ksteps) sstore(lds + ((s + 1) & 1) * 2 * kSlot);
       __syncthreads();
     }
   }
