@@ -164,28 +164,28 @@ struct TileProduct {
     for (int g = 0; g < FR * FC; ++g) multiply(f, g);
   }
   // Multiplies `f` while `next` is read, and LOADS wave loads (load(u)) go out.
-  // The order is fixed here: all waves issue their loads at once after a
-  // barrier, and in a row they would keep the matrix units waiting for the
-  // address units; so each goes out with one read and two multiplications.
+  // The order is fixed here: one LDS read to two multiplications, and the loads
+  // evenly among all of them. The address units take 16 cycles for a wave load
+  // and all waves issue theirs in the same half step; closer together they
+  // would hold up the multiplications behind them.
   template <int LOADS, typename F>
   __device__ inline void half_step(const Frags& f, Frags& next, const char* lr, const char* lc,
                                    int kk, F load) {
     constexpr int kMma = FR * FC, kReads = FR + FC;
     constexpr int kPer = kMma >= 2 * kReads ? 2 : 1;
-    int g = 0;
+    constexpr int kEvery = LOADS ? kMma / (LOADS ? LOADS : 1) : kMma + 1;
+    static_assert(kEvery >= 1, "a multiplication to each load");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < kReads || u < LOADS; ++u) {
-      if (u < kReads) read(next, lr, lc, kk, u);
-      if (u < LOADS) load(u);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e, ++g)
-        if (g < kMma) multiply(f, g);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int g = 0; g < kMma; ++g) {
+      if (g % kPer == 0 && g / kPer < kReads) read(next, lr, lc, kk, g / kPer);
+      if (g % kEvery == 0 && g / kEvery < LOADS) load(g / kEvery);
+      multiply(f, g);
+      if ((g + 1) % kPer == 0) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int e = 0; e < kMma; ++e)
-      if (e >= g) multiply(f, e);
+    for (int u = 0; u < kReads; ++u)
+      if (u * kPer >= kMma) read(next, lr, lc, kk, u);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -323,9 +323,9 @@ struct TileProduct {
     else
       wait_barrier<0>();
     // A step's second half is multiplied while the next step's first half is
-    // read from LDS, and its first half while its second half is read; in
-    // between, when all waves have read the step, its slots are loaded anew: with C
-    // of the next step but one and R of the one after.
+    // read from LDS, and its first half while its second half is read. In
+    // between all waves have read the step, and its slots are loaded anew: with C
+    // of the next step but one in this half, R of the one after in the next.
     unsigned slot = 0;  // of this step's R
     const char *pr = lds, *pc = lds + kSlot;
     auto next_slots = [&]() {
@@ -335,22 +335,19 @@ struct TileProduct {
     };
     Frags a, b;
     read(a, pr, pc, 0);
+    auto next_r = [&](int u) { lr.load(u); };
+    auto next_c = [&](int u) { lc.load(u); };
     int s = 0;
+    half_step<0>(a, b, pr, pc, 1, none);
     for (; s < total - 3; ++s) {
-      half_step<0>(a, b, pr, pc, 1, none);
       wait_barrier<LR>();  // the next step has landed, R of the one after may be in flight
       next_slots();
-      half_step<LR + LC>(b, a, pr, pc, 0, [&](int u) {
-        if (u < LC)
-          lc.load(u);
-        else
-          lr.load(u - LC);
-      });
+      half_step<LC>(b, a, pr, pc, 0, next_c);
       lc.advance();
+      half_step<LR>(a, b, pr, pc, 1, next_r);
       lr.advance();
     }
     for (; s < total - 1; ++s) {
-      half_step<0>(a, b, pr, pc, 1, none);
       if (s == total - 3)
         wait_barrier<LR>();
       else
@@ -358,8 +355,8 @@ struct TileProduct {
       next_slots();
       if (s == total - 3) load_c();  // the last step's
       half_step<0>(b, a, pr, pc, 0, none);
+      half_step<0>(a, b, pr, pc, 1, none);
     }
-    half_step<0>(a, b, pr, pc, 1, none);
     multiply(b);
   }
 
