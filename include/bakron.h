@@ -490,9 +490,9 @@ int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n,
  *   gtype  the type of G (T x m, ldg >= m) and of dX (T x n, ldx >= n): F32,
  *          BF16 or F16. Vq m x n int8 (ldv >= n); sv float32 length m and
  *          channel float32 length n, each nullable (all 1).
- * G[t][i] sv[i] is rounded to float32 and then kept with 8 bits for BF16 (an
- * error of 2^-9 to 2^-8 a term, as the output's own), 16 for F16, all 24 for
- * F32; products are exact, sums float32, one rounding to gtype.
+ * G[t][i] sv[i] is rounded to float32 and then, for BF16 and F16, to 11 bits
+ * (down to 2^-28 of the token's largest, and to 2^-39 of it below); F32 keeps
+ * all 24. Products are exact, sums float32, one rounding to gtype.
  * dX must not overlap the inputs (BAKRON_EINVAL). m, n <= 2^20. Asynchronous,
  * deterministic.
  * ------------------------------------------------------------------------ */

@@ -45,9 +45,8 @@ inline bool tiles_ok(int64_t a, int64_t b) {
 constexpr size_t kAlign = 256;
 
 // Sizes of the input gradient: rows of planes short enough for the tile
-// product's 32-bit offsets, and a grid of 64 x 64 transposes.
+// product's 32-bit offsets.
 constexpr int64_t kMaxPlaneCols = (int64_t)1 << 20;
-inline int grad_planes(int t) { return t == BAKRON_F32 ? 3 : t == BAKRON_BF16 ? 1 : 2; }
 inline bool grad_sizes_ok(int t, int64_t T, int64_t m, int64_t n) {
   return type_ok(t) && T >= 0 && m >= 0 && n >= 0 && T <= INT_MAX && m <= kMaxPlaneCols &&
          n <= kMaxPlaneCols && T * (m + 64) <= ((int64_t)1 << 41);
@@ -105,7 +104,7 @@ int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n, const int8_t*
 
 size_t bakron_matmul_int8_grad_workspace_bytes(int gtype, int64_t T, int64_t m, int64_t n) {
   if (!grad_sizes_ok(gtype, T, m, n)) return 0;
-  return matmul_int8_grad_bytes(grad_planes(gtype), T, m, n) + kAlign;
+  return matmul_int8_grad_bytes((int)type_size(gtype), T, m, n) + kAlign;
 }
 
 int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n, const void* G, int64_t ldg,
@@ -120,7 +119,7 @@ int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n, const vo
     return BAKRON_EINVAL;
   if ((uintptr_t)sv % 4 || (uintptr_t)channel % 4) return BAKRON_EINVAL;
   if (!workspace || (uintptr_t)workspace % kAlign ||
-      workspace_bytes < matmul_int8_grad_bytes(grad_planes(gtype), T, m, n))
+      workspace_bytes < matmul_int8_grad_bytes((int)type_size(gtype), T, m, n))
     return BAKRON_EINVAL;
   if (overlap(dX, T, n, ldx, es, G, T, m, ldg, es) || overlap(dX, T, n, ldx, es, Vq, m, n, ldv, 1) ||
       overlap(dX, T, n, ldx, es, sv, 1, m, m, 4) || overlap(dX, T, n, ldx, es, channel, 1, n, n, 4))

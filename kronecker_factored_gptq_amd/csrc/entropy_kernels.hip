@@ -8,12 +8,14 @@
 //
 // Gradient: with D[t][v] = exp(z - lse_t) - [v = y_t] (0 for a token without a
 // target), dX = g (.) (D W) and dW = D^T (g (.) X). The vocabulary goes by in
-// pieces: a piece's logits are formed again, D is written as 16-bit planes in
-// both orders, and the two products are formed from it; dX is summed over the
-// pieces in float32.
+// pieces: a piece's logits are formed again, D is written as 16-bit planes, and
+// the two products are formed from it, W, X and (for dW) D read k-major; dX is
+// summed over the pieces in float32.
 //
 // float32 operands are three bfloat16 planes each (exact), and a product the six
 // pairs of planes whose terms reach float32's precision.
+#include <initializer_list>
+
 #include "launch.hpp"
 #include "tile_product.hpp"
 
@@ -45,8 +47,8 @@ template <> struct Kind<F16> {
 template <typename X> constexpr float dscale() { return Kind<X>::f16 ? 16384.0f : 1.0f; }
 
 template <typename X> inline PlanePairs pairs_of() {
-  if (kPlanes[Kind<X>::split] == 3) return {6, {0, 0, 1, 0, 2, 1}, {0, 1, 0, 2, 0, 1}};
-  return {1, {0}, {0}};
+  if (kPlanes[Kind<X>::split] == 3) return {6, 0x120100, 0x102010};
+  return {1, 0, 0};
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -84,7 +86,7 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_kernel(
   if (ANY)
     tp.run_any(W, X, kbytes, r0, c0, lds);
   else
-    tp.run(W, X, kbytes, pairs, r0, c0, lds);
+    tp.run(W, X, kbytes, pairs, r0, c0, 0, TP::steps(kbytes, pairs), lds);
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int64_t rb = r0 + tp.wave_r(), T = X.rows;
   // rows of this lane's that are W's: 16 i + 4 q + e < left
@@ -172,13 +174,13 @@ __global__ __launch_bounds__(1024) void entropy_weights_kernel(
   for (int64_t t = threadIdx.x; t < T; t += 1024) rel[t] = m == 0 ? 0.0f : w[t] / mx;
 }
 
-// D's planes of a piece, in both orders (each nullable): P rows are tokens, Pt
-// rows the piece's. Written up to the planes' padding, with zeros there.
+// D's planes of a piece, rows the tokens, written up to the planes' padding, with
+// zeros there.
 template <class M, int KIND, int BR, int BC, int WR, int WC, bool ANY>
 __global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
     TileOperand W, TileOperand X, int64_t kbytes, PlanePairs pairs, const int64_t* __restrict__ y,
-    int64_t V, int64_t v0, const float* __restrict__ lse, float scale, Planes P, Planes Pt,
-    unsigned nr, unsigned nc) {
+    int64_t V, int64_t v0, const float* __restrict__ lse, float scale, Planes P, unsigned nr,
+    unsigned nc) {
   typedef TileProduct<M, BR, BC, WR, WC> TP;
   constexpr int NP = kPlanes[KIND];
   extern __shared__ char lds[];
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
   if (ANY)
     tp.run_any(W, X, kbytes, r0, c0, lds);
   else
-    tp.run(W, X, kbytes, pairs, r0, c0, lds);
+    tp.run(W, X, kbytes, pairs, r0, c0, 0, TP::steps(kbytes, pairs), lds);
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int64_t T = X.rows;
 #pragma unroll
@@ -214,16 +216,9 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
         for (int p = 0; p < NP; ++p) w[p][e] = k[p];
       }
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        if (P.w && t < T && r * 2 < P.ld)
+      for (int p = 0; p < NP; ++p)
+        if (t < T && r * 2 < P.ld)
           *(uint2*)(P.w + p * P.plane + t * P.ld + r * 2) = __builtin_bit_cast(uint2, w[p]);
-        if (Pt.w && t * 2 < Pt.ld) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r + e < W.rows)
-              *(unsigned short*)(Pt.w + p * Pt.plane + (r + e) * Pt.ld + t * 2) = w[p][e];
-        }
-      }
     }
   }
 }
@@ -250,7 +245,7 @@ template <class M, int KIND, int BR, int BC, int WR, int WC, bool ANY>
 static hipError_t start_entropy_diff(const TileOperand& W, const TileOperand& X, int64_t kbytes,
                                      const PlanePairs& pairs, const int64_t* y, int64_t V,
                                      int64_t v0, const float* lse, float scale, Planes P,
-                                     Planes Pt, hipStream_t s) {
+                                     hipStream_t s) {
   typedef TileProduct<M, BR, BC, WR, WC> TP;
   auto* k = entropy_diff_kernel<M, KIND, BR, BC, WR, WC, ANY>;
   if (TP::kLds > 65536) {
@@ -260,7 +255,7 @@ static hipError_t start_entropy_diff(const TileOperand& W, const TileOperand& X,
   }
   const int64_t nr = (W.rows + BR - 1) / BR, nc = (X.rows + BC - 1) / BC;
   hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc)), dim3(TP::kThreads), TP::kLds, s, W, X, kbytes,
-                     pairs, y, V, v0, lse, scale, P, Pt, (unsigned)nr, (unsigned)nc);
+                     pairs, y, V, v0, lse, scale, P, (unsigned)nr, (unsigned)nc);
   return hipGetLastError();
 }
 
@@ -272,8 +267,7 @@ static int64_t plane_piece(int64_t d, int64_t V) {
   if (p < 256) p = 256;
   return p < V ? p : V;
 }
-// Columns of D held at once: 256 MiB in each order, small enough for the
-// last-level cache to serve the products that read them.
+// Columns of D held at once: 256 MiB, what the last-level cache holds.
 static int64_t diff_piece(int es, int64_t T, int64_t d, int64_t V) {
   const int64_t per = 2 * T * (es == 4 ? 3 : 1);
   int64_t p = per ? ((int64_t)256 << 20) / per / 256 * 256 : V;
@@ -303,7 +297,7 @@ size_t entropy_bytes(int es, int64_t T, int64_t d, int64_t V) {
 }
 
 struct GradLayout {
-  size_t w, rel, top, xp, xt, wp, wt, p, pt, acc, total;
+  size_t w, rel, top, xp, xs, wp, p, acc, parts, total;
   int64_t piece, ldacc;
 };
 static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
@@ -315,13 +309,16 @@ static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
   L.rel = L.w + up256((size_t)T * 4);
   L.top = L.rel + up256((size_t)T * 4);
   L.xp = L.top + 256;
-  L.xt = L.xp + (es == 4 ? (size_t)(3 * T * plane_ld(d)) : 0);
-  L.wp = L.xt + (size_t)(np * d * plane_ld(T));
-  L.wt = L.wp + (es == 4 ? (size_t)(3 * L.piece * plane_ld(d)) : 0);
-  L.p = L.wt + (size_t)(np * d * plane_ld(L.piece));
-  L.pt = L.p + (size_t)(np * T * plane_ld(L.piece));
-  L.acc = L.pt + (size_t)(np * L.piece * plane_ld(T));
-  L.total = L.acc + (L.piece < V ? up256((size_t)(T * L.ldacc) * 4) : 0);
+  L.xs = L.xp + (es == 4 ? up256((size_t)(3 * T * plane_ld(d))) : 0);
+  L.wp = L.xs + up256((size_t)(np * T * plane_ld(d)));
+  L.p = L.wp + up256((size_t)(np * L.piece * plane_ld(d)));
+  L.acc = L.p + up256((size_t)(np * T * plane_ld(L.piece)));
+  L.parts = L.acc + (L.piece < V ? up256((size_t)(T * L.ldacc) * 4) : 0);
+  // both products, and dW's of the last, shorter piece
+  size_t most = plane_product_bytes(d, T);
+  for (int64_t rows : {L.piece, L.piece ? V % L.piece : 0})
+    if (rows && plane_product_bytes(d, rows) > most) most = plane_product_bytes(d, rows);
+  L.total = L.parts + most;
   return L;
 }
 size_t entropy_grad_bytes(int es, int64_t T, int64_t d, int64_t V) {
@@ -344,23 +341,23 @@ hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t l
   int64_t nparts = 0;
   hipError_t e;
   constexpr bool split = sizeof(X) == 4;
-  TileOperand xo = {(const char*)x, ldx * (int64_t)sizeof(X), 0, T};
+  TileOperand xo = {(const char*)x, ldx * (int64_t)sizeof(X), 0, T, 0};
   int64_t kbytes = d * (int64_t)sizeof(X), piece = V;
   if (split) {
     const Planes p = {b + L.xp, plane_ld(d), T * plane_ld(d)};
-    if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, p, s)) != hipSuccess) return e;
-    xo = {p.w, p.ld, p.plane, T};
+    if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, nullptr, p, s)) != hipSuccess) return e;
+    xo = {p.w, p.ld, p.plane, T, 0};
     kbytes = (d + 7) / 8 * 16;
     piece = plane_piece(d, V);
   }
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
     const int64_t rows = V - v0 < piece ? V - v0 : piece;
-    TileOperand wo = {(const char*)(w + v0 * ldw), ldw * (int64_t)sizeof(X), 0, rows};
+    TileOperand wo = {(const char*)(w + v0 * ldw), ldw * (int64_t)sizeof(X), 0, rows, 0};
     if (split) {
       const Planes p = {b + L.wp, plane_ld(d), rows * plane_ld(d)};
-      if ((e = launch_planes<X, K::split>(rows, d, w + v0 * ldw, ldw, nullptr, p, s)) != hipSuccess)
+      if ((e = launch_planes<X, K::split>(rows, d, w + v0 * ldw, ldw, nullptr, nullptr, p, s)) != hipSuccess)
         return e;
-      wo = {p.w, p.ld, p.plane, rows};
+      wo = {p.w, p.ld, p.plane, rows, 0};
     }
     if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
       e = start_entropy<M, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
@@ -384,68 +381,74 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
   if (T <= 0) {  // no tokens: dW is zero, an empty sum
     const Planes none = {(char*)ws, 0, 0};
     const PlaneEpilogue ep = {nullptr, nullptr, nullptr, 1.0f, nullptr, 0};
-    return dW ? launch_plane_product<X, K::f16>(d, V, 0, none, none, pairs_of<X>(), ep, dW, lddw, s)
+    return dW ? launch_plane_product<X, K::f16, true>(d, V, 0, none, none, pairs_of<X>(), ep, dW,
+                                                      lddw, nullptr, s)
               : hipSuccess;
   }
   const GradLayout L = grad_layout(sizeof(X), T, d, V);
   char* b = (char*)ws;
   float *wt = (float*)(b + L.w), *rel = (float*)(b + L.rel), *top = (float*)(b + L.top);
+  float *acc = (float*)(b + L.acc), *parts = (float*)(b + L.parts);
   const PlanePairs pairs = pairs_of<X>();
   constexpr bool split = sizeof(X) == 4;
   constexpr int64_t es = sizeof(X);
   hipLaunchKernelGGL(entropy_weights_kernel, dim3(1), dim3(1024), 0, s, T, V, y, g, wt, rel, top);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  TileOperand xo = {(const char*)x, ldx * es, 0, T};
+  TileOperand xo = {(const char*)x, ldx * es, 0, T, 0};
   int64_t kbytes = d * es;
   if (split) {
     const Planes p = {b + L.xp, plane_ld(d), T * plane_ld(d)};
-    if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, p, s)) != hipSuccess) return e;
-    xo = {p.w, p.ld, p.plane, T};
+    if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, nullptr, p, s)) != hipSuccess)
+      return e;
+    xo = {p.w, p.ld, p.plane, T, 0};
     kbytes = (d + 7) / 8 * 16;
   }
-  const Planes xt = {b + L.xt, plane_ld(T), d * plane_ld(T)};
-  if (dW && (e = launch_planes_t<X, K::split>(T, d, x, ldx, rel, xt, s)) != hipSuccess) return e;
-  float* acc = (float*)(b + L.acc);
+  const Planes xs = {b + L.xs, plane_ld(d), T * plane_ld(d)};
+  if (dW && (e = launch_planes<X, K::split>(T, d, x, ldx, rel, nullptr, xs, s)) != hipSuccess)
+    return e;
   for (int64_t v0 = 0; v0 < V; v0 += L.piece) {
     const int64_t rows = V - v0 < L.piece ? V - v0 : L.piece;
     const X* wv = w + v0 * ldw;
-    TileOperand wo = {(const char*)wv, ldw * es, 0, rows};
-    if (split) {
-      const Planes p = {b + L.wp, plane_ld(d), rows * plane_ld(d)};
-      if ((e = launch_planes<X, K::split>(rows, d, wv, ldw, nullptr, p, s)) != hipSuccess) return e;
-      wo = {p.w, p.ld, p.plane, rows};
+    // W's piece: as it is where the direct loads can take it, along d for the
+    // logits and k-major for dX, else as planes
+    TileOperand wo = {(const char*)wv, ldw * es, 0, rows, 0};
+    const bool direct = !split && tile_direct(wo, kbytes);
+    Planes wp = {(char*)const_cast<X*>(wv), ldw * es, 0};
+    if (!direct && (split || dX)) {
+      wp = {b + L.wp, plane_ld(d), rows * plane_ld(d)};
+      if ((e = launch_planes<X, K::split>(rows, d, wv, ldw, nullptr, nullptr, wp, s)) != hipSuccess)
+        return e;
+      if (split) wo = {wp.w, wp.ld, wp.plane, rows, 0};
     }
-    const Planes P = {dX ? b + L.p : nullptr, plane_ld(rows), T * plane_ld(rows)};
-    const Planes Pt = {dW ? b + L.pt : nullptr, plane_ld(T), rows * plane_ld(T)};
+    const Planes P = {b + L.p, plane_ld(rows), T * plane_ld(rows)};
     if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
       e = start_entropy_diff<M, K::split, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, V, v0, lse,
-                                                                dscale<X>(), P, Pt, s);
+                                                                dscale<X>(), P, s);
     else if (((rows + 255) / 256) * ((T + 255) / 256) >= 192)
       e = start_entropy_diff<M, K::split, 256, 256, 2, 4, false>(wo, xo, kbytes, pairs, y, V, v0,
-                                                                 lse, dscale<X>(), P, Pt, s);
+                                                                 lse, dscale<X>(), P, s);
     else
       e = start_entropy_diff<M, K::split, 128, 128, 2, 2, false>(wo, xo, kbytes, pairs, y, V, v0,
-                                                                 lse, dscale<X>(), P, Pt, s);
+                                                                 lse, dscale<X>(), P, s);
     if (e != hipSuccess) return e;
     if (dX) {
-      const Planes wtp = {b + L.wt, plane_ld(rows), d * plane_ld(rows)};
-      if ((e = launch_planes_t<X, K::split>(rows, d, wv, ldw, nullptr, wtp, s)) != hipSuccess)
-        return e;
       const bool last = v0 + rows == V;
       const float* prev = v0 > 0 ? acc : nullptr;
       if (last) {
         const PlaneEpilogue ep = {nullptr, wt, nullptr, 1.0f / dscale<X>(), prev, L.ldacc};
-        e = launch_plane_product<X, K::f16>(d, T, rows, wtp, P, pairs, ep, dX, lddx, s);
+        e = launch_plane_product<X, K::f16, false>(d, T, rows, wp, P, pairs, ep, dX, lddx, parts, s);
       } else {
         const PlaneEpilogue ep = {nullptr, nullptr, nullptr, 1.0f, prev, L.ldacc};
-        e = launch_plane_product<float, K::f16>(d, T, rows, wtp, P, pairs, ep, acc, L.ldacc, s);
+        e = launch_plane_product<float, K::f16, false>(d, T, rows, wp, P, pairs, ep, acc, L.ldacc,
+                                                       parts, s);
       }
       if (e != hipSuccess) return e;
     }
     if (dW) {
       const PlaneEpilogue ep = {nullptr, nullptr, top, 1.0f / dscale<X>(), nullptr, 0};
-      e = launch_plane_product<X, K::f16>(d, rows, T, xt, Pt, pairs, ep, dW + v0 * lddw, lddw, s);
+      e = launch_plane_product<X, K::f16, true>(d, rows, T, xs, P, pairs, ep, dW + v0 * lddw, lddw,
+                                                parts, s);
       if (e != hipSuccess) return e;
     }
   }

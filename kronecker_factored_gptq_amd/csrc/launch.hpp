@@ -295,19 +295,16 @@ struct Planes {
   char* w;
   int64_t ld, plane;
 };
-// out = planes (KIND, a Split) of X (rows x cols) times col_scale (nullable).
+// out = planes (KIND, a Split) of X (rows x cols) times row_scale (nullable; a row
+// whose scale is 0 gives 0 whatever it holds) and col_scale (nullable).
 template <typename X, int KIND>
 hipError_t launch_planes(int64_t rows, int64_t cols, const X* x, int64_t ldx,
-                         const float* col_scale, Planes out, hipStream_t s);
-// out = planes of the transpose of X (rows x cols) times row_scale (nullable; a
-// row whose scale is 0 gives 0 whatever it holds): cols x rows.
-template <typename X, int KIND>
-hipError_t launch_planes_t(int64_t rows, int64_t cols, const X* x, int64_t ldx,
-                           const float* row_scale, Planes out, hipStream_t s);
-// The plane pairs of a product: planes r[i] and c[i] of its two operands.
+                         const float* row_scale, const float* col_scale, Planes out, hipStream_t s);
+// The plane pairs of a product: planes (r >> 4 i) % 16 and (c >> 4 i) % 16 of its
+// two operands, i < n <= 8.
 struct PlanePairs {
   int n;
-  unsigned char r[6], c[6];
+  unsigned r, c;
 };
 // Y[c][r] = (sum + prev[c][r]) * row_scale[r] * alpha * beta * col_scale[c];
 // every pointer nullable. prev has rows of whole groups of four, 16-byte
@@ -319,15 +316,19 @@ struct PlaneEpilogue {
   int64_t ldprev;
 };
 // The sum over the plane pairs of R[r][k] C[c][k], k < K, for R's rows r < M and
-// C's rows c < N. F16P: the planes are float16 (else bfloat16).
-template <typename O, bool F16P>
+// C's rows c < N, the planes float16 (F16P) or bfloat16. R is k-major (K rows of
+// M), C too with CK; else C's rows are along k and zero from K to a multiple of 8.
+// `parts` holds plane_product_bytes(M, N) for the sums of a k that is split
+// over workgroups.
+size_t plane_product_bytes(int64_t M, int64_t N);
+template <typename O, bool F16P, bool CK>
 hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C,
                                 const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,
-                                int64_t ldy, hipStream_t s);
+                                int64_t ldy, float* parts, hipStream_t s);
 
 // dX (T x n) = channel (.) ((G sv) Vq); sv and channel nullable. ws holds
-// matmul_int8_grad_bytes(planes of G's type: float 3, BF16 1, F16 2).
-size_t matmul_int8_grad_bytes(int planes, int64_t T, int64_t m, int64_t n);
+// matmul_int8_grad_bytes(size of G's elements).
+size_t matmul_int8_grad_bytes(int es, int64_t T, int64_t m, int64_t n);
 template <typename G>
 hipError_t launch_matmul_int8_grad(int64_t T, int64_t m, int64_t n, const G* g, int64_t ldg,
                                    const int8_t* Vq, int64_t ldv, const float* sv,

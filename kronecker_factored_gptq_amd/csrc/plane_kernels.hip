@@ -11,24 +11,62 @@ struct I8 {
 };
 __device__ inline float to_f32(I8 x) { return (float)x.v; }
 
+namespace {
+
+// Eight elements of a row from column c on, zero past `cols`; `vec`: whole
+// groups of eight are aligned to their size (at most 16 bytes).
+template <typename X>
+__device__ inline void load8(const X* row, int64_t c, int64_t cols, bool vec, float* v) {
+  constexpr int kBytes = 8 * sizeof(X) < 16 ? 8 * sizeof(X) : 16;
+  constexpr int kPer = kBytes / sizeof(X);
+  if (vec && c + 8 <= cols) {
+    X t[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer)
+      __builtin_memcpy(t + i, __builtin_assume_aligned(row + c + i, kBytes), kBytes);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f32(row[c + i]) : 0.0f;
+  }
+}
+template <typename X>
+inline bool load8_ok(const X* x, int64_t ld) {
+  constexpr int kBytes = 8 * sizeof(X) < 16 ? 8 * sizeof(X) : 16;
+  return (uintptr_t)x % kBytes == 0 && ld * sizeof(X) % kBytes == 0;
+}
+
+}  // namespace
+
 // Eight columns of one row per thread, one 16-byte store per plane.
 template <typename X, int KIND>
 __global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
                                                      const X* __restrict__ x, int64_t ldx,
-                                                     const float* __restrict__ cs, Planes out) {
+                                                     const float* __restrict__ rs,
+                                                     const float* __restrict__ cs, Planes out,
+                                                     bool vec) {
   constexpr int NP = kPlanes[KIND];
   const int64_t per = out.ld / 16;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= rows * per) return;
   const int64_t r = at / per, c0 = (at - r * per) * 8;
+  float v[8];
+  load8(x + r * ldx, c0, cols, vec, v);
+  if (cs) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= cs[c0 + e < cols ? c0 + e : cols - 1];
+  }
+  if (rs) {
+    const float f = rs[r];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = f == 0.0f ? 0.0f : v[e] * f;
+  }
   unsigned short w[NP][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int64_t c = c0 + e;
-    float v = 0.0f;
-    if (c < cols) v = to_f32(x[r * ldx + c]) * (cs ? cs[c] : 1.0f);
     unsigned short t[NP];
-    split16<KIND>(v, t);
+    split16<KIND>(v[e], t);
 #pragma unroll
     for (int p = 0; p < NP; ++p) w[p][e] = t[p];
   }
@@ -37,56 +75,46 @@ __global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
     *(v4i*)(out.w + p * out.plane + r * out.ld + c0 * 2) = __builtin_bit_cast(v4i, w[p]);
 }
 
-// The transpose by tiles of 64 x 64 through LDS, both sides in full lines.
 template <typename X, int KIND>
-__global__ __launch_bounds__(256) void planes_t_kernel(int64_t rows, int64_t cols,
-                                                       const X* __restrict__ x, int64_t ldx,
-                                                       const float* __restrict__ rs, Planes out) {
-  constexpr int NP = kPlanes[KIND];
-  __shared__ float tile[64][65];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const int64_t r = r0 + u * 4 + ty, c = c0 + tx;
-    float v = r < rows && c < cols ? to_f32(x[r * ldx + c]) : 0.0f;
-    if (rs && r < rows) v = rs[r] == 0.0f ? 0.0f : v * rs[r];
-    tile[u * 4 + ty][tx] = v;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int e = u * 256 + threadIdx.x, c = e >> 3, k = (e & 7) * 8;
-    if (c0 + c >= cols) continue;
-    unsigned short w[NP][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      unsigned short t[NP];
-      split16<KIND>(tile[k + i][c], t);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) w[p][i] = t[p];
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-      *(v4i*)(out.w + p * out.plane + (c0 + c) * out.ld + (r0 + k) * 2) =
-          __builtin_bit_cast(v4i, w[p]);
-  }
+hipError_t launch_planes(int64_t rows, int64_t cols, const X* x, int64_t ldx,
+                         const float* row_scale, const float* col_scale, Planes out,
+                         hipStream_t s) {
+  const int64_t n = rows * (out.ld / 16);
+  if (n <= 0) return hipSuccess;
+  hipLaunchKernelGGL((planes_kernel<X, KIND>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                     rows, cols, x, ldx, row_scale, col_scale, out, load8_ok(x, ldx));
+  return hipGetLastError();
 }
 
-template <class M, typename O, int BR, int BC, int WR, int WC>
+// ---- products -----------------------------------------------------------------
+
+// Workgroup b: tile b % (nr nc), of `splits` equal ranges of the steps number
+// b / (nr nc). With more than one range the sums go to parts[range][c][r]
+// (rows ldp apart, ranges `stride`) and the epilogue to plane_join_kernel.
+template <class M, typename O, int BR, int BC, int WR, int WC, bool CK>
 __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
     TileOperand R, TileOperand C, int64_t kbytes, PlanePairs pairs, PlaneEpilogue ep,
-    O* __restrict__ Y, int64_t ldy, bool vec, unsigned nr, unsigned nc) {
-  typedef TileProduct<M, BR, BC, WR, WC> TP;
+    O* __restrict__ Y, int64_t ldy, bool vec, unsigned nr, unsigned nc, int splits,
+    float* __restrict__ parts, int64_t ldp, int64_t stride) {
+  typedef TileProduct<M, BR, BC, WR, WC, true, CK> TP;
   extern __shared__ char lds[];
+  const unsigned tiles = nr * nc;
+  const int range = blockIdx.x / tiles;
   int tr, tc;
-  tile_of(blockIdx.x, nr, nc, tr, tc);
+  tile_of(blockIdx.x - range * tiles, nr, nc, tr, tc);
   const int64_t r0 = (int64_t)tr * BR, c0 = (int64_t)tc * BC;
+  const int total = TP::steps(kbytes, pairs);
   TP tp;
   tp.zero();
-  tp.run(R, C, kbytes, pairs, r0, c0, lds);
+  tp.run(R, C, kbytes, pairs, r0, c0, (int)((int64_t)total * range / splits),
+         (int)((int64_t)total * (range + 1) / splits), lds);
   const int lane = threadIdx.x & 63;
   const int64_t rb = r0 + tp.wave_r() + 4 * (lane >> 4), cb = c0 + tp.wave_c() + (lane & 15);
+  if (splits > 1) {
+    store_tile(tp, r0, c0, R.rows, C.rows, parts + range * stride, ldp, true,
+               [&](float a, int, int, int) { return a; });
+    return;
+  }
   const float all = (ep.alpha ? *ep.alpha : 1.0f) * ep.beta;
   float sr[TP::FR][4], sc[TP::FC];
 #pragma unroll
@@ -122,72 +150,171 @@ __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
              [&](float a, int i, int j, int e) { return a * sr[i][e] * sc[j]; });
 }
 
-template <class M, typename O, int BR, int BC, int WR, int WC>
+// The ranges' sums in order, and the epilogue; four columns of one row a thread.
+template <typename O>
+__global__ __launch_bounds__(256) void plane_join_kernel(int64_t M, int64_t N, int splits,
+                                                         const float* __restrict__ parts,
+                                                         int64_t ldp, int64_t stride,
+                                                         PlaneEpilogue ep, O* __restrict__ Y,
+                                                         int64_t ldy, bool vec) {
+  const int64_t per = ldp / 4;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= N * per) return;
+  const int64_t c = at / per, r = (at - c * per) * 4;
+  f32x4 a = {0, 0, 0, 0};
+  for (int k = 0; k < splits; ++k) a += *(const f32x4*)(parts + k * stride + c * ldp + r);
+  if (ep.prev) a += *(const f32x4*)(ep.prev + c * ep.ldprev + r);
+  const float all = (ep.alpha ? *ep.alpha : 1.0f) * ep.beta;
+  const float sc = ep.col_scale ? ep.col_scale[c] : 1.0f;
+  O t[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float sr = ep.row_scale ? ep.row_scale[r + e < M ? r + e : M - 1] : 1.0f;
+    t[e] = from_f32<O>(a[e] * (sr * all) * sc);
+  }
+  if (vec && r + 4 <= M) {
+    *(typename Vec4<O>::type*)(Y + c * ldy + r) = __builtin_bit_cast(typename Vec4<O>::type, t);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r + e < M) Y[c * ldy + r + e] = t[e];
+  }
+}
+
+// Workgroups of 128 x 128 tiles that run at once: two on each of 256 CUs.
+constexpr int64_t kWorkgroups = 512;
+// A range of fewer steps costs more in its sums than it saves.
+constexpr int64_t kMinSteps = 8;
+
+static int64_t small_tiles(int64_t M, int64_t N) { return ((M + 127) / 128) * ((N + 127) / 128); }
+
+size_t plane_product_bytes(int64_t M, int64_t N) {
+  const int64_t tiles = small_tiles(M, N);
+  if (tiles == 0 || tiles * 2 > kWorkgroups) return 0;
+  return (size_t)(kWorkgroups / tiles * N * ((M + 3) / 4 * 4)) * sizeof(float);
+}
+
+template <class M, typename O, int BR, int BC, int WR, int WC, bool CK>
 static hipError_t start_plane_product(const TileOperand& R, const TileOperand& C, int64_t kbytes,
                                       const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,
-                                      int64_t ldy, hipStream_t s) {
-  typedef TileProduct<M, BR, BC, WR, WC> TP;
-  auto* k = plane_product_kernel<M, O, BR, BC, WR, WC>;
+                                      int64_t ldy, int splits, float* parts, hipStream_t s) {
+  typedef TileProduct<M, BR, BC, WR, WC, true, CK> TP;
+  auto* k = plane_product_kernel<M, O, BR, BC, WR, WC, CK>;
   if (TP::kLds > 65536) {
     const hipError_t e =
         hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, TP::kLds);
     if (e != hipSuccess) return e;
   }
   const int64_t nr = (R.rows + BR - 1) / BR, nc = (C.rows + BC - 1) / BC;
-  hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc)), dim3(TP::kThreads), TP::kLds, s, R, C, kbytes,
-                     pairs, ep, Y, ldy, vec4_ok(Y, ldy), (unsigned)nr, (unsigned)nc);
+  const int64_t ldp = (R.rows + 3) / 4 * 4, stride = C.rows * ldp;
+  const bool vec = vec4_ok(Y, ldy);
+  hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc * splits)), dim3(TP::kThreads), TP::kLds, s, R, C,
+                     kbytes, pairs, ep, Y, ldy, vec, (unsigned)nr, (unsigned)nc, splits, parts, ldp,
+                     stride);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  hipLaunchKernelGGL(plane_join_kernel<O>, dim3((unsigned)((stride / 4 + 255) / 256)), dim3(256), 0,
+                     s, R.rows, C.rows, splits, parts, ldp, stride, ep, Y, ldy, vec);
   return hipGetLastError();
 }
 
-template <typename O, bool F16P>
+template <typename O, bool F16P, bool CK>
 hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C,
                                 const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,
-                                int64_t ldy, hipStream_t s) {
+                                int64_t ldy, float* parts, hipStream_t s) {
   typedef typename std::conditional<F16P, MmaF16, MmaBF16>::type Mma;
   if (M <= 0 || N <= 0) return hipSuccess;
-  const TileOperand r = {R.w, R.ld, R.plane, M}, c = {C.w, C.ld, C.plane, N};
+  const TileOperand r = {R.w, R.ld, R.plane, M, K}, c = {C.w, C.ld, C.plane, N, K};
   const int64_t kbytes = (K + 7) / 8 * 16;  // whole 16-byte chunks: the planes' padding is zero
   const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
   if (big >= 192)
-    return start_plane_product<Mma, O, 256, 256, 2, 4>(r, c, kbytes, pairs, ep, Y, ldy, s);
-  return start_plane_product<Mma, O, 128, 128, 2, 2>(r, c, kbytes, pairs, ep, Y, ldy, s);
-}
-
-template <typename X, int KIND>
-hipError_t launch_planes(int64_t rows, int64_t cols, const X* x, int64_t ldx,
-                         const float* col_scale, Planes out, hipStream_t s) {
-  const int64_t n = rows * (out.ld / 16);
-  if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL((planes_kernel<X, KIND>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                     rows, cols, x, ldx, col_scale, out);
-  return hipGetLastError();
-}
-
-template <typename X, int KIND>
-hipError_t launch_planes_t(int64_t rows, int64_t cols, const X* x, int64_t ldx,
-                           const float* row_scale, Planes out, hipStream_t s) {
-  if (rows <= 0 || cols <= 0) return hipSuccess;
-  hipLaunchKernelGGL((planes_t_kernel<X, KIND>),
-                     dim3((unsigned)((rows + 63) / 64), (unsigned)((cols + 63) / 64)), dim3(256), 0,
-                     s, rows, cols, x, ldx, row_scale, out);
-  return hipGetLastError();
+    return start_plane_product<Mma, O, 256, 256, 2, 4, CK>(r, c, kbytes, pairs, ep, Y, ldy, 1, parts,
+                                                           s);
+  // few tiles: k split so that the chip is filled
+  const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes * pairs.n;
+  int64_t splits = kWorkgroups / small_tiles(M, N);
+  if (splits > steps / kMinSteps) splits = steps / kMinSteps;
+  return start_plane_product<Mma, O, 128, 128, 2, 2, CK>(r, c, kbytes, pairs, ep, Y, ldy,
+                                                         splits > 1 ? (int)splits : 1, parts, s);
 }
 
 // ---------------------------------------------------------------------------
 // Input gradient of the 8-bit product: dX[t][j] = channel[j] sum_i (G[t][i]
-// sv[i]) Vq[i][j]. The codes are exact in bfloat16, so the product runs on
-// the bfloat16 instructions with Vq's transpose as one plane and G sv as as
-// many planes as its type has bits: one for bfloat16 (its rounding is as large
-// as the output's own), two for float16 (2^-16 against the output's 2^-11), three
-// for float32 (all 24 bits).
+// sv[i]) Vq[i][j]. The codes are exact in 16-bit floats, so the product runs on
+// those instructions with Vq as one k-major plane. For a 16-bit G the other
+// operand is one float16 plane of G sv times a power of two for each token,
+// which brings the token's largest to [2^14, 2^15): 11 bits, which values down to
+// 2^-28 of the largest keep. (One bfloat16 plane would keep 8 bits, as coarse as
+// a bfloat16 output, at the same cost; more bits cost a second product.) A
+// float32 G is three bfloat16 planes, all 24 bits.
 // ---------------------------------------------------------------------------
-template <typename G> struct GradSplit;
-template <> struct GradSplit<float> { static constexpr int kind = kBF16x3; };
-template <> struct GradSplit<BF16> { static constexpr int kind = kBF16x1; };
-template <> struct GradSplit<F16> { static constexpr int kind = kBF16x2; };
+template <typename G>
+__global__ __launch_bounds__(256) void grad_tokens_kernel(int64_t m, const G* __restrict__ g,
+                                                          int64_t ldg, const float* __restrict__ sv,
+                                                          Planes out, float* __restrict__ unscale,
+                                                          bool vec) {
+  __shared__ unsigned red[4];
+  const int tid = threadIdx.x;
+  const G* row = g + (int64_t)blockIdx.x * ldg;
+  const int64_t cols = out.ld / 2;
+  auto at = [&](int64_t c, float* v) {
+    load8(row, c, m, vec, v);
+    if (sv) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < m) v[e] *= sv[c + e];
+    }
+  };
+  unsigned top = 0;
+  for (int64_t c = tid * 8; c < cols; c += 2048) {
+    float v[8];
+    at(c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned a = __float_as_uint(v[e]) & 0x7fffffffu;
+      top = a > top ? a : top;
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const unsigned u = __shfl_xor(top, o, 64);
+    top = u > top ? u : top;
+  }
+  if ((tid & 63) == 0) red[tid >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = red[w] > top ? red[w] : top;
+  // 2^k with 2^(14 - k) <= the largest < 2^(15 - k); an infinity or NaN counts as
+  // 2^127 (finite values beside it stay finite), small ones as 2^-112 (2^k stays normal)
+  const int e = (int)(top >> 23) - 127;
+  const int k = e > 127 ? -113 : e < -112 ? 126 : 14 - e;
+  const float scale = __uint_as_float((unsigned)(k + 127) << 23);
+  if (tid == 0) unscale[blockIdx.x] = __uint_as_float((unsigned)(127 - k) << 23);
+  for (int64_t c = tid * 8; c < cols; c += 2048) {
+    float v[8];
+    at(c, v);
+    _Float16 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = (_Float16)(v[i] * scale);
+    *(v4i*)(out.w + (int64_t)blockIdx.x * out.ld + c * 2) = __builtin_bit_cast(v4i, w);
+  }
+}
 
-size_t matmul_int8_grad_bytes(int planes, int64_t T, int64_t m, int64_t n) {
-  return (size_t)plane_ld(m) * (size_t)(n + planes * T);
+static inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+struct GradOffsets {
+  size_t v, g, unscale, parts, total;
+};
+static GradOffsets grad_offsets(int es, int64_t T, int64_t m, int64_t n) {
+  GradOffsets o;
+  o.v = 0;
+  o.g = o.v + up256((size_t)(m * plane_ld(n)));
+  o.unscale = o.g + up256((size_t)((es == 4 ? 3 : 1) * T * plane_ld(m)));
+  o.parts = o.unscale + up256((size_t)T * 4);
+  o.total = o.parts + plane_product_bytes(n, T);
+  return o;
+}
+size_t matmul_int8_grad_bytes(int es, int64_t T, int64_t m, int64_t n) {
+  return grad_offsets(es, T, m, n).total;
 }
 
 template <typename G>
@@ -195,35 +322,50 @@ hipError_t launch_matmul_int8_grad(int64_t T, int64_t m, int64_t n, const G* g, 
                                    const int8_t* Vq, int64_t ldv, const float* sv,
                                    const float* channel, G* dX, int64_t ldx, void* ws,
                                    hipStream_t s) {
-  constexpr int kind = GradSplit<G>::kind;
+  constexpr bool wide = sizeof(G) == 4;
+  constexpr int kind = wide ? kBF16x1 : kF16x1;
   if (T <= 0 || n <= 0) return hipSuccess;
-  const int64_t ld = plane_ld(m);
-  const Planes v = {(char*)ws, ld, 0}, gp = {(char*)ws + n * ld, ld, T * ld};
-  hipError_t e = launch_planes_t<I8, kBF16x1>(m, n, (const I8*)Vq, ldv, nullptr, v, s);
+  const GradOffsets o = grad_offsets(sizeof(G), T, m, n);
+  char* b = (char*)ws;
+  const Planes v = {b + o.v, plane_ld(n), 0}, gp = {b + o.g, plane_ld(m), T * plane_ld(m)};
+  float* unscale = (float*)(b + o.unscale);
+  hipError_t e = launch_planes<I8, kind>(m, n, (const I8*)Vq, ldv, nullptr, nullptr, v, s);
   if (e != hipSuccess) return e;
-  if ((e = launch_planes<G, kind>(T, m, g, ldg, sv, gp, s)) != hipSuccess) return e;
-  const PlanePairs pairs = {kPlanes[kind], {0, 0, 0}, {0, 1, 2}};
-  const PlaneEpilogue ep = {channel, nullptr, nullptr, 1.0f, nullptr, 0};
-  return launch_plane_product<G, false>(n, T, m, v, gp, pairs, ep, dX, ldx, s);
+  PlanePairs pairs = {1, 0, 0};
+  PlaneEpilogue ep = {channel, nullptr, nullptr, 1.0f, nullptr, 0};
+  if constexpr (wide) {
+    pairs = {3, 0x000, 0x210};
+    e = launch_planes<G, kBF16x3>(T, m, g, ldg, nullptr, sv, gp, s);
+  } else {
+    ep.col_scale = unscale;
+    hipLaunchKernelGGL(grad_tokens_kernel<G>, dim3((unsigned)T), dim3(256), 0, s, m, g, ldg, sv, gp,
+                       unscale, load8_ok(g, ldg));
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  return launch_plane_product<G, !wide, false>(n, T, m, v, gp, pairs, ep, dX, ldx,
+                                               (float*)(b + o.parts), s);
 }
 
-#define BK_INST_P(X, KIND)                                                                  \
-  template hipError_t launch_planes<X, KIND>(int64_t, int64_t, const X*, int64_t,           \
-                                             const float*, Planes, hipStream_t);            \
-  template hipError_t launch_planes_t<X, KIND>(int64_t, int64_t, const X*, int64_t,         \
-                                               const float*, Planes, hipStream_t);
+#define BK_INST_P(X, KIND)                                                                 \
+  template hipError_t launch_planes<X, KIND>(int64_t, int64_t, const X*, int64_t,          \
+                                             const float*, const float*, Planes, hipStream_t);
 BK_INST_P(float, kBF16x3)
 BK_INST_P(BF16, kBF16x1)
 BK_INST_P(F16, kF16x1)
 #undef BK_INST_P
-#define BK_INST_Y(O, F)                                                                     \
-  template hipError_t launch_plane_product<O, F>(int64_t, int64_t, int64_t, Planes, Planes, \
-                                                 const PlanePairs&, const PlaneEpilogue&,   \
-                                                 O*, int64_t, hipStream_t);
-BK_INST_Y(float, false)
-BK_INST_Y(float, true)
-BK_INST_Y(BF16, false)
-BK_INST_Y(F16, true)
+#define BK_INST_Y(O, F, CK)                                                                \
+  template hipError_t launch_plane_product<O, F, CK>(int64_t, int64_t, int64_t, Planes,    \
+                                                     Planes, const PlanePairs&,            \
+                                                     const PlaneEpilogue&, O*, int64_t,    \
+                                                     float*, hipStream_t);
+BK_INST_Y(float, false, false)
+BK_INST_Y(float, true, false)
+BK_INST_Y(BF16, false, false)
+BK_INST_Y(F16, true, false)
+BK_INST_Y(float, false, true)
+BK_INST_Y(BF16, false, true)
+BK_INST_Y(F16, true, true)
 #undef BK_INST_Y
 #define BK_INST(G)                                                                            \
   template hipError_t launch_matmul_int8_grad<G>(int64_t, int64_t, int64_t, const G*,         \

@@ -83,8 +83,8 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
   if (ANY) {
     tp.run_any(V, Xq, n, r0, c0, lds);
   } else {
-    const PlanePairs one = {1, {0}, {0}};
-    tp.run(V, Xq, n, one, r0, c0, lds);
+    const PlanePairs one = {1, 0, 0};
+    tp.run(V, Xq, n, one, r0, c0, 0, TP::steps(n, one), lds);
   }
   const int lane = threadIdx.x & 63;
   float st[TP::FC], sr[TP::FR][4];
@@ -133,7 +133,7 @@ hipError_t launch_matmul_int8(int64_t T, int64_t m, int64_t n, const int8_t* Xq,
                               const float* sx, const int8_t* Vq, int64_t ldv, const float* sv, O* Y,
                               int64_t ldy, hipStream_t s) {
   if (T <= 0 || m <= 0) return hipSuccess;
-  const TileOperand V = {(const char*)Vq, ldv, 0, m}, X = {(const char*)Xq, ldx, 0, T};
+  const TileOperand V = {(const char*)Vq, ldv, 0, m, 0}, X = {(const char*)Xq, ldx, 0, T, 0};
   const bool direct = tile_direct(V, n) && tile_direct(X, n);
   if (!direct) return start_matmul_int8<O, 128, 128, 2, 2, true>(V, X, n, sx, sv, Y, ldy, s);
   const int64_t big = ((m + 255) / 256) * ((T + 255) / 256);

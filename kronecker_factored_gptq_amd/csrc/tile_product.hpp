@@ -53,11 +53,12 @@ struct MmaF16 {
   }
 };
 
-// One operand: `rows` rows of `kbytes` bytes, `ld` bytes apart, in planes
-// `plane` bytes apart.
+// One operand, in planes `plane` bytes apart: `rows` rows of a product's kbytes
+// bytes, `ld` bytes apart; or k-major: `krows` rows of k, `ld` bytes apart, each
+// holding that k of all `rows`, readable up to a multiple of 16 bytes.
 struct TileOperand {
   const char* p;
-  int64_t ld, plane, rows;
+  int64_t ld, plane, rows, krows;
 };
 
 // The largest row stride (and row length, in bytes) the direct loads take: the
@@ -138,8 +139,9 @@ struct TileProduct {
     typedef short v4s __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4s lds_v4s;
     const int k = 8 * q + (r16 >> 2);  // and 4 further, of 32 kk on
-    const char* a = lds + (kk * 32 + k) * (2 * B) + ((row0 / 16 + i) ^ swap_at(k)) * 32 +
-                    (r16 & 3) * 8;
+    // block row0 / 16 + i, the first a multiple of the wave's fragments
+    const int at = k * (2 * B) + ((row0 / 16) ^ swap_at(k)) * 32 + (r16 & 3) * 8;
+    const char* a = lds + (at ^ (i * 32)) + kk * 64 * B;
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a);
     const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(a + 8 * B));
     const int2 x = __builtin_bit_cast(int2, lo), y = __builtin_bit_cast(int2, hi);
@@ -197,12 +199,17 @@ struct TileProduct {
   }
 
   // 64 lanes x 16 bytes from global memory straight into LDS at `lds` + 16 *
-  // lane. The LDS address is a number, so the compiler ties no LDS read to
-  // these loads: the waits are the ones written in run().
-  __device__ static inline void load_lds(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
-                                         unsigned lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rsrc, (__attribute__((address_space(3))) void*)(uintptr_t)lds, 16, voff, soff, 0, 0);
+  // lane. No register is loaded, so the instruction can stand by itself: as a
+  // builtin it makes the compiler wait for every such load in flight before a
+  // transposing LDS read, which is what run()'s own waits are there to avoid.
+  // (s_nop: the wait states from a register write to its use as an address.)
+  __device__ static inline void load_lds(v4i rsrc, int voff, int soff, unsigned lds) {
+    asm volatile(
+        "s_mov_b32 m0, %3\n\t"
+        "s_nop 4\n\t"
+        "buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
+        "s"(rsrc), "s"(soff), "s"(lds)
+        : "memory");
   }
 
   // One operand's loads: a lane's byte offsets for each of a step's NL wave
@@ -213,19 +220,21 @@ struct TileProduct {
   // chunks past its rows.
   template <bool K, int B, int NL>
   struct Loader {
-    const char* p;
-    int64_t plane;
-    int bytes, step;  // of the buffer; from one k step to the next
+    const char* p;  // k-major: of the next step
+    const char* first;
+    int64_t plane, kstride;
+    int bytes;
     int off[NL];
     int krow;       // k-major: this lane's k of the first load
     bool past;      // this lane's chunk is past the end in the last k step
     int ksteps, k, pair, npairs;  // the next step to load
     unsigned lds, slot;           // this wave's place in slot 0; the next slot
-    const unsigned char* planes;
-    __amdgpu_buffer_rsrc_t rsrc;
+    unsigned planes;
+    v4i rsrc;
 
     __device__ inline void init(const TileOperand& o, int64_t row0, int64_t kbytes, int npairs_,
-                                const unsigned char* planes_, unsigned lds_, unsigned slot_) {
+                                unsigned planes_, int step0, unsigned lds_,
+                                unsigned slot_) {
       const int lane = threadIdx.x & 63;
       const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
       const int rows = o.rows - row0 < B ? (int)(o.rows - row0) : B, ld = (int)o.ld;
@@ -235,11 +244,9 @@ struct TileProduct {
       planes = planes_;
       lds = lds_ + wave * 1024;
       slot = slot_;
-      k = pair = 0;
       if (!K) {
-        p = o.p + row0 * o.ld;
+        first = o.p + row0 * o.ld;
         bytes = (rows - 1) * ld + (int)kbytes;
-        step = kStepBytes;
         const int row8 = lane >> 3, chunk = chunk_at((wave & 1) * 8 + row8, lane & 7);
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
@@ -248,10 +255,9 @@ struct TileProduct {
         }
         past = chunk * 16 + (ksteps - 1) * kStepBytes >= (int)kbytes;
       } else {
-        p = o.p + row0 * 2;
-        const int kn = (int)(kbytes / 2);
-        bytes = (kn - 1) * ld + rows * 2;
-        step = 64 * ld;
+        first = o.p + row0 * 2;
+        kstride = 64 * o.ld;  // past 32 bits over all steps, so the buffer moves along
+        bytes = 63 * ld + (rows + 7) / 8 * 16;  // whole chunks: the rows are padded to them
         constexpr int per = B / 8;  // chunks of a k; kLanesK k in a wave load
         constexpr int lanes_k = 64 / per;
         krow = lane / per;
@@ -261,26 +267,40 @@ struct TileProduct {
           const int chunk = ((pos >> 1) ^ swap_at(kr)) * 2 + (pos & 1);
           off[j] = chunk * 8 < rows ? kr * ld + chunk * 16 : (int)0x80000000;
         }
-        krow += wave * lanes_k + (ksteps - 1) * 64 - kn;  // >= 0: past the last k
+        krow += wave * lanes_k + (ksteps - 1) * 64 - (int)o.krows;  // >= 0: past the last k
       }
-      select(planes[0]);
+      pair = __builtin_amdgcn_readfirstlane(step0 / ksteps);
+      k = step0 - pair * ksteps;
+      select(planes >> 4 * pair & 15);
     }
     __device__ inline void select(int pl) {
-      rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p + pl * plane), 0, bytes,
-                                               0x00020000);
+      p = first + pl * plane;
+      if (K) p += k * kstride;
+      point();
+    }
+    __device__ inline void point() {
+      const uint64_t a = (uint64_t)p;
+      rsrc[0] = __builtin_amdgcn_readfirstlane((int)(unsigned)a);
+      rsrc[1] = __builtin_amdgcn_readfirstlane((int)(unsigned)(a >> 32) & 0xffff);
+      rsrc[2] = __builtin_amdgcn_readfirstlane(bytes);
+      rsrc[3] = 0x00020000;
     }
     __device__ inline void load(int j) const {
       const bool last = k == ksteps - 1;
       bool cut = last && past;
       if (K) cut = last && krow + j * kWaves * (64 / (B / 8)) >= 0;
-      load_lds(rsrc, cut ? (int)0x80000000 : off[j], k * step,
+      load_lds(rsrc, cut ? (int)0x80000000 : off[j], K ? 0 : k * kStepBytes,
                lds + slot * kSlot + j * kWaves * 1024);
     }
     __device__ inline void advance() {
       slot = slot >= 3 ? slot - 3 : slot + 2;
       if (++k == ksteps && pair + 1 < npairs) {
         k = 0;
-        select(planes[++pair]);
+        ++pair;
+        select(planes >> 4 * pair & 15);
+      } else if (K) {
+        p += kstride;
+        point();
       }
     }
   };
@@ -289,16 +309,24 @@ struct TileProduct {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
   }
 
-  // D's tile at (r0, c0); operands as tile_direct wants them, kbytes of k.
+  // The number of steps of a product.
+  __device__ static inline int steps(int64_t kbytes, const PlanePairs& pairs) {
+    return (int)((kbytes + kStepBytes - 1) / kStepBytes) * pairs.n;
+  }
+
+  // D's tile at (r0, c0), summed over the product's steps [s0, s1); operands as
+  // tile_direct wants them, kbytes of k.
   __device__ inline void run(const TileOperand& R, const TileOperand& C, int64_t kbytes,
-                             const PlanePairs& pairs, int64_t r0, int64_t c0, char* lds) {
-    const int total = (int)((kbytes + kStepBytes - 1) / kStepBytes) * pairs.n;
-    if (total == 0) return;
+                             const PlanePairs& pairs, int64_t r0, int64_t c0, int s0, int s1,
+                             char* lds) {
+    s0 = __builtin_amdgcn_readfirstlane(s0);
+    const int total = __builtin_amdgcn_readfirstlane(s1) - s0;
+    if (total <= 0) return;
     const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
     Loader<RK, BR, LR> lr;
     Loader<CK, BC, LC> lc;
-    lr.init(R, r0, kbytes, pairs.n, pairs.r, base, 0);
-    lc.init(C, c0, kbytes, pairs.n, pairs.c, base, 1);
+    lr.init(R, r0, kbytes, pairs.n, pairs.r, s0, base, 0);
+    lc.init(C, c0, kbytes, pairs.n, pairs.c, s0, base, 1);
     auto load_r = [&]() {
 #pragma unroll
       for (int u = 0; u < LR; ++u) lr.load(u);

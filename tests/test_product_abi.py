@@ -86,7 +86,7 @@ def test_matmul_int8_grad_empty_and_workspace():
     assert _grad(T=0, G=None, D=None, ws=None) == bk.OK
     assert _grad(n=0, V=None, c=None, D=None, ws=None) == bk.OK
     q = bk.lib().bakron_matmul_int8_grad_workspace_bytes
-    assert 0 < q(bk.BF16, 64, 64, 64) < q(bk.F16, 64, 64, 64) < q(bk.F32, 64, 64, 64) < q(bk.F32, 64, 200, 64)
+    assert 0 < q(bk.BF16, 64, 64, 64) == q(bk.F16, 64, 64, 64) < q(bk.F32, 64, 64, 64) < q(bk.F32, 64, 200, 64)
     assert q(bk.F64, 64, 64, 64) == q(bk.F32, -1, 64, 64) == q(bk.F32, 64, 1 << 21, 64) == 0
 
 
