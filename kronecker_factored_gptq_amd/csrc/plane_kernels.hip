@@ -11,34 +11,6 @@ struct I8 {
 };
 __device__ inline float to_f32(I8 x) { return (float)x.v; }
 
-namespace {
-
-// Eight elements of a row from column c on, zero past `cols`; `vec`: whole
-// groups of eight are aligned to their size (at most 16 bytes).
-template <typename X>
-__device__ inline void load8(const X* row, int64_t c, int64_t cols, bool vec, float* v) {
-  constexpr int kBytes = 8 * sizeof(X) < 16 ? 8 * sizeof(X) : 16;
-  constexpr int kPer = kBytes / sizeof(X);
-  if (vec && c + 8 <= cols) {
-    X t[8];
-#pragma unroll
-    for (int i = 0; i < 8; i += kPer)
-      __builtin_memcpy(t + i, __builtin_assume_aligned(row + c + i, kBytes), kBytes);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f32(row[c + i]) : 0.0f;
-  }
-}
-template <typename X>
-inline bool load8_ok(const X* x, int64_t ld) {
-  constexpr int kBytes = 8 * sizeof(X) < 16 ? 8 * sizeof(X) : 16;
-  return (uintptr_t)x % kBytes == 0 && ld * sizeof(X) % kBytes == 0;
-}
-
-}  // namespace
-
 // Eight columns of one row per thread, one 16-byte store per plane.
 template <typename X, int KIND>
 __global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
@@ -51,8 +23,10 @@ __global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= rows * per) return;
   const int64_t r = at / per, c0 = (at - r * per) * 8;
+  const Eight<X> t8 = load8(x + r * ldx, c0, cols, vec);
   float v[8];
-  load8(x + r * ldx, c0, cols, vec, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = to_f32(t8.v[e]);
   if (cs) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= cs[c0 + e < cols ? c0 + e : cols - 1];
@@ -248,56 +222,67 @@ hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Plane
 // a bfloat16 output, at the same cost; more bits cost a second product.) A
 // float32 G is three bfloat16 planes, all 24 bits.
 // ---------------------------------------------------------------------------
-template <typename G>
+template <typename G, int NV>
 __global__ __launch_bounds__(256) void grad_tokens_kernel(int64_t m, const G* __restrict__ g,
                                                           int64_t ldg, const float* __restrict__ sv,
                                                           Planes out, float* __restrict__ unscale,
-                                                          bool vec) {
+                                                          bool vec, bool vecs) {
   __shared__ unsigned red[4];
-  const int tid = threadIdx.x;
-  const G* row = g + (int64_t)blockIdx.x * ldg;
-  const int64_t cols = out.ld / 2;
-  auto at = [&](int64_t c, float* v) {
-    load8(row, c, m, vec, v);
-    if (sv) {
+  const RowOf<G, NV> row(g + (int64_t)blockIdx.x * ldg, m, vec);
+  auto values = [&](int64_t c, const Eight<G>& t, float* v) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < m) v[e] *= sv[c + e];
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(t.v[e]);
+    if (sv) {
+      float f[8];
+      factors8(sv, c, m, vecs, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= f[e];
     }
   };
   unsigned top = 0;
-  for (int64_t c = tid * 8; c < cols; c += 2048) {
+  row.each(m, [&](int64_t c, const Eight<G>& t) {
     float v[8];
-    at(c, v);
+    values(c, t, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
+      // what lies past m was read as zero
       const unsigned a = __float_as_uint(v[e]) & 0x7fffffffu;
       top = a > top ? a : top;
     }
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const unsigned u = __shfl_xor(top, o, 64);
-    top = u > top ? u : top;
-  }
-  if ((tid & 63) == 0) red[tid >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = red[w] > top ? red[w] : top;
+  });
+  top = max_of_256(top, red);
   // 2^k with 2^(14 - k) <= the largest < 2^(15 - k); an infinity or NaN counts as
   // 2^127 (finite values beside it stay finite), small ones as 2^-112 (2^k stays normal)
   const int e = (int)(top >> 23) - 127;
   const int k = e > 127 ? -113 : e < -112 ? 126 : 14 - e;
   const float scale = __uint_as_float((unsigned)(k + 127) << 23);
-  if (tid == 0) unscale[blockIdx.x] = __uint_as_float((unsigned)(127 - k) << 23);
-  for (int64_t c = tid * 8; c < cols; c += 2048) {
+  if (threadIdx.x == 0) unscale[blockIdx.x] = __uint_as_float((unsigned)(127 - k) << 23);
+  row.each(out.ld / 2, [&](int64_t c, const Eight<G>& t) {
     float v[8];
-    at(c, v);
+    values(c, t, v);
     _Float16 w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = (_Float16)(v[i] * scale);
     *(v4i*)(out.w + (int64_t)blockIdx.x * out.ld + c * 2) = __builtin_bit_cast(v4i, w);
+  });
+}
+
+template <typename G>
+static hipError_t launch_grad_tokens(int64_t T, int64_t m, const G* g, int64_t ldg, const float* sv,
+                                     Planes out, float* unscale, hipStream_t s) {
+  const bool vec = load8_ok(g, ldg), vecs = load8_ok(sv, 0);
+#define BK_ROWS(NV)                                                                              \
+  hipLaunchKernelGGL((grad_tokens_kernel<G, NV>), dim3((unsigned)T), dim3(256), 0, s, m, g, ldg, \
+                     sv, out, unscale, vec, vecs)
+  switch (row_groups(out.ld / 2)) {
+    case 1: BK_ROWS(1); break;
+    case 2: BK_ROWS(2); break;
+    case 4: BK_ROWS(4); break;
+    case 8: BK_ROWS(8); break;
+    default: BK_ROWS(0);
   }
+#undef BK_ROWS
+  return hipGetLastError();
 }
 
 static inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -338,9 +323,7 @@ hipError_t launch_matmul_int8_grad(int64_t T, int64_t m, int64_t n, const G* g, 
     e = launch_planes<G, kBF16x3>(T, m, g, ldg, nullptr, sv, gp, s);
   } else {
     ep.col_scale = unscale;
-    hipLaunchKernelGGL(grad_tokens_kernel<G>, dim3((unsigned)T), dim3(256), 0, s, m, g, ldg, sv, gp,
-                       unscale, load8_ok(g, ldg));
-    e = hipGetLastError();
+    e = launch_grad_tokens(T, m, g, ldg, sv, gp, unscale, s);
   }
   if (e != hipSuccess) return e;
   return launch_plane_product<G, !wide, false>(n, T, m, v, gp, pairs, ep, dX, ldx,

@@ -13,52 +13,74 @@ namespace bk {
 // |x|, in which a NaN is larger than infinity: a token with an infinity or a
 // NaN gets that as its scale, and codes whose products it makes NaN.
 // ---------------------------------------------------------------------------
-template <typename X, bool CH, bool VEC>
+template <typename X, int NV>
 __global__ __launch_bounds__(256) void quantize_tokens_kernel(
     int64_t n, const X* __restrict__ x, int64_t ldx, const float* __restrict__ c,
-    signed char* __restrict__ q, int64_t ldq, float* __restrict__ s) {
+    signed char* __restrict__ q, int64_t ldq, float* __restrict__ s, bool vec, bool vecc,
+    bool vecq) {
   __shared__ unsigned red[4];
-  const int tid = threadIdx.x;
-  const X* row = x + (int64_t)blockIdx.x * ldx;
+  const RowOf<X, NV> row(x + (int64_t)blockIdx.x * ldx, n, vec);
   signed char* out = q + (int64_t)blockIdx.x * ldq;
-  auto at = [&](int64_t j) {
-    const float v = to_f32(row[j]);
-    return CH ? v * c[j] : v;
+  auto values = [&](int64_t j, const Eight<X>& t, float* v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(t.v[e]);
+    if (c) {
+      float f[8];
+      factors8(c, j, n, vecc, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= f[e];
+    }
   };
   unsigned top = 0;
-  for (int64_t j = tid; j < n; j += 256) {
-    const unsigned a = __float_as_uint(at(j)) & 0x7fffffffu;
-    top = a > top ? a : top;
-  }
+  row.each(n, [&](int64_t j, const Eight<X>& t) {
+    float v[8];
+    values(j, t, v);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const unsigned u = __shfl_xor(top, o, 64);
-    top = u > top ? u : top;
-  }
-  if ((tid & 63) == 0) red[tid >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = red[w] > top ? red[w] : top;
+    for (int e = 0; e < 8; ++e) {
+      // what lies past n was read as zero
+      const unsigned a = __float_as_uint(v[e]) & 0x7fffffffu;
+      top = a > top ? a : top;
+    }
+  });
+  top = max_of_256(top, red);
   const float scale = top == 0 ? 1.0f : __uint_as_float(top) / 127.0f;
-  if (tid == 0) s[blockIdx.x] = scale;
-  for (int64_t j = tid; j < n; j += 256) {
-    const float v = __builtin_rintf(at(j) / scale);
-    // a NaN compares false everywhere: code 0
-    const int code = v >= 127.0f ? 127 : v <= -127.0f ? -127 : v == v ? (int)v : 0;
-    out[j] = (signed char)code;
-  }
+  if (threadIdx.x == 0) s[blockIdx.x] = scale;
+  row.each(n, [&](int64_t j, const Eight<X>& t) {
+    float v[8];
+    values(j, t, v);
+    signed char w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = __builtin_rintf(v[e] / scale);
+      // a NaN compares false everywhere: code 0
+      w[e] = (signed char)(u >= 127.0f ? 127 : u <= -127.0f ? -127 : u == u ? (int)u : 0);
+    }
+    if (vecq && j + 8 <= n) {
+      *(uint2*)(out + j) = __builtin_bit_cast(uint2, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e < n) out[j + e] = w[e];
+    }
+  });
 }
 
 template <typename X>
 hipError_t launch_quantize_tokens(int64_t T, int64_t n, const X* x, int64_t ldx, const float* c,
                                   int8_t* q, int64_t ldq, float* s, hipStream_t st) {
   if (T <= 0) return hipSuccess;
-  if (c)
-    hipLaunchKernelGGL((quantize_tokens_kernel<X, true, false>), dim3((unsigned)T), dim3(256), 0,
-                       st, n, x, ldx, c, (signed char*)q, ldq, s);
-  else
-    hipLaunchKernelGGL((quantize_tokens_kernel<X, false, false>), dim3((unsigned)T), dim3(256), 0,
-                       st, n, x, ldx, c, (signed char*)q, ldq, s);
+  const bool vec = load8_ok(x, ldx), vecc = load8_ok(c, 0), vecq = load8_ok(q, ldq);
+#define BK_ROWS(NV)                                                                            \
+  hipLaunchKernelGGL((quantize_tokens_kernel<X, NV>), dim3((unsigned)T), dim3(256), 0, st, n, x, \
+                     ldx, c, (signed char*)q, ldq, s, vec, vecc, vecq)
+  switch (row_groups(n)) {
+    case 1: BK_ROWS(1); break;
+    case 2: BK_ROWS(2); break;
+    case 4: BK_ROWS(4); break;
+    case 8: BK_ROWS(8); break;
+    default: BK_ROWS(0);
+  }
+#undef BK_ROWS
   return hipGetLastError();
 }
 

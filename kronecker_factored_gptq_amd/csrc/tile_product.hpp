@@ -568,4 +568,82 @@ __device__ inline void split16(float x, unsigned short* w) {
   }
 }
 
+// ---- rows ---------------------------------------------------------------------
+// Eight elements of a row from column c on, zero past `cols`; `vec` (load8_ok):
+// groups of eight are aligned to their size, or to 16 bytes.
+template <typename X> struct Eight {
+  X v[8];
+};
+template <typename X> constexpr int kLoadBytes = 8 * sizeof(X) < 16 ? 8 * sizeof(X) : 16;
+template <typename X>
+__device__ inline Eight<X> load8(const X* row, int64_t c, int64_t cols, bool vec) {
+  Eight<X> t;
+  if (vec && c + 8 <= cols) {
+    constexpr int kPer = kLoadBytes<X> / sizeof(X);
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer)
+      __builtin_memcpy(t.v + i, __builtin_assume_aligned(row + c + i, kLoadBytes<X>),
+                       kLoadBytes<X>);
+  } else {
+    __builtin_memset(&t, 0, sizeof t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) t.v[i] = row[c + i];
+  }
+  return t;
+}
+template <typename X>
+inline bool load8_ok(const X* x, int64_t ld) {
+  return (uintptr_t)x % kLoadBytes<X> == 0 && ld * sizeof(X) % kLoadBytes<X> == 0;
+}
+
+// A workgroup of 256 threads on one row: groups of eight elements, group k of
+// thread t at column 8 (256 k + t). The first NV groups of each thread stay in
+// registers, so that a row is read once for its maximum and what follows.
+template <typename X, int NV>
+struct RowOf {
+  Eight<X> keep[NV > 0 ? NV : 1];
+  const X* row;
+  int64_t cols;
+  bool vec;
+
+  __device__ inline RowOf(const X* r, int64_t n, bool v) : row(r), cols(n), vec(v) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) keep[k] = load8(row, at(k), cols, vec);
+  }
+  __device__ static inline int64_t at(int64_t k) { return 8 * (256 * k + threadIdx.x); }
+  // f(column, eight elements) for every group with columns below `upto`
+  template <typename F> __device__ inline void each(int64_t upto, F f) const {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (at(k) < upto) f(at(k), keep[k]);
+    for (int64_t k = NV; at(k) < upto; ++k) f(at(k), load8(row, at(k), cols, vec));
+  }
+};
+// Eight factors of the columns from c on (0 past `cols`).
+__device__ inline void factors8(const float* cs, int64_t c, int64_t cols, bool vec, float* f) {
+  const Eight<float> t = load8(cs, c, cols, vec);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = t.v[i];
+}
+// The largest of the workgroup's values (256 threads).
+__device__ inline unsigned max_of_256(unsigned top, unsigned* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const unsigned u = __shfl_xor(top, o, 64);
+    top = u > top ? u : top;
+  }
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = red[w] > top ? red[w] : top;
+  return top;
+}
+// Groups a thread keeps for rows of n columns: the row, if 8 groups hold it
+// (16384 columns, at most 64 registers).
+inline int row_groups(int64_t n) {
+  const int64_t g = (n + 2047) / 2048;
+  return g <= 1 ? 1 : g <= 2 ? 2 : g <= 4 ? 4 : g <= 8 ? 8 : 0;
+}
+
 }  // namespace bk
