@@ -470,16 +470,20 @@ int bakron_sample_sqnorms(int dtype, int64_t N, int64_t d, const void *X, int64_
  * the sum, its product with sx and that with sv are rounded to float32 in this
  * order, then once to ytype. Rows that start at multiples of 16 bytes
  * with n a multiple of 16 are read fastest; any alignment and stride works.
- * Y must not overlap the inputs (BAKRON_EINVAL).
+ * Y must not overlap the inputs (BAKRON_EINVAL). The workspace query gives 0,
+ * and workspace may be NULL, where the call needs none (few tokens, many
+ * tiles).
  *
  * Both are asynchronous and deterministic. T, m <= 2^31 - 1.
  * ------------------------------------------------------------------------ */
 int bakron_quantize_tokens(int xtype, int64_t T, int64_t n, const void *X, int64_t ldx,
                            const float *channel, int8_t *Xq, int64_t ldq, float *sx, void *stream);
+size_t bakron_matmul_int8_workspace_bytes(int64_t T, int64_t m, int64_t n);
 int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n,
                        const int8_t *Xq, int64_t ldx, const float *sx,
                        const int8_t *Vq, int64_t ldv, const float *sv,
-                       void *Y, int64_t ldy, void *stream);
+                       void *Y, int64_t ldy,
+                       void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Input gradient of the 8-bit product, the tokens' rounding passed straight

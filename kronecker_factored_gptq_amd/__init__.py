@@ -137,8 +137,10 @@ def lib() -> ctypes.CDLL:
     L.bakron_quantize_tokens.argtypes = [_int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp]
     L.bakron_quantize_tokens.restype = _int
     L.bakron_matmul_int8.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
-                                     _i64, _vp]
+                                     _i64, _vp, _sz, _vp]
     L.bakron_matmul_int8.restype = _int
+    L.bakron_matmul_int8_workspace_bytes.argtypes = [_i64, _i64, _i64]
+    L.bakron_matmul_int8_workspace_bytes.restype = _sz
     L.bakron_matmul_int8_grad_workspace_bytes.argtypes = [_int, _i64, _i64, _i64]
     L.bakron_matmul_int8_grad_workspace_bytes.restype = _sz
     L.bakron_matmul_int8_grad.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
@@ -831,7 +833,8 @@ def quantize_tokens(X: torch.Tensor, channel_scales: Optional[torch.Tensor] = No
 
 def matmul_int8(Xq: torch.Tensor, sx: torch.Tensor, Vq: torch.Tensor,
                 sv: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.float32,
-                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y[t][i] = sx[t] sv[i] sum_j Xq[t][j] Vq[i][j] (bakron_matmul_int8): the
     tokens of ``quantize_tokens`` through a layer held as the solve's codes.
     Xq is T x n and Vq m x n, int8 (``V.to(torch.int8)`` of codes inside
@@ -839,7 +842,7 @@ def matmul_int8(Xq: torch.Tensor, sx: torch.Tensor, Vq: torch.Tensor,
     None for 1 (column scales go to ``quantize_tokens``). The sums are exact
     (n <= 131071). Y is T x m in ``out_dtype`` (float32, bfloat16 or float16),
     or ``out`` and its type. Asynchronous."""
-    dev = _check_device(Xq, sx, Vq, sv, out)
+    dev = _check_device(Xq, sx, Vq, sv, out, workspace)
     ldx, ldv = _matrix(Xq, "Xq", torch.int8), _matrix(Vq, "Vq", torch.int8)
     (T, n), m = Xq.shape, Vq.size(0)
     if Vq.size(1) != n:
@@ -851,9 +854,13 @@ def matmul_int8(Xq: torch.Tensor, sx: torch.Tensor, Vq: torch.Tensor,
         out = torch.empty((T, m), dtype=out_dtype, device=dev)
     else:
         _check_out(out, (T, m), out.dtype, "out")
+    L = lib()
+    need = L.bakron_matmul_int8_workspace_bytes(T, m, n)
+    ws = _workspace(need, dev, workspace) if need else None
     with torch.cuda.device(dev):
-        rc = lib().bakron_matmul_int8(code, T, m, n, _p(Xq), ldx, _p(sx), _p(Vq), ldv, _p(sv),
-                                      _p(out), _ld(out, "out"), _stream(dev))
+        rc = L.bakron_matmul_int8(code, T, m, n, _p(Xq), ldx, _p(sx), _p(Vq), ldv, _p(sv),
+                                  _p(out), _ld(out, "out"), _p(ws),
+                                  ws.numel() * ws.element_size() if need else 0, _stream(dev))
     if rc != OK:
         raise BakronError(rc, "bakron_matmul_int8")
     return out

@@ -42,6 +42,11 @@ inline bool tiles_ok(int64_t a, int64_t b) {
   return ((a + 127) / 128) * ((b + 127) / 128) <= INT_MAX;
 }
 
+inline bool int8_sizes_ok(int64_t T, int64_t m, int64_t n) {
+  return T >= 0 && m >= 0 && n >= 0 && T <= INT_MAX && m <= INT_MAX && n <= kMaxInt8Sum &&
+         tiles_ok(T, m);
+}
+
 constexpr size_t kAlign = 256;
 
 // Sizes of the input gradient: rows of planes short enough for the tile
@@ -80,14 +85,22 @@ int bakron_quantize_tokens(int xtype, int64_t T, int64_t n, const void* X, int64
   return status(launch_quantize_tokens(T, n, (const F16*)X, ldx, channel, Xq, ldq, sx, s));
 }
 
+size_t bakron_matmul_int8_workspace_bytes(int64_t T, int64_t m, int64_t n) {
+  if (!int8_sizes_ok(T, m, n)) return 0;
+  const size_t b = matmul_int8_bytes(T, m, n);
+  return b ? b + kAlign : 0;
+}
+
 int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n, const int8_t* Xq, int64_t ldx,
                        const float* sx, const int8_t* Vq, int64_t ldv, const float* sv, void* Y,
-                       int64_t ldy, void* stream) {
-  if (!type_ok(ytype) || T < 0 || m < 0 || n < 0 || T > INT_MAX || m > INT_MAX || n > kMaxInt8Sum)
-    return BAKRON_EINVAL;
+                       int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!type_ok(ytype) || !int8_sizes_ok(T, m, n)) return BAKRON_EINVAL;
   if (T == 0 || m == 0) return BAKRON_OK;
   const size_t es = type_size(ytype);
-  if (!tiles_ok(T, m) || !matrix_ok(Xq, T, n, ldx, 1) || !matrix_ok(Vq, m, n, ldv, 1) ||
+  const size_t need = matmul_int8_bytes(T, m, n);
+  if (need && (!workspace || (uintptr_t)workspace % kAlign || workspace_bytes < need))
+    return BAKRON_EINVAL;
+  if (!matrix_ok(Xq, T, n, ldx, 1) || !matrix_ok(Vq, m, n, ldv, 1) ||
       !matrix_ok(Y, T, m, ldy, es))
     return BAKRON_EINVAL;
   if (!sx || (uintptr_t)sx % 4 || (uintptr_t)sv % 4) return BAKRON_EINVAL;
@@ -96,10 +109,10 @@ int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n, const int8_t*
     return BAKRON_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (ytype == BAKRON_F32)
-    return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (float*)Y, ldy, s));
+    return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (float*)Y, ldy, workspace, s));
   if (ytype == BAKRON_BF16)
-    return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (BF16*)Y, ldy, s));
-  return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (F16*)Y, ldy, s));
+    return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (BF16*)Y, ldy, workspace, s));
+  return status(launch_matmul_int8(T, m, n, Xq, ldx, sx, Vq, ldv, sv, (F16*)Y, ldy, workspace, s));
 }
 
 size_t bakron_matmul_int8_grad_workspace_bytes(int gtype, int64_t T, int64_t m, int64_t n) {

@@ -314,10 +314,12 @@ static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
   L.p = L.wp + up256((size_t)(np * L.piece * plane_ld(d)));
   L.acc = L.p + up256((size_t)(np * T * plane_ld(L.piece)));
   L.parts = L.acc + (L.piece < V ? up256((size_t)(T * L.ldacc) * 4) : 0);
-  // both products, and dW's of the last, shorter piece
-  size_t most = plane_product_bytes(d, T);
+  // both products, of whole pieces and of the last one
+  const int n = es == 4 ? 6 : 1;
+  size_t most = 0;
   for (int64_t rows : {L.piece, L.piece ? V % L.piece : 0})
-    if (rows && plane_product_bytes(d, rows) > most) most = plane_product_bytes(d, rows);
+    for (size_t b : {plane_product_bytes(d, T, rows, n), plane_product_bytes(d, rows, T, n)})
+      if (rows && b > most) most = b;
   L.total = L.parts + most;
   return L;
 }

@@ -279,11 +279,13 @@ struct F16;
 template <typename X>
 hipError_t launch_quantize_tokens(int64_t T, int64_t n, const X* x, int64_t ldx, const float* c,
                                   int8_t* q, int64_t ldq, float* s, hipStream_t st);
-// Y (T x m) = sx sv^T (.) (Xq Vq^T), sv nullable (all 1).
+// Y (T x m) = sx sv^T (.) (Xq Vq^T), sv nullable (all 1). ws holds
+// matmul_int8_bytes.
+size_t matmul_int8_bytes(int64_t T, int64_t m, int64_t n);
 template <typename O>
 hipError_t launch_matmul_int8(int64_t T, int64_t m, int64_t n, const int8_t* Xq, int64_t ldx,
                               const float* sx, const int8_t* Vq, int64_t ldv, const float* sv, O* Y,
-                              int64_t ldy, hipStream_t s);
+                              int64_t ldy, void* ws, hipStream_t s);
 
 // ---- operands and products of 16-bit planes (plane_kernels.hip) ------------
 // A matrix held as planes for the 16-bit matrix instructions (tile_product.hpp):
@@ -318,9 +320,9 @@ struct PlaneEpilogue {
 // The sum over the plane pairs of R[r][k] C[c][k], k < K, for R's rows r < M and
 // C's rows c < N, the planes float16 (F16P) or bfloat16. R is k-major (K rows of
 // M), C too with CK; else C's rows are along k and zero from K to a multiple of 8.
-// `parts` holds plane_product_bytes(M, N) for the sums of a k that is split
-// over workgroups.
-size_t plane_product_bytes(int64_t M, int64_t N);
+// `parts` holds plane_product_bytes for the sums of a k that is split over
+// workgroups.
+size_t plane_product_bytes(int64_t M, int64_t N, int64_t K, int npairs);
 template <typename O, bool F16P, bool CK>
 hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Planes C,
                                 const PlanePairs& pairs, const PlaneEpilogue& ep, O* Y,

@@ -85,8 +85,7 @@ __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
   const int lane = threadIdx.x & 63;
   const int64_t rb = r0 + tp.wave_r() + 4 * (lane >> 4), cb = c0 + tp.wave_c() + (lane & 15);
   if (splits > 1) {
-    store_tile(tp, r0, c0, R.rows, C.rows, parts + range * stride, ldp, true,
-               [&](float a, int, int, int) { return a; });
+    store_sums(tp, r0, c0, C.rows, parts + range * stride, ldp);
     return;
   }
   const float all = (ep.alpha ? *ep.alpha : 1.0f) * ep.beta;
@@ -155,17 +154,14 @@ __global__ __launch_bounds__(256) void plane_join_kernel(int64_t M, int64_t N, i
   }
 }
 
-// Workgroups of 128 x 128 tiles that run at once: two on each of 256 CUs.
-constexpr int64_t kWorkgroups = 512;
-// A range of fewer steps costs more in its sums than it saves.
-constexpr int64_t kMinSteps = 8;
-
-static int64_t small_tiles(int64_t M, int64_t N) { return ((M + 127) / 128) * ((N + 127) / 128); }
-
-size_t plane_product_bytes(int64_t M, int64_t N) {
-  const int64_t tiles = small_tiles(M, N);
-  if (tiles == 0 || tiles * 2 > kWorkgroups) return 0;
-  return (size_t)(kWorkgroups / tiles * N * ((M + 3) / 4 * 4)) * sizeof(float);
+static bool plane_big(int64_t M, int64_t N) {
+  return ((M + 255) / 256) * ((N + 255) / 256) >= 192;
+}
+static int plane_splits(int64_t M, int64_t N, int64_t K, int npairs) {
+  return plane_big(M, N) ? 1 : split_steps(M, N, (K + 63) / 64 * npairs);
+}
+size_t plane_product_bytes(int64_t M, int64_t N, int64_t K, int npairs) {
+  return (size_t)split_words(M, N, plane_splits(M, N, K, npairs)) * 4;
 }
 
 template <class M, typename O, int BR, int BC, int WR, int WC, bool CK>
@@ -200,16 +196,11 @@ hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Plane
   if (M <= 0 || N <= 0) return hipSuccess;
   const TileOperand r = {R.w, R.ld, R.plane, M, K}, c = {C.w, C.ld, C.plane, N, K};
   const int64_t kbytes = (K + 7) / 8 * 16;  // whole 16-byte chunks: the planes' padding is zero
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= 192)
+  if (plane_big(M, N))
     return start_plane_product<Mma, O, 256, 256, 2, 4, CK>(r, c, kbytes, pairs, ep, Y, ldy, 1, parts,
                                                            s);
-  // few tiles: k split so that the chip is filled
-  const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes * pairs.n;
-  int64_t splits = kWorkgroups / small_tiles(M, N);
-  if (splits > steps / kMinSteps) splits = steps / kMinSteps;
-  return start_plane_product<Mma, O, 128, 128, 2, 2, CK>(r, c, kbytes, pairs, ep, Y, ldy,
-                                                         splits > 1 ? (int)splits : 1, parts, s);
+  return start_plane_product<Mma, O, 128, 128, 2, 2, CK>(
+      r, c, kbytes, pairs, ep, Y, ldy, plane_splits(M, N, K, pairs.n), parts, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -295,7 +286,7 @@ static GradOffsets grad_offsets(int es, int64_t T, int64_t m, int64_t n) {
   o.g = o.v + up256((size_t)(m * plane_ld(n)));
   o.unscale = o.g + up256((size_t)((es == 4 ? 3 : 1) * T * plane_ld(m)));
   o.parts = o.unscale + up256((size_t)T * 4);
-  o.total = o.parts + plane_product_bytes(n, T);
+  o.total = o.parts + plane_product_bytes(n, T, m, es == 4 ? 3 : 1);
   return o;
 }
 size_t matmul_int8_grad_bytes(int es, int64_t T, int64_t m, int64_t n) {

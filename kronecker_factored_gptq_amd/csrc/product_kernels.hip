@@ -2,6 +2,7 @@
 // product of the int8 tokens with a layer's int8 codes (the solve's V), scaled
 // per token and output channel, and its input gradient.
 #include "launch.hpp"
+#include "skinny_product.hpp"
 #include "tile_product.hpp"
 
 namespace bk {
@@ -94,11 +95,13 @@ template <typename O, int BR, int BC, int WR, int WC, bool ANY>
 __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
     TileOperand V, TileOperand Xq, int64_t n, const float* __restrict__ sx,
     const float* __restrict__ sv, O* __restrict__ Y, int64_t ldy, bool vec, unsigned nr,
-    unsigned nc) {
+    unsigned nc, int splits, int* __restrict__ parts, int64_t ldp) {
   typedef TileProduct<MmaI8, BR, BC, WR, WC> TP;
   extern __shared__ char lds[];
+  const unsigned tiles = nr * nc;
+  const int range = blockIdx.x / tiles;
   int tr, tc;
-  tile_of(blockIdx.x, nr, nc, tr, tc);
+  tile_of(blockIdx.x - range * tiles, nr, nc, tr, tc);
   const int64_t r0 = (int64_t)tr * BR, c0 = (int64_t)tc * BC;
   TP tp;
   tp.zero();
@@ -106,7 +109,13 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
     tp.run_any(V, Xq, n, r0, c0, lds);
   } else {
     const PlanePairs one = {1, 0, 0};
-    tp.run(V, Xq, n, one, r0, c0, 0, TP::steps(n, one), lds);
+    const int64_t total = TP::steps(n, one);
+    tp.run(V, Xq, n, one, r0, c0, (int)(total * range / splits),
+           (int)(total * (range + 1) / splits), lds);
+    if (splits > 1) {
+      store_sums(tp, r0, c0, Xq.rows, parts + range * Xq.rows * ldp, ldp);
+      return;
+    }
   }
   const int lane = threadIdx.x & 63;
   float st[TP::FC], sr[TP::FR][4];
@@ -132,10 +141,37 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
              [&](int a, int i, int j, int e) { return (float)a * st[j] * sr[i][e]; });
 }
 
+// The ranges' sums and the scales; four channels of one token a thread.
+template <typename O>
+__global__ __launch_bounds__(256) void join_int8_kernel(int64_t m, int64_t T, int splits,
+                                                        const int* __restrict__ parts, int64_t ldp,
+                                                        const float* __restrict__ sx,
+                                                        const float* __restrict__ sv,
+                                                        O* __restrict__ Y, int64_t ldy, bool vec) {
+  const int64_t per = ldp / 4;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= T * per) return;
+  const int64_t t = at / per, r = (at - t * per) * 4;
+  const float st = sx[t];
+  v4i a = {0, 0, 0, 0};
+  for (int k = 0; k < splits; ++k) a += *(const v4i*)(parts + (k * T + t) * ldp + r);
+  O y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    y[e] = from_f32<O>((float)a[e] * st * (sv ? sv[r + e < m ? r + e : m - 1] : 1.0f));
+  if (vec && r + 4 <= m) {
+    *(typename Vec4<O>::type*)(Y + t * ldy + r) = __builtin_bit_cast(typename Vec4<O>::type, y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r + e < m) Y[t * ldy + r + e] = y[e];
+  }
+}
+
 template <typename O, int BR, int BC, int WR, int WC, bool ANY>
 static hipError_t start_matmul_int8(const TileOperand& V, const TileOperand& X, int64_t n,
                                     const float* sx, const float* sv, O* Y, int64_t ldy,
-                                    hipStream_t s) {
+                                    int splits, int* parts, hipStream_t s) {
   typedef TileProduct<MmaI8, BR, BC, WR, WC> TP;
   auto* k = matmul_int8_kernel<O, BR, BC, WR, WC, ANY>;
   constexpr int lds = TP::kLds;
@@ -145,23 +181,122 @@ static hipError_t start_matmul_int8(const TileOperand& V, const TileOperand& X, 
     if (e != hipSuccess) return e;
   }
   const int64_t nr = (V.rows + BR - 1) / BR, nc = (X.rows + BC - 1) / BC;
-  hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc)), dim3(TP::kThreads), lds, s, V, X, n, sx, sv, Y,
-                     ldy, vec4_ok(Y, ldy), (unsigned)nr, (unsigned)nc);
+  const int64_t ldp = (V.rows + 3) / 4 * 4;
+  const bool vec = vec4_ok(Y, ldy);
+  hipLaunchKernelGGL(k, dim3((unsigned)(nr * nc * splits)), dim3(TP::kThreads), lds, s, V, X, n, sx,
+                     sv, Y, ldy, vec, (unsigned)nr, (unsigned)nc, splits, parts, ldp);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t per = ldp / 4;
+  hipLaunchKernelGGL(join_int8_kernel<O>, dim3((unsigned)((X.rows * per + 255) / 256)), dim3(256), 0,
+                     s, V.rows, X.rows, splits, parts, ldp, sx, sv, Y, ldy, vec);
   return hipGetLastError();
+}
+
+// Few tokens: the codes are read once, by workgroups of 16 RT channels.
+template <typename O, int RT, int NT, bool ANY>
+__global__ __launch_bounds__(512) void skinny_int8_kernel(TileOperand V, TileOperand Xq, int64_t n,
+                                                          const float* __restrict__ sx,
+                                                          const float* __restrict__ sv,
+                                                          O* __restrict__ Y, int64_t ldy, bool vec) {
+  typedef SkinnyProduct<MmaI8, RT, NT, RT == 1 ? 4 : 2, ANY> SP;
+  __shared__ __attribute__((aligned(16))) char lds[SP::kLds];
+  const int64_t c0 = (int64_t)blockIdx.y * SP::kCols;
+  const TileOperand X = {Xq.p + c0 * Xq.ld, Xq.ld, 0, Xq.rows - c0, 0};
+  const int64_t r0 = (int64_t)blockIdx.x * SP::kRows;
+  // the scales are on their way while the product is formed
+  const int64_t t = c0 + SP::tile_c(), r = r0 + SP::tile_r();
+  const bool mine = SP::has_tile() && t < Xq.rows && r < V.rows;
+  float st = 0.0f, sr[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+  if (mine) {
+    st = sx[t];
+    if (sv) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sr[e] = sv[r + e < V.rows ? r + e : r];
+    }
+  }
+  SP::run(V, X, n, r0, lds, [&](v4i sum) {
+    if (!mine) return;
+    O y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = from_f32<O>((float)sum[e] * st * sr[e]);
+    if (vec && r + 4 <= V.rows) {
+      *(typename Vec4<O>::type*)(Y + t * ldy + r) =
+          __builtin_bit_cast(typename Vec4<O>::type, y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r + e < V.rows) Y[t * ldy + r + e] = y[e];
+    }
+  });
+}
+
+template <typename O, bool ANY>
+static hipError_t start_skinny_int8(const TileOperand& V, const TileOperand& X, int64_t n,
+                                    const float* sx, const float* sv, O* Y, int64_t ldy,
+                                    hipStream_t s) {
+  const bool vec = vec4_ok(Y, ldy);
+  // several tiles of tokens: 32 channels a workgroup where that still gives every
+  // CU one, since the tokens are then read half as often (14336 x 4096, 32 tokens:
+  // 23 us against 28; 16 tokens: 18 against 19; one: 15 against 13.5)
+  const int nt = X.rows > 48 ? 4 : (int)((X.rows + 15) / 16);
+  const bool wide = V.rows >= 32 * 256 && X.rows > 8;
+#define BK_SKINNY(RT, NT)                                                                     \
+  hipLaunchKernelGGL((skinny_int8_kernel<O, RT, NT, ANY>),                                    \
+                     dim3((unsigned)((V.rows + 16 * RT - 1) / (16 * RT)),                     \
+                          (unsigned)((X.rows + 16 * NT - 1) / (16 * NT))),                    \
+                     dim3(512), 0, s, V, X, n, sx, sv, Y, ldy, vec)
+  if (wide) switch (nt) {
+      case 1: BK_SKINNY(2, 1); break;
+      case 2: BK_SKINNY(2, 2); break;
+      case 3: BK_SKINNY(2, 3); break;
+      default: BK_SKINNY(2, 4);
+    }
+  else switch (nt) {
+      case 1: BK_SKINNY(1, 1); break;
+      case 2: BK_SKINNY(1, 2); break;
+      case 3: BK_SKINNY(1, 3); break;
+      default: BK_SKINNY(1, 4);
+    }
+#undef BK_SKINNY
+  return hipGetLastError();
+}
+
+// The most tokens the skinny kernel takes. It reads the tokens once for every 16
+// or 32 channels, so the more codes there are the sooner tiles of 128 channels are
+// faster (4096 x 4096, 64 tokens: 12.3 us against 12.6; 8192 x 8192, 48: 25 against
+// 21, 16: 17 against 18; 28672 x 4096, 16: 34 against 28, 4: 25).
+static int64_t skinny_tokens(int64_t m, int64_t n) {
+  return m * n <= (1 << 24) ? 64 : m * n <= (1 << 26) ? 16 : 8;
+}
+
+static bool int8_big(int64_t T, int64_t m) {
+  return ((m + 255) / 256) * ((T + 255) / 256) >= 192;
+}
+static int int8_splits(int64_t T, int64_t m, int64_t n) {
+  if (T <= skinny_tokens(m, n) || int8_big(T, m)) return 1;
+  return split_steps(m, T, (n + kStepBytes - 1) / kStepBytes);
+}
+size_t matmul_int8_bytes(int64_t T, int64_t m, int64_t n) {
+  return (size_t)split_words(m, T, int8_splits(T, m, n)) * 4;
 }
 
 template <typename O>
 hipError_t launch_matmul_int8(int64_t T, int64_t m, int64_t n, const int8_t* Xq, int64_t ldx,
                               const float* sx, const int8_t* Vq, int64_t ldv, const float* sv, O* Y,
-                              int64_t ldy, hipStream_t s) {
+                              int64_t ldy, void* ws, hipStream_t s) {
   if (T <= 0 || m <= 0) return hipSuccess;
   const TileOperand V = {(const char*)Vq, ldv, 0, m, 0}, X = {(const char*)Xq, ldx, 0, T, 0};
   const bool direct = tile_direct(V, n) && tile_direct(X, n);
-  if (!direct) return start_matmul_int8<O, 128, 128, 2, 2, true>(V, X, n, sx, sv, Y, ldy, s);
-  const int64_t big = ((m + 255) / 256) * ((T + 255) / 256);
-  if (big >= 192)
-    return start_matmul_int8<O, 256, 256, 2, 4, false>(V, X, n, sx, sv, Y, ldy, s);
-  return start_matmul_int8<O, 128, 128, 2, 2, false>(V, X, n, sx, sv, Y, ldy, s);
+  if (T <= skinny_tokens(m, n))
+    return direct ? start_skinny_int8<O, false>(V, X, n, sx, sv, Y, ldy, s)
+                  : start_skinny_int8<O, true>(V, X, n, sx, sv, Y, ldy, s);
+  if (!direct)
+    return start_matmul_int8<O, 128, 128, 2, 2, true>(V, X, n, sx, sv, Y, ldy, 1, nullptr, s);
+  if (int8_big(T, m))
+    return start_matmul_int8<O, 256, 256, 2, 4, false>(V, X, n, sx, sv, Y, ldy, 1, nullptr, s);
+  return start_matmul_int8<O, 128, 128, 2, 2, false>(V, X, n, sx, sv, Y, ldy, int8_splits(T, m, n),
+                                                     (int*)ws, s);
 }
 
 #define BK_INST_Q(X)                                                                        \
@@ -175,7 +310,7 @@ BK_INST_Q(F16)
 #define BK_INST_O(O)                                                                          \
   template hipError_t launch_matmul_int8<O>(int64_t, int64_t, int64_t, const int8_t*,         \
                                             int64_t, const float*, const int8_t*, int64_t,    \
-                                            const float*, O*, int64_t, hipStream_t);
+                                            const float*, O*, int64_t, void*, hipStream_t);
 BK_INST_O(float)
 BK_INST_O(BF16)
 BK_INST_O(F16)

@@ -87,6 +87,30 @@ __device__ inline void tile_of(unsigned b, unsigned nr, unsigned nc, int& tr, in
   tc = (int)(first + in % width);
 }
 
+// 16 bytes of a row from byte k on, of any alignment; past kbytes they are zero
+// (elements of E bytes, each wholly inside or outside).
+template <int E>
+__device__ inline v4i load_any(const char* row, int64_t k, int64_t kbytes) {
+  v4i v = {0, 0, 0, 0};
+  if (k + 16 <= kbytes) {
+    __builtin_memcpy(&v, row + k, 16);
+  } else {
+    unsigned w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; e += E)
+      if (k + e < kbytes) {
+        unsigned x;
+        if (E == 1)
+          x = *(const unsigned char*)(row + k + e);
+        else
+          x = *(const unsigned short*)(row + k + e);
+        w[e / 4] |= x << (8 * (e % 4));
+      }
+    v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+  }
+  return v;
+}
+
 // How an operand lies in memory and in LDS: its rows along k (kbytes of k in
 // each), or k-major (k its rows, `ld` apart, its tile's rows side by side).
 template <class M, int BR, int BC, int WR, int WC, bool RK = false, bool CK = false>
@@ -389,29 +413,8 @@ struct TileProduct {
   }
 
   // The same for operands of any alignment, stride and k (M::kElem-sized
-  // elements): a step is read to registers while the one before is computed,
-  // partial chunks element by element, and then written to LDS.
-  __device__ static inline v4i load_any(const char* row, int64_t k, int64_t kbytes) {
-    v4i v = {0, 0, 0, 0};
-    if (k + 16 <= kbytes) {
-      __builtin_memcpy(&v, row + k, 16);
-    } else {
-      unsigned w[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 16; e += M::kElem)
-        if (k + e < kbytes) {
-          unsigned x;
-          if (M::kElem == 1)
-            x = *(const unsigned char*)(row + k + e);
-          else
-            x = *(const unsigned short*)(row + k + e);
-          w[e / 4] |= x << (8 * (e % 4));
-        }
-      v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-    }
-    return v;
-  }
-
+  // elements): a step is read to registers while the one before is computed, and
+  // then written to LDS.
   __device__ inline void run_any(const TileOperand& R, const TileOperand& C, int64_t kbytes,
                                  int64_t r0, int64_t c0, char* lds) {
     const int tid = threadIdx.x;
@@ -423,12 +426,12 @@ struct TileProduct {
 #pragma unroll
       for (int u = 0; u < NR; ++u) {
         const int e = u * kThreads + tid, r = e >> 3;
-        vr[u] = load_any(R.p + (r0 + (r < rows ? r : rows - 1)) * R.ld, k + (e & 7) * 16, kbytes);
+        vr[u] = load_any<M::kElem>(R.p + (r0 + (r < rows ? r : rows - 1)) * R.ld, k + (e & 7) * 16, kbytes);
       }
 #pragma unroll
       for (int u = 0; u < NC; ++u) {
         const int e = u * kThreads + tid, r = e >> 3;
-        vc[u] = load_any(C.p + (c0 + (r < cols ? r : cols - 1)) * C.ld, k + (e & 7) * 16, kbytes);
+        vc[u] = load_any<M::kElem>(C.p + (c0 + (r < cols ? r : cols - 1)) * C.ld, k + (e & 7) * 16, kbytes);
       }
     };
     auto sstore = [&](char* b) {
@@ -530,6 +533,52 @@ __device__ inline void store_tile(const TP& tp, int64_t r0, int64_t c0, int64_t 
           if (cb + j * 16 < cols && rb + i * 16 + e < rows)
             Y[(cb + j * 16) * ldy + rb + i * 16 + e] = from_f32<O>(f(tp.acc[i][j][e], i, j, e));
   }
+}
+
+// A tile's sums as they are to parts[c][r .. r + 3], rows ldp (a multiple of four,
+// at least `rows`) 4-byte words apart, 16-byte aligned.
+template <class TP>
+__device__ inline void store_sums(const TP& tp, int64_t r0, int64_t c0, int64_t cols, void* parts,
+                                  int64_t ldp) {
+  const int lane = threadIdx.x & 63;
+  const int64_t rb = r0 + tp.wave_r() + 4 * (lane >> 4), cb = c0 + tp.wave_c() + (lane & 15);
+#pragma unroll
+  for (int j = 0; j < TP::FC; ++j) {
+    if (cb + j * 16 >= cols) continue;
+#pragma unroll
+    for (int i = 0; i < TP::FR; ++i)
+      if (rb + i * 16 < ldp)
+        *(typename TP::acc_t*)((int*)parts + (cb + j * 16) * ldp + rb + i * 16) = tp.acc[i][j];
+  }
+}
+
+// A product of few tiles is split along k over workgroups, each range of steps
+// summed apart and the ranges joined by a second kernel. Of 128 x 128 tiles two
+// workgroups run on each of 256 CUs; a range's steps follow one another at 0.5 us,
+// and its sums are written and read again at 2.4 bytes a ps with 3 us for the
+// second kernel (measured over 1024 x 2048 to 28672 x 4096 and 17 to 256
+// columns: 4096 x 14336 with 128 columns 58 us in one range, 28 in 16; 14336 x 4096
+// with 256 columns 24 us in one, 38 in 2). The number of ranges that takes least.
+constexpr int64_t kWorkgroups = 512;
+inline int64_t tiles128(int64_t M, int64_t N) { return ((M + 127) / 128) * ((N + 127) / 128); }
+inline int split_steps(int64_t M, int64_t N, int64_t steps) {
+  if (M <= 0 || N <= 0) return 1;
+  const int64_t most = kWorkgroups / tiles128(M, N);
+  const double word = (double)M * (double)N * 8 / 2.4e6;
+  int best = 1;
+  double least = 0.5 * (double)steps;
+  for (int n = 2; n <= most && n <= steps / 2; ++n) {
+    const double t = 0.5 * (double)((steps + n - 1) / n) + 3 + n * word;
+    if (t < least) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
+}
+// words of the ranges' sums, rows of M padded to four
+inline int64_t split_words(int64_t M, int64_t N, int splits) {
+  return splits > 1 ? splits * N * ((M + 3) / 4 * 4) : 0;
 }
 
 // ---- planes -----------------------------------------------------------------

@@ -36,10 +36,11 @@ def test_quantize_tokens_empty():
 
 
 def _matmul(**kw):
-    a = dict(t=bk.F32, T=3, m=5, n=4, X=at(1), ldx=4, sx=at(2), V=at(3), ldv=4, sv=at(4), Y=at(5), ldy=5)
+    a = dict(t=bk.F32, T=3, m=5, n=4, X=at(1), ldx=4, sx=at(2), V=at(3), ldv=4, sv=at(4), Y=at(5), ldy=5, ws=at(9),
+             wsb=1 << 40)
     a.update(kw)
     return bk.lib().bakron_matmul_int8(a["t"], a["T"], a["m"], a["n"], a["X"], a["ldx"], a["sx"], a["V"], a["ldv"],
-                                       a["sv"], a["Y"], a["ldy"], None)
+                                       a["sv"], a["Y"], a["ldy"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -52,6 +53,9 @@ def _matmul(**kw):
     dict(T=(1 << 31) - 1, m=(1 << 31) - 1, ldy=(1 << 31) - 1),
     # the output over an input
     dict(Y=at(1)), dict(Y=at(2)), dict(Y=at(3)), dict(Y=at(4)),
+    # a call that needs a workspace
+    dict(T=100, n=8192, ldx=8192, ldv=8192, ws=None), dict(T=100, n=8192, ldx=8192, ldv=8192, wsb=100),
+    dict(T=100, n=8192, ldx=8192, ldv=8192, ws=ctypes.c_void_p(0x900008)),
 ])
 def test_matmul_int8_rejects_bad_arguments(bad):
     assert _matmul(**bad) == bk.EINVAL
@@ -60,6 +64,9 @@ def test_matmul_int8_rejects_bad_arguments(bad):
 def test_matmul_int8_empty():
     assert _matmul(T=0, X=None, sx=None, Y=None) == bk.OK
     assert _matmul(m=0, V=None, sv=None, Y=None) == bk.OK
+    q = bk.lib().bakron_matmul_int8_workspace_bytes
+    assert q(1, 4096, 4096) == q(8192, 14336, 4096) == q(0, 5, 5) == q(5, 0, 5) == q(-1, 5, 5) == 0
+    assert 0 < q(100, 4096, 8192) <= 512 * 128 * 128 * 4 + 256
 
 
 def _grad(**kw):
