@@ -214,15 +214,16 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _check_device(*ts):
-    dev = None
+    dev = index = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()
+        if i < 0 or not t.is_cuda:
             raise ValueError("all tensors must be on the GPU")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
+            dev, index = t.device, i
+        elif i != index:
             raise ValueError("all tensors must be on one device")
     return dev
 
@@ -775,35 +776,73 @@ _FLOATS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 def _ft(dtype: torch.dtype, name: str) -> int:
     """The element type code of the calls beside the solve."""
-    if dtype not in _FLOATS:
+    code = _FLOATS.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
-    return _FLOATS[dtype]
+    return code
 
 
-def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None) -> int:
-    """The leading dimension of a 2-D row-major input whose rows may be any
-    distance apart (at least their length)."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
+def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None):
+    """(rows, columns, leading dimension) of a 2-D row-major operand whose rows
+    may be any distance apart (at least their length)."""
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
     if rows <= 1:
-        return max(cols, 1)
-    if t.stride(0) < cols:
+        return rows, cols, max(cols, 1)
+    if ld < cols:
         raise ValueError(f"{name} rows overlap (leading dimension below the row length)")
-    return max(int(t.stride(0)), 1)
+    return rows, cols, max(ld, 1)
 
 
-def _vector(t: Optional[torch.Tensor], n: int, name: str, dtype: torch.dtype = torch.float32) -> None:
+def _vector(t: Optional[torch.Tensor], n: int, name: str,
+            dtype: torch.dtype = torch.float32) -> Optional[int]:
+    """The address of a contiguous vector of length n (None for None)."""
     if t is None:
-        return
+        return None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of length {n}")
+    return t.data_ptr()
+
+
+def _output(t: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, name: str, dev):
+    """A caller's output, checked, or a new one, and its leading dimension."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=dtype, device=dev), max(cols, 1)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    return t, _matrix(t, name)[2]
+
+
+def _scratch(nbytes: int, dev, ws: Optional[torch.Tensor]):
+    """(tensor, address, size) of a workspace of at least nbytes; nothing for 0."""
+    if not nbytes:
+        return None, None, 0
+    t = _workspace(nbytes, dev, ws)
+    return t, t.data_ptr(), t.numel() * t.element_size()
+
+
+def _call(what: str, dev, f, *args) -> None:
+    """f(*args, the current stream) on `dev`, which is made the current device if
+    it is not."""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, stream)
+    if rc != OK:
+        raise BakronError(rc, what)
 
 
 def quantize_tokens(X: torch.Tensor, channel_scales: Optional[torch.Tensor] = None):
@@ -815,19 +854,15 @@ def quantize_tokens(X: torch.Tensor, channel_scales: Optional[torch.Tensor] = No
     bytes) and sx (float32, T). Asynchronous."""
     dev = _check_device(X, channel_scales)
     code = _ft(X.dtype, "X")
-    ldx = _matrix(X, "X")
-    T, n = X.shape
-    _vector(channel_scales, n, "channel_scales")
+    T, n, ldx = _matrix(X, "X")
+    c = _vector(channel_scales, n, "channel_scales")
     ldq = (n + 15) // 16 * 16
     Xq = torch.empty((T, ldq), dtype=torch.int8, device=dev)
     if ldq != n:
         Xq = Xq[:, :n]
     sx = torch.empty(T, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        rc = lib().bakron_quantize_tokens(code, T, n, _p(X), ldx, _p(channel_scales), _p(Xq), ldq,
-                                          _p(sx), _stream(dev))
-    if rc != OK:
-        raise BakronError(rc, "bakron_quantize_tokens")
+    _call("bakron_quantize_tokens", dev, lib().bakron_quantize_tokens, code, T, n, X.data_ptr(), ldx, c,
+          Xq.data_ptr(), ldq, sx.data_ptr())
     return Xq, sx
 
 
@@ -843,26 +878,18 @@ def matmul_int8(Xq: torch.Tensor, sx: torch.Tensor, Vq: torch.Tensor,
     (n <= 131071). Y is T x m in ``out_dtype`` (float32, bfloat16 or float16),
     or ``out`` and its type. Asynchronous."""
     dev = _check_device(Xq, sx, Vq, sv, out, workspace)
-    ldx, ldv = _matrix(Xq, "Xq", torch.int8), _matrix(Vq, "Vq", torch.int8)
-    (T, n), m = Xq.shape, Vq.size(0)
-    if Vq.size(1) != n:
-        raise ValueError(f"Xq and Vq must have rows of one length, got {n} and {Vq.size(1)}")
-    _vector(sx, T, "sx")
-    _vector(sv, m, "sv")
-    code = _ft(out_dtype if out is None else out.dtype, "out_dtype")
-    if out is None:
-        out = torch.empty((T, m), dtype=out_dtype, device=dev)
-    else:
-        _check_out(out, (T, m), out.dtype, "out")
+    T, n, ldx = _matrix(Xq, "Xq", torch.int8)
+    m, nv, ldv = _matrix(Vq, "Vq", torch.int8)
+    if nv != n:
+        raise ValueError(f"Xq and Vq must have rows of one length, got {n} and {nv}")
+    px, pv = _vector(sx, T, "sx"), _vector(sv, m, "sv")
+    dtype = out_dtype if out is None else out.dtype
+    code = _ft(dtype, "out_dtype")
+    out, ldy = _output(out, T, m, dtype, "out", dev)
     L = lib()
-    need = L.bakron_matmul_int8_workspace_bytes(T, m, n)
-    ws = _workspace(need, dev, workspace) if need else None
-    with torch.cuda.device(dev):
-        rc = L.bakron_matmul_int8(code, T, m, n, _p(Xq), ldx, _p(sx), _p(Vq), ldv, _p(sv),
-                                  _p(out), _ld(out, "out"), _p(ws),
-                                  ws.numel() * ws.element_size() if need else 0, _stream(dev))
-    if rc != OK:
-        raise BakronError(rc, "bakron_matmul_int8")
+    ws, pw, nw = _scratch(L.bakron_matmul_int8_workspace_bytes(T, m, n), dev, workspace)
+    _call("bakron_matmul_int8", dev, L.bakron_matmul_int8, code, T, m, n, Xq.data_ptr(), ldx, px,
+          Vq.data_ptr(), ldv, pv, out.data_ptr(), ldy, pw, nw)
     return out
 
 
@@ -877,38 +904,30 @@ def matmul_int8_grad(G: torch.Tensor, Vq: torch.Tensor, sv: Optional[torch.Tenso
     (length n) are float32, None for 1. Asynchronous."""
     dev = _check_device(G, Vq, sv, channel_scales, workspace, out)
     code = _ft(G.dtype, "G")
-    ldg, ldv = _matrix(G, "G"), _matrix(Vq, "Vq", torch.int8)
-    (T, m), n = G.shape, Vq.size(1)
-    if Vq.size(0) != m:
-        raise ValueError(f"G must have a column for each row of Vq, got {m} and {Vq.size(0)}")
-    _vector(sv, m, "sv")
-    _vector(channel_scales, n, "channel_scales")
-    if out is None:
-        out = torch.empty((T, n), dtype=G.dtype, device=dev)
-    else:
-        _check_out(out, (T, n), G.dtype, "out")
+    T, m, ldg = _matrix(G, "G")
+    mv, n, ldv = _matrix(Vq, "Vq", torch.int8)
+    if mv != m:
+        raise ValueError(f"G must have a column for each row of Vq, got {m} and {mv}")
+    pv, pc = _vector(sv, m, "sv"), _vector(channel_scales, n, "channel_scales")
+    out, ldx = _output(out, T, n, G.dtype, "out", dev)
     L = lib()
-    ws = _workspace(L.bakron_matmul_int8_grad_workspace_bytes(code, T, m, n), dev, workspace)
-    with torch.cuda.device(dev):
-        rc = L.bakron_matmul_int8_grad(code, T, m, n, _p(G), ldg, _p(Vq), ldv, _p(sv),
-                                       _p(channel_scales), _p(out), _ld(out, "out"), _p(ws),
-                                       ws.numel() * ws.element_size(), _stream(dev))
-    if rc != OK:
-        raise BakronError(rc, "bakron_matmul_int8_grad")
+    ws, pw, nw = _scratch(L.bakron_matmul_int8_grad_workspace_bytes(code, T, m, n), dev, workspace)
+    _call("bakron_matmul_int8_grad", dev, L.bakron_matmul_int8_grad, code, T, m, n, G.data_ptr(), ldg,
+          Vq.data_ptr(), ldv, pv, pc, out.data_ptr(), ldx, pw, nw)
     return out
 
 
 def _entropy_args(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor):
-    """(type code, ldx, ldw, T, d, V) of the cross entropy's operands."""
+    """(type, T, d, V, X, ldx, W, ldw, targets) of the cross entropy's operands."""
     code = _ft(X.dtype, "X")
-    ldx, ldw = _matrix(X, "X"), _matrix(W, "W", X.dtype)
-    (T, d), V = X.shape, W.size(0)
-    if W.size(1) != d:
-        raise ValueError(f"X and W must have rows of one length, got {d} and {W.size(1)}")
+    T, d, ldx = _matrix(X, "X")
+    V, dw, ldw = _matrix(W, "W", X.dtype)
+    if dw != d:
+        raise ValueError(f"X and W must have rows of one length, got {d} and {dw}")
     if V < 1:
         raise ValueError("W must have a row")
-    _vector(targets, T, "targets", torch.int64)
-    return code, ldx, ldw, T, d, V
+    y = _vector(targets, T, "targets", torch.int64)
+    return code, T, d, V, X.data_ptr(), ldx, W.data_ptr(), ldw, y
 
 
 def cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
@@ -920,16 +939,12 @@ def cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
     without a target, whose loss is 0. Returns loss and lse = log sum exp of the
     logits, float32 vectors of length T. Asynchronous."""
     dev = _check_device(X, W, targets, workspace)
-    code, ldx, ldw, T, d, V = _entropy_args(X, W, targets)
-    loss = torch.empty(T, dtype=torch.float32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    args = _entropy_args(X, W, targets)
+    code, T, d, V = args[:4]
+    loss, lse = torch.empty((2, T), dtype=torch.float32, device=dev).unbind(0)
     L = lib()
-    ws = _workspace(L.bakron_cross_entropy_workspace_bytes(code, T, d, V), dev, workspace)
-    with torch.cuda.device(dev):
-        rc = L.bakron_cross_entropy(code, T, d, V, _p(X), ldx, _p(W), ldw, _p(targets), _p(loss),
-                                    _p(lse), _p(ws), ws.numel() * ws.element_size(), _stream(dev))
-    if rc != OK:
-        raise BakronError(rc, "bakron_cross_entropy")
+    ws, pw, nw = _scratch(L.bakron_cross_entropy_workspace_bytes(code, T, d, V), dev, workspace)
+    _call("bakron_cross_entropy", dev, L.bakron_cross_entropy, *args, loss.data_ptr(), lse.data_ptr(), pw, nw)
     return loss, lse
 
 
@@ -942,19 +957,16 @@ def cross_entropy_grad(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, 
     targets) for their mean). The rows of dX are the output-side samples of the
     layer below (``gram`` takes them in float32). Asynchronous."""
     dev = _check_device(X, W, targets, lse, g, workspace)
-    code, ldx, ldw, T, d, V = _entropy_args(X, W, targets)
-    _vector(lse, T, "lse")
-    _vector(g, T, "g")
+    args = _entropy_args(X, W, targets)
+    code, T, d, V = args[:4]
+    pl, pg = _vector(lse, T, "lse"), _vector(g, T, "g")
     dX = torch.empty((T, d), dtype=X.dtype, device=dev) if need_dX else None
     dW = torch.empty((V, d), dtype=X.dtype, device=dev) if need_dW else None
     L = lib()
-    ws = _workspace(L.bakron_cross_entropy_grad_workspace_bytes(code, T, d, V), dev, workspace)
-    with torch.cuda.device(dev):
-        rc = L.bakron_cross_entropy_grad(code, T, d, V, _p(X), ldx, _p(W), ldw, _p(targets), _p(lse),
-                                         _p(g), _p(dX), max(d, 1), _p(dW), max(d, 1), _p(ws),
-                                         ws.numel() * ws.element_size(), _stream(dev))
-    if rc != OK:
-        raise BakronError(rc, "bakron_cross_entropy_grad")
+    ws, pw, nw = _scratch(L.bakron_cross_entropy_grad_workspace_bytes(code, T, d, V), dev, workspace)
+    _call("bakron_cross_entropy_grad", dev, L.bakron_cross_entropy_grad, *args, pl, pg,
+          None if dX is None else dX.data_ptr(), max(d, 1), None if dW is None else dW.data_ptr(),
+          max(d, 1), pw, nw)
     return dX, dW
 
 
