@@ -523,7 +523,7 @@ int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n,
  * Products are exact (for F32 to 2^-21 of each term), sums and exponentials
  * float32. Logits of -inf add nothing; a token with a logit of +inf or NaN gets
  * NaN (its loss is 0 all the same without a target). For F32 an infinity in X or
- * W makes the logits it enters NaN.
+ * W may make the logits it enters NaN.
  *
  * bakron_cross_entropy_grad: with g[t] the gradient of loss[t] (1 / T or 1 /
  * (number of targets) for a mean) and lse as the forward call gave it,

@@ -17,6 +17,7 @@
 #include <initializer_list>
 
 #include "launch.hpp"
+#include "skinny_product.hpp"
 #include "tile_product.hpp"
 
 namespace bk {
@@ -25,17 +26,20 @@ namespace {
 
 template <typename X> struct Kind;
 template <> struct Kind<float> {
-  typedef MmaBF16 mma;
+  typedef MmaBF16 mma;  // of the planes
+  typedef MmaF32 whole;
   static constexpr int split = kBF16x3;
   static constexpr bool f16 = false;
 };
 template <> struct Kind<BF16> {
   typedef MmaBF16 mma;
+  typedef MmaBF16 whole;
   static constexpr int split = kBF16x1;
   static constexpr bool f16 = false;
 };
 template <> struct Kind<F16> {
   typedef MmaF16 mma;
+  typedef MmaF16 whole;
   static constexpr int split = kF16x1;
   static constexpr bool f16 = true;
 };
@@ -126,21 +130,73 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_kernel(
   }
 }
 
-// 16 tokens per workgroup, 16 threads to each, the parts in a fixed order.
+// The same for few tokens, bound by reading W once: part blockIdx.x * RT + i are
+// its 16 rows of that number.
+template <class M, int RT, int NT, bool ANY>
+__global__ __launch_bounds__(512) void skinny_entropy_kernel(TileOperand W, TileOperand X,
+                                                             int64_t kbytes,
+                                                             const int64_t* __restrict__ y,
+                                                             MaxSum* __restrict__ parts,
+                                                             float* __restrict__ zy) {
+  typedef SkinnyProduct<M, RT, NT, RT == 1 ? 4 : 2, ANY> SP;
+  __shared__ __attribute__((aligned(16))) char lds[SP::kLds];
+  const int64_t r0 = (int64_t)blockIdx.x * SP::kRows, r = r0 + SP::tile_r();
+  const int64_t t = SP::tile_c(), T = X.rows;
+  const int64_t yt = SP::has_tile() && t < T ? y[t] : -1;
+  SP::run(W, X, kbytes, r0, lds, [&](f32x4 z) {
+    const int left = W.rows - r < 4 ? (int)(W.rows - r) : 4;
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) m = fmaxf(m, z[e]);
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) s += exp_of(z[e] - base);
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (t >= T) return;
+    const int64_t part = r / 16;
+    if ((threadIdx.x & 63) < 16 && part * 16 < W.rows) parts[part * T + t] = {m, s};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left && yt == r + e) zy[t] = z[e];
+  });
+}
+
+// TX tokens per workgroup, 256 / TX threads to each, the parts in a fixed order.
+template <int TX>
 __global__ __launch_bounds__(256) void entropy_join_kernel(
     int64_t T, int64_t V, int64_t nparts, const MaxSum* __restrict__ parts,
     const float* __restrict__ zy, const int64_t* __restrict__ y, float* __restrict__ loss,
     float* __restrict__ lse) {
-  __shared__ MaxSum red[16][16];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t t = (int64_t)blockIdx.x * 16 + tx;
+  constexpr int TY = 256 / TX;
+  __shared__ MaxSum red[256];
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int64_t t = (int64_t)blockIdx.x * TX + tx;
   MaxSum a = {-__builtin_inff(), 0.0f};
-  if (t < T)
-    for (int64_t p = ty; p < nparts; p += 16) a = join(a, parts[p * T + t]);
-  red[ty][tx] = a;
+  if (t < T) {
+    int64_t p = ty;
+    for (; p + 3 * TY < nparts; p += 4 * TY) {  // four loads on their way at once
+      MaxSum b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) b[k] = parts[(p + k * TY) * T + t];
+      a = join(a, join(join(b[0], b[1]), join(b[2], b[3])));
+    }
+    for (; p < nparts; p += TY) a = join(a, parts[p * T + t]);
+  }
+  red[threadIdx.x] = a;
   __syncthreads();
+#pragma unroll
+  for (int k = TY / 2; k > 0; k /= 2) {
+    if (ty < k) red[threadIdx.x] = join(red[threadIdx.x], red[threadIdx.x + k * TX]);
+    __syncthreads();
+  }
   if (ty == 0 && t < T) {
-    for (int k = 1; k < 16; ++k) a = join(a, red[k][tx]);
+    a = red[tx];
     const float l = a.m + logf(a.s);
     lse[t] = l;
     loss[t] = y[t] >= 0 && y[t] < V ? l - zy[t] : 0.0f;
@@ -241,6 +297,24 @@ static hipError_t start_entropy(const TileOperand& W, const TileOperand& X, int6
   return hipGetLastError();
 }
 
+template <class M, bool ANY>
+static hipError_t start_skinny_entropy(const TileOperand& W, const TileOperand& X, int64_t kbytes,
+                                       const int64_t* y, MaxSum* parts, float* zy, hipStream_t s) {
+  const int nt = (int)((X.rows + 15) / 16);
+#define BK_SKINNY(RT, NT)                                                            \
+  hipLaunchKernelGGL((skinny_entropy_kernel<M, RT, NT, ANY>),                        \
+                     dim3((unsigned)((W.rows + 16 * RT - 1) / (16 * RT))), dim3(512), 0, s, W, X, \
+                     kbytes, y, parts, zy)
+  switch (nt) {
+    case 1: BK_SKINNY(1, 1); break;
+    case 2: BK_SKINNY(2, 2); break;
+    case 3: BK_SKINNY(2, 3); break;
+    default: BK_SKINNY(2, 4);
+  }
+#undef BK_SKINNY
+  return hipGetLastError();
+}
+
 template <class M, int KIND, int BR, int BC, int WR, int WC, bool ANY>
 static hipError_t start_entropy_diff(const TileOperand& W, const TileOperand& X, int64_t kbytes,
                                      const PlanePairs& pairs, const int64_t* y, int64_t V,
@@ -277,6 +351,9 @@ static int64_t diff_piece(int es, int64_t T, int64_t d, int64_t V) {
   return p < V ? p : V;
 }
 
+// The most tokens the forward's skinny kernel takes.
+constexpr int64_t kSkinnyTokens = 64;
+
 // Offsets into the workspaces.
 struct EntropyLayout {
   size_t parts, zy, xp, wp, total;
@@ -284,12 +361,14 @@ struct EntropyLayout {
 static EntropyLayout entropy_layout(int es, int64_t T, int64_t d, int64_t V) {
   EntropyLayout L;
   L.parts = 0;
-  // two waves of rows in each tile, of at least 128 rows
-  const int64_t nparts = 2 * ((V + 127) / 128) + 2 * ((V + 255) / 256);
+  // two waves of rows in each tile, of at least 128 rows; or every 16 rows
+  const bool skinny = T <= kSkinnyTokens;
+  const int64_t nparts = skinny ? (V + 15) / 16 : 2 * ((V + 127) / 128);
   L.zy = L.parts + up256((size_t)(nparts * T) * sizeof(MaxSum));
   L.xp = L.zy + up256((size_t)T * 4);
-  L.wp = L.xp + (es == 4 ? (size_t)(3 * T * plane_ld(d)) : 0);
-  L.total = L.wp + (es == 4 ? (size_t)(3 * plane_piece(d, V) * plane_ld(d)) : 0);
+  const bool planes = es == 4 && !skinny;
+  L.wp = L.xp + (planes ? (size_t)(3 * T * plane_ld(d)) : 0);
+  L.total = L.wp + (planes ? (size_t)(3 * plane_piece(d, V) * plane_ld(d)) : 0);
   return L;
 }
 size_t entropy_bytes(int es, int64_t T, int64_t d, int64_t V) {
@@ -345,6 +424,17 @@ hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t l
   constexpr bool split = sizeof(X) == 4;
   TileOperand xo = {(const char*)x, ldx * (int64_t)sizeof(X), 0, T, 0};
   int64_t kbytes = d * (int64_t)sizeof(X), piece = V;
+  if (T <= kSkinnyTokens) {
+    const TileOperand wo = {(const char*)w, ldw * (int64_t)sizeof(X), 0, V, 0};
+    typedef typename K::whole MW;
+    e = tile_direct(wo, kbytes) && tile_direct(xo, kbytes)
+            ? start_skinny_entropy<MW, false>(wo, xo, kbytes, y, parts, zy, s)
+            : start_skinny_entropy<MW, true>(wo, xo, kbytes, y, parts, zy, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(entropy_join_kernel<1>, dim3((unsigned)T), dim3(256), 0, s, T, V,
+                       (V + 15) / 16, parts, zy, y, loss, lse);
+    return hipGetLastError();
+  }
   if (split) {
     const Planes p = {b + L.xp, plane_ld(d), T * plane_ld(d)};
     if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, nullptr, p, s)) != hipSuccess) return e;
@@ -369,8 +459,8 @@ hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t l
       e = start_entropy<M, 128, 128, 2, 2, false>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(entropy_join_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, s, T, V,
-                     nparts, parts, zy, y, loss, lse);
+  hipLaunchKernelGGL(entropy_join_kernel<16>, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, s, T,
+                     V, nparts, parts, zy, y, loss, lse);
   return hipGetLastError();
 }
 

@@ -52,6 +52,19 @@ struct MmaF16 {
                                                   __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
 };
+// float32 itself, four k at a time (at a sixteenth of bfloat16's rate): for
+// products bound by reading their operands.
+struct MmaF32 {
+  typedef f32x4 acc_t;
+  static constexpr int kElem = 4;
+  __device__ static inline acc_t mma(v4i a, v4i b, acc_t c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(a[e]), __int_as_float(b[e]), c, 0, 0,
+                                               0);
+    return c;
+  }
+};
 
 // One operand, in planes `plane` bytes apart: `rows` rows of a product's kbytes
 // bytes, `ld` bytes apart; or k-major: `krows` rows of k, `ld` bytes apart, each
@@ -102,8 +115,10 @@ __device__ inline v4i load_any(const char* row, int64_t k, int64_t kbytes) {
         unsigned x;
         if (E == 1)
           x = *(const unsigned char*)(row + k + e);
-        else
+        else if (E == 2)
           x = *(const unsigned short*)(row + k + e);
+        else
+          x = *(const unsigned*)(row + k + e);
         w[e / 4] |= x << (8 * (e % 4));
       }
     v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};

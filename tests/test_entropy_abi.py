@@ -64,7 +64,7 @@ def test_empty_and_workspaces():
     assert _grad(d=0, X=None, W=None, dX=None, dW=None, ws=None) == bk.OK
     assert _grad(dX=None, dW=None, ws=None) == bk.OK
     for q in (bk.lib().bakron_cross_entropy_workspace_bytes, bk.lib().bakron_cross_entropy_grad_workspace_bytes):
-        assert 0 < q(bk.BF16, 64, 64, 64) < q(bk.F32, 64, 64, 64) < q(bk.F32, 64, 64, 6400)
+        assert 0 < q(bk.BF16, 128, 64, 64) < q(bk.F32, 128, 64, 64) < q(bk.F32, 128, 64, 6400)
         assert q(bk.F64, 64, 64, 64) == q(bk.F32, -1, 64, 64) == q(bk.F32, 64, 64, 0) == 0
     # pieces, not the logits: 16384 tokens of 131072 words hold 4 GiB of bfloat16 logits
     assert bk.lib().bakron_cross_entropy_grad_workspace_bytes(bk.BF16, 16384, 4096, 131072) < (3 << 30) // 2
