@@ -87,24 +87,42 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_kernel(
   const int64_t r0 = (int64_t)tr * BR, c0 = (int64_t)tc * BC;
   TP tp;
   tp.zero();
-  if (ANY)
-    tp.run_any(W, X, kbytes, r0, c0, lds);
-  else
-    tp.run(W, X, kbytes, pairs, r0, c0, 0, TP::steps(kbytes, pairs), lds);
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int64_t rb = r0 + tp.wave_r(), T = X.rows;
   // rows of this lane's that are W's: 16 i + 4 q + e < left
   const int left = (int)(W.rows - rb < TP::FR * 16 ? W.rows - rb : TP::FR * 16) - 4 * q;
-  const int64_t part = part0 + (int64_t)tr * WR + (threadIdx.x >> 6) / WC;
+  // where 16 i + e of the lane's rows is the target: read before the product, whose
+  // end would otherwise wait for them
+  int target[TP::FC];
 #pragma unroll
   for (int j = 0; j < TP::FC; ++j) {
     const int64_t t = c0 + tp.wave_c() + j * 16 + (lane & 15);
-    float m = -__builtin_inff();
+    const int64_t yt = y[t < T ? t : T - 1], at = yt - v0 - rb - 4 * q;
+    target[j] = yt >= 0 && at >= 0 && at < left && t < T ? (int)at : -1;
+  }
+  if (ANY)
+    tp.run_any(W, X, kbytes, r0, c0, lds);
+  else
+    tp.run(W, X, kbytes, pairs, r0, c0, 0, TP::steps(kbytes, pairs), lds);
+  if (rb + TP::FR * 16 > W.rows) {  // the last tile: rows past W's add nothing
 #pragma unroll
     for (int i = 0; i < TP::FR; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (16 * i + e < left) m = fmaxf(m, tp.acc[i][j][e]);
+        if (16 * i + e >= left) {
+#pragma unroll
+          for (int j = 0; j < TP::FC; ++j) tp.acc[i][j][e] = -__builtin_inff();
+        }
+  }
+  const int64_t part = part0 + (int64_t)tr * WR + (threadIdx.x >> 6) / WC;
+#pragma unroll
+  for (int j = 0; j < TP::FC; ++j) {
+    const int64_t t = c0 + tp.wave_c() + j * 16 + (lane & 15);
+    float m = tp.acc[0][j][0];
+#pragma unroll
+    for (int i = 0; i < TP::FR; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, tp.acc[i][j][e]);
     m = fmaxf(m, __shfl_xor(m, 16, 64));
     m = fmaxf(m, __shfl_xor(m, 32, 64));
     // a set of -inf alone sums to 0 (and one with a NaN to NaN)
@@ -113,19 +131,16 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_kernel(
 #pragma unroll
     for (int i = 0; i < TP::FR; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * i + e < left) s += exp_of(tp.acc[i][j][e] - base);
+      for (int e = 0; e < 4; ++e) s += exp_of(tp.acc[i][j][e] - base);
     s += __shfl_xor(s, 16, 64);
     s += __shfl_xor(s, 32, 64);
-    if (t < T) {
-      if (q == 0) parts[part * T + t] = {m, s};
-      const int64_t yt = y[t];  // the target among this lane's rows
-      const int64_t at = yt < 0 ? -1 : yt - v0 - rb - 4 * q;
+    if (t < T && q == 0) parts[part * T + t] = {m, s};
+    if (target[j] >= 0) {
 #pragma unroll
       for (int i = 0; i < TP::FR; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (16 * i + e == at && at < left) zy[t] = tp.acc[i][j][e];
+          if (16 * i + e == target[j]) zy[t] = tp.acc[i][j][e];
     }
   }
 }
@@ -245,27 +260,38 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
   const int64_t r0 = (int64_t)tr * BR, c0 = (int64_t)tc * BC;
   TP tp;
   tp.zero();
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int64_t T = X.rows, rb = r0 + tp.wave_r() + 4 * q;
+  // The token's lse, and where 16 i + e of the lane's rows is the target (-1:
+  // nowhere, -2: the token has none); read before the product, whose end would
+  // otherwise wait for them.
+  int target[TP::FC];
+  float norm[TP::FC];
+#pragma unroll
+  for (int j = 0; j < TP::FC; ++j) {
+    const int64_t t = c0 + tp.wave_c() + j * 16 + (lane & 15), tt = t < T ? t : T - 1;
+    const int64_t yt = y[tt], at = yt - v0 - rb;
+    target[j] = yt < 0 || yt >= V ? -2 : at >= 0 && at < TP::FR * 16 ? (int)at : -1;
+    norm[j] = lse[tt];
+  }
   if (ANY)
     tp.run_any(W, X, kbytes, r0, c0, lds);
   else
     tp.run(W, X, kbytes, pairs, r0, c0, 0, TP::steps(kbytes, pairs), lds);
-  const int lane = threadIdx.x & 63, q = lane >> 4;
-  const int64_t T = X.rows;
+  const bool whole = r0 + tp.wave_r() + TP::FR * 16 <= W.rows;
 #pragma unroll
   for (int j = 0; j < TP::FC; ++j) {
     const int64_t t = c0 + tp.wave_c() + j * 16 + (lane & 15);
-    const int64_t yt = t < T ? y[t] : -1;
-    const bool has = yt >= 0 && yt < V;
-    const float l = t < T ? lse[t] : 0.0f;
+    const bool has = target[j] != -2;
 #pragma unroll
     for (int i = 0; i < TP::FR; ++i) {
-      const int64_t r = r0 + tp.wave_r() + i * 16 + 4 * q;
+      const int64_t r = rb + i * 16;
       unsigned short w[NP][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float v = exp_of(tp.acc[i][j][e] - l);
-        if (v0 + r + e == yt) v -= 1.0f;
-        v = has && r + e < W.rows ? v * scale : 0.0f;
+        float v = exp_of(tp.acc[i][j][e] - norm[j]);
+        if (16 * i + e == target[j]) v -= 1.0f;
+        v = has && (whole || r + e < W.rows) ? v * scale : 0.0f;
         unsigned short k[NP];
         split16<KIND>(v, k);
 #pragma unroll
