@@ -471,8 +471,7 @@ int bakron_sample_sqnorms(int dtype, int64_t N, int64_t d, const void *X, int64_
  * order, then once to ytype. Rows that start at multiples of 16 bytes
  * with n a multiple of 16 are read fastest; any alignment and stride works.
  * Y must not overlap the inputs (BAKRON_EINVAL). The workspace query gives 0,
- * and workspace may be NULL, where the call needs none (few tokens, many
- * tiles).
+ * and workspace may be NULL, where the call needs none.
  *
  * Both are asynchronous and deterministic. T, m <= 2^31 - 1.
  * ------------------------------------------------------------------------ */

@@ -308,7 +308,7 @@ struct PlanePairs {
   int n;
   unsigned r, c;
 };
-// Y[c][r] = (sum + prev[c][r]) * row_scale[r] * alpha * beta * col_scale[c];
+// Y[c][r] = (sum + prev[c][r]) * row_scale[r] * (col_scale[c] * alpha * beta);
 // every pointer nullable. prev has rows of whole groups of four, 16-byte
 // aligned, and may be Y.
 struct PlaneEpilogue {

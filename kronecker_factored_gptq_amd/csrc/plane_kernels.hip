@@ -89,38 +89,38 @@ __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
     return;
   }
   const float all = (ep.alpha ? *ep.alpha : 1.0f) * ep.beta;
-  float sr[TP::FR][4], sc[TP::FC];
+  float sc[TP::FC];
 #pragma unroll
-  for (int i = 0; i < TP::FR; ++i)
+  for (int j = 0; j < TP::FC; ++j) {
+    const int64_t c = cb + j * 16;
+    sc[j] = (ep.col_scale ? ep.col_scale[c < C.rows ? c : C.rows - 1] : 1.0f) * all;
+  }
+  if (ep.prev) {  // rows of whole groups of four: its columns are padded
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sr[i][e] = all;
+    for (int j = 0; j < TP::FC; ++j) {
+      const int64_t c = cb + j * 16;
+      if (c < C.rows) {
+#pragma unroll
+        for (int i = 0; i < TP::FR; ++i)
+          if (rb + i * 16 < R.rows)
+            tp.acc[i][j] += *(const f32x4*)(ep.prev + c * ep.ldprev + rb + i * 16);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one column's loads at a time: registers
+    }
+  }
   if (ep.row_scale) {
 #pragma unroll
     for (int i = 0; i < TP::FR; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int64_t r = rb + i * 16 + e;
-        sr[i][e] = ep.row_scale[r < R.rows ? r : R.rows - 1] * all;
+        const float f = ep.row_scale[r < R.rows ? r : R.rows - 1];
+#pragma unroll
+        for (int j = 0; j < TP::FC; ++j) tp.acc[i][j][e] *= f;
       }
   }
-#pragma unroll
-  for (int j = 0; j < TP::FC; ++j) {
-    const int64_t c = cb + j * 16;
-    sc[j] = ep.col_scale ? ep.col_scale[c < C.rows ? c : C.rows - 1] : 1.0f;
-  }
-  if (ep.prev) {  // rows of whole groups of four: its columns are padded
-#pragma unroll
-    for (int j = 0; j < TP::FC; ++j) {
-      const int64_t c = cb + j * 16;
-      if (c >= C.rows) continue;
-#pragma unroll
-      for (int i = 0; i < TP::FR; ++i)
-        if (rb + i * 16 < R.rows)
-          tp.acc[i][j] += *(const f32x4*)(ep.prev + c * ep.ldprev + rb + i * 16);
-    }
-  }
   store_tile(tp, r0, c0, R.rows, C.rows, Y, ldy, vec,
-             [&](float a, int i, int j, int e) { return a * sr[i][e] * sc[j]; });
+             [&](float a, int, int j, int) { return a * sc[j]; });
 }
 
 // The ranges' sums in order, and the epilogue; four columns of one row a thread.
@@ -138,12 +138,12 @@ __global__ __launch_bounds__(256) void plane_join_kernel(int64_t M, int64_t N, i
   for (int k = 0; k < splits; ++k) a += *(const f32x4*)(parts + k * stride + c * ldp + r);
   if (ep.prev) a += *(const f32x4*)(ep.prev + c * ep.ldprev + r);
   const float all = (ep.alpha ? *ep.alpha : 1.0f) * ep.beta;
-  const float sc = ep.col_scale ? ep.col_scale[c] : 1.0f;
+  const float sc = (ep.col_scale ? ep.col_scale[c] : 1.0f) * all;
   O t[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float sr = ep.row_scale ? ep.row_scale[r + e < M ? r + e : M - 1] : 1.0f;
-    t[e] = from_f32<O>(a[e] * (sr * all) * sc);
+    t[e] = from_f32<O>(a[e] * sr * sc);
   }
   if (vec && r + 4 <= M) {
     *(typename Vec4<O>::type*)(Y + c * ldy + r) = __builtin_bit_cast(typename Vec4<O>::type, t);

@@ -202,7 +202,10 @@ struct TileProduct {
   }
   __device__ inline void multiply(const Frags& f) {
 #pragma unroll
-    for (int g = 0; g < FR * FC; ++g) multiply(f, g);
+    for (int g = 0; g < FR * FC; ++g) {
+      multiply(f, g);
+      if (g % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // in order: registers
+    }
   }
   // Multiplies `f` while `next` is read, and LOADS wave loads (load(u)) go out.
   // The order is fixed here: one LDS read to two multiplications, and the loads
