@@ -247,7 +247,7 @@ __global__ __launch_bounds__(1024) void entropy_weights_kernel(
 
 // D's planes of a piece, rows the tokens, written up to the planes' padding, with
 // zeros there.
-template <class M, int KIND, int BR, int BC, int WR, int WC, bool ANY>
+template <class M, int KIND, int BR, int BC, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
     TileOperand W, TileOperand X, int64_t kbytes, PlanePairs pairs, const int64_t* __restrict__ y,
     int64_t V, int64_t v0, const float* __restrict__ lse, float scale, Planes P, unsigned nr,
@@ -274,10 +274,7 @@ __global__ __launch_bounds__(64 * WR * WC) void entropy_diff_kernel(
     target[j] = yt < 0 || yt >= V ? -2 : at >= 0 && at < TP::FR * 16 ? (int)at : -1;
     norm[j] = lse[tt];
   }
-  if (ANY)
-    tp.run_any(W, X, kbytes, r0, c0, lds);
-  else
-    tp.run(W, X, kbytes, pairs, r0, c0, 0, TP::steps(kbytes, pairs), lds);
+  tp.run(W, X, kbytes, pairs, r0, c0, 0, TP::steps(kbytes, pairs), lds);
   const bool whole = r0 + tp.wave_r() + TP::FR * 16 <= W.rows;
 #pragma unroll
   for (int j = 0; j < TP::FC; ++j) {
@@ -341,13 +338,13 @@ static hipError_t start_skinny_entropy(const TileOperand& W, const TileOperand& 
   return hipGetLastError();
 }
 
-template <class M, int KIND, int BR, int BC, int WR, int WC, bool ANY>
+template <class M, int KIND, int BR, int BC, int WR, int WC>
 static hipError_t start_entropy_diff(const TileOperand& W, const TileOperand& X, int64_t kbytes,
                                      const PlanePairs& pairs, const int64_t* y, int64_t V,
                                      int64_t v0, const float* lse, float scale, Planes P,
                                      hipStream_t s) {
   typedef TileProduct<M, BR, BC, WR, WC> TP;
-  auto* k = entropy_diff_kernel<M, KIND, BR, BC, WR, WC, ANY>;
+  auto* k = entropy_diff_kernel<M, KIND, BR, BC, WR, WC>;
   if (TP::kLds > 65536) {
     const hipError_t e =
         hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, TP::kLds);
@@ -414,7 +411,7 @@ static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
   L.rel = L.w + up256((size_t)T * 4);
   L.top = L.rel + up256((size_t)T * 4);
   L.xp = L.top + 256;
-  L.xs = L.xp + (es == 4 ? up256((size_t)(3 * T * plane_ld(d))) : 0);
+  L.xs = L.xp + up256((size_t)(np * T * plane_ld(d)));
   L.wp = L.xs + up256((size_t)(np * T * plane_ld(d)));
   L.p = L.wp + up256((size_t)(np * L.piece * plane_ld(d)));
   L.acc = L.p + up256((size_t)(np * T * plane_ld(L.piece)));
@@ -508,19 +505,21 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
   float *wt = (float*)(b + L.w), *rel = (float*)(b + L.rel), *top = (float*)(b + L.top);
   float *acc = (float*)(b + L.acc), *parts = (float*)(b + L.parts);
   const PlanePairs pairs = pairs_of<X>();
-  constexpr bool split = sizeof(X) == 4;
-  constexpr int64_t es = sizeof(X);
   hipLaunchKernelGGL(entropy_weights_kernel, dim3(1), dim3(1024), 0, s, T, V, y, g, wt, rel, top);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  // Both operands as they are, where the direct loads can take them (along d for
+  // the logits, W also k-major for dX); else as planes.
+  constexpr int64_t es = sizeof(X);
+  const int64_t kbytes = (d + 7) / 8 * 16;
   TileOperand xo = {(const char*)x, ldx * es, 0, T, 0};
-  int64_t kbytes = d * es;
-  if (split) {
+  const bool direct = es == 2 && d % 8 == 0 && tile_direct(xo, kbytes) &&
+                      tile_direct({(const char*)w, ldw * es, 0, V, 0}, kbytes);
+  if (!direct) {
     const Planes p = {b + L.xp, plane_ld(d), T * plane_ld(d)};
     if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, nullptr, p, s)) != hipSuccess)
       return e;
     xo = {p.w, p.ld, p.plane, T, 0};
-    kbytes = (d + 7) / 8 * 16;
   }
   const Planes xs = {b + L.xs, plane_ld(d), T * plane_ld(d)};
   if (dW && (e = launch_planes<X, K::split>(T, d, x, ldx, rel, nullptr, xs, s)) != hipSuccess)
@@ -528,27 +527,20 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
   for (int64_t v0 = 0; v0 < V; v0 += L.piece) {
     const int64_t rows = V - v0 < L.piece ? V - v0 : L.piece;
     const X* wv = w + v0 * ldw;
-    // W's piece: as it is where the direct loads can take it, along d for the
-    // logits and k-major for dX, else as planes
-    TileOperand wo = {(const char*)wv, ldw * es, 0, rows, 0};
-    const bool direct = !split && tile_direct(wo, kbytes);
     Planes wp = {(char*)const_cast<X*>(wv), ldw * es, 0};
-    if (!direct && (split || dX)) {
+    if (!direct) {
       wp = {b + L.wp, plane_ld(d), rows * plane_ld(d)};
       if ((e = launch_planes<X, K::split>(rows, d, wv, ldw, nullptr, nullptr, wp, s)) != hipSuccess)
         return e;
-      if (split) wo = {wp.w, wp.ld, wp.plane, rows, 0};
     }
+    const TileOperand wo = {wp.w, wp.ld, wp.plane, rows, 0};
     const Planes P = {b + L.p, plane_ld(rows), T * plane_ld(rows)};
-    if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
-      e = start_entropy_diff<M, K::split, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, V, v0, lse,
-                                                                dscale<X>(), P, s);
-    else if (((rows + 255) / 256) * ((T + 255) / 256) >= 192)
-      e = start_entropy_diff<M, K::split, 256, 256, 2, 4, false>(wo, xo, kbytes, pairs, y, V, v0,
-                                                                 lse, dscale<X>(), P, s);
+    if (((rows + 255) / 256) * ((T + 255) / 256) >= 192)
+      e = start_entropy_diff<M, K::split, 256, 256, 2, 4>(wo, xo, kbytes, pairs, y, V, v0, lse,
+                                                          dscale<X>(), P, s);
     else
-      e = start_entropy_diff<M, K::split, 128, 128, 2, 2, false>(wo, xo, kbytes, pairs, y, V, v0,
-                                                                 lse, dscale<X>(), P, s);
+      e = start_entropy_diff<M, K::split, 128, 128, 2, 2>(wo, xo, kbytes, pairs, y, V, v0, lse,
+                                                          dscale<X>(), P, s);
     if (e != hipSuccess) return e;
     if (dX) {
       const bool last = v0 + rows == V;
