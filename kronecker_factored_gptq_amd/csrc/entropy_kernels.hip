@@ -384,9 +384,9 @@ struct EntropyLayout {
 static EntropyLayout entropy_layout(int es, int64_t T, int64_t d, int64_t V) {
   EntropyLayout L;
   L.parts = 0;
-  // two waves of rows in each tile, of at least 128 rows; or every 16 rows
+  // two waves of rows in each tile, of at least 64 rows; or every 16 rows
   const bool skinny = T <= kSkinnyTokens;
-  const int64_t nparts = skinny ? (V + 15) / 16 : 2 * ((V + 127) / 128);
+  const int64_t nparts = skinny ? (V + 15) / 16 : 2 * ((V + 63) / 64);
   L.zy = L.parts + up256((size_t)(nparts * T) * sizeof(MaxSum));
   L.xp = L.zy + up256((size_t)T * 4);
   const bool planes = es == 4 && !skinny;
@@ -474,12 +474,16 @@ hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t l
         return e;
       wo = {p.w, p.ld, p.plane, rows, 0};
     }
+    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes * pairs.n;
+    const int tile = plan_tiles(rows, T, steps, false, false).tile;
     if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
       e = start_entropy<M, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
-    else if (((rows + 255) / 256) * ((T + 255) / 256) >= 192)
+    else if (tile == 256)
       e = start_entropy<M, 256, 256, 2, 4, false>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
-    else
+    else if (tile == 128)
       e = start_entropy<M, 128, 128, 2, 2, false>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
+    else
+      e = start_entropy<M, 64, 64, 2, 2, false>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(entropy_join_kernel<16>, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, s, T,
@@ -535,12 +539,17 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
     }
     const TileOperand wo = {wp.w, wp.ld, wp.plane, rows, 0};
     const Planes P = {b + L.p, plane_ld(rows), T * plane_ld(rows)};
-    if (((rows + 255) / 256) * ((T + 255) / 256) >= 192)
+    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes * pairs.n;
+    const int tile = plan_tiles(rows, T, steps, false, false).tile;
+    if (tile == 256)
       e = start_entropy_diff<M, K::split, 256, 256, 2, 4>(wo, xo, kbytes, pairs, y, V, v0, lse,
                                                           dscale<X>(), P, s);
-    else
+    else if (tile == 128)
       e = start_entropy_diff<M, K::split, 128, 128, 2, 2>(wo, xo, kbytes, pairs, y, V, v0, lse,
                                                           dscale<X>(), P, s);
+    else
+      e = start_entropy_diff<M, K::split, 64, 64, 2, 2>(wo, xo, kbytes, pairs, y, V, v0, lse,
+                                                        dscale<X>(), P, s);
     if (e != hipSuccess) return e;
     if (dX) {
       const bool last = v0 + rows == V;

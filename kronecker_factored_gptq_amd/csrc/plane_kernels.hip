@@ -154,14 +154,11 @@ __global__ __launch_bounds__(256) void plane_join_kernel(int64_t M, int64_t N, i
   }
 }
 
-static bool plane_big(int64_t M, int64_t N) {
-  return ((M + 255) / 256) * ((N + 255) / 256) >= 192;
-}
-static int plane_splits(int64_t M, int64_t N, int64_t K, int npairs) {
-  return plane_big(M, N) ? 1 : split_steps(M, N, (K + 63) / 64 * npairs);
+static TilePlan plane_plan(int64_t M, int64_t N, int64_t K, int npairs) {
+  return plan_tiles(M, N, (K + 63) / 64 * npairs, true, true);
 }
 size_t plane_product_bytes(int64_t M, int64_t N, int64_t K, int npairs) {
-  return (size_t)split_words(M, N, plane_splits(M, N, K, npairs)) * 4;
+  return (size_t)split_words(M, N, plane_plan(M, N, K, npairs).splits) * 4;
 }
 
 template <class M, typename O, int BR, int BC, int WR, int WC, bool CK>
@@ -196,11 +193,15 @@ hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Plane
   if (M <= 0 || N <= 0) return hipSuccess;
   const TileOperand r = {R.w, R.ld, R.plane, M, K}, c = {C.w, C.ld, C.plane, N, K};
   const int64_t kbytes = (K + 7) / 8 * 16;  // whole 16-byte chunks: the planes' padding is zero
-  if (plane_big(M, N))
+  const TilePlan plan = plane_plan(M, N, K, pairs.n);
+  if (plan.tile == 256)
     return start_plane_product<Mma, O, 256, 256, 2, 4, CK>(r, c, kbytes, pairs, ep, Y, ldy, 1, parts,
                                                            s);
-  return start_plane_product<Mma, O, 128, 128, 2, 2, CK>(
-      r, c, kbytes, pairs, ep, Y, ldy, plane_splits(M, N, K, pairs.n), parts, s);
+  if (plan.tile == 128)
+    return start_plane_product<Mma, O, 128, 128, 2, 2, CK>(r, c, kbytes, pairs, ep, Y, ldy,
+                                                           plan.splits, parts, s);
+  return start_plane_product<Mma, O, 64, 64, 2, 2, CK>(r, c, kbytes, pairs, ep, Y, ldy, plan.splits,
+                                                       parts, s);
 }
 
 // ---------------------------------------------------------------------------

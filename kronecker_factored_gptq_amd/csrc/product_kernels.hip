@@ -287,19 +287,16 @@ static int64_t skinny_tokens(int64_t m, int64_t n) {
   return m * n <= (1 << 24) ? 64 : m * n <= (1 << 26) ? 16 : 8;
 }
 
-static bool int8_big(int64_t T, int64_t m) {
-  return ((m + 255) / 256) * ((T + 255) / 256) >= 192;
-}
-static int int8_splits(int64_t T, int64_t m, int64_t n) {
-  if (T <= skinny_tokens(m, n) || int8_big(T, m)) return 1;
-  return split_steps(m, T, (n + kStepBytes - 1) / kStepBytes);
+static TilePlan int8_plan(int64_t T, int64_t m, int64_t n) {
+  return plan_tiles(m, T, (n + kStepBytes - 1) / kStepBytes, false, true);
 }
 static bool int8_packs(int64_t T, int64_t m, int64_t n) {
   return n % 16 != 0 && T > skinny_tokens(m, n);
 }
 static int64_t packed_ld(int64_t n) { return (n + kStepBytes - 1) / kStepBytes * kStepBytes; }
 size_t matmul_int8_bytes(int64_t T, int64_t m, int64_t n) {
-  return (size_t)split_words(m, T, int8_splits(T, m, n)) * 4 +
+  if (T <= skinny_tokens(m, n)) return 0;
+  return (size_t)split_words(m, T, int8_plan(T, m, n).splits) * 4 +
          (int8_packs(T, m, n) ? (size_t)((T + m) * packed_ld(n)) : 0);
 }
 
@@ -327,10 +324,13 @@ hipError_t launch_matmul_int8(int64_t T, int64_t m, int64_t n, const int8_t* Xq,
                   : start_skinny_int8<O, true>(V, X, n, sx, sv, Y, ldy, s);
   if (!direct)
     return start_matmul_int8<O, 128, 128, 2, 2, true>(V, X, n, sx, sv, Y, ldy, 1, nullptr, s);
-  if (int8_big(T, m))
+  const TilePlan plan = int8_plan(T, m, n);
+  if (plan.tile == 256)
     return start_matmul_int8<O, 256, 256, 2, 4, false>(V, X, n, sx, sv, Y, ldy, 1, nullptr, s);
-  return start_matmul_int8<O, 128, 128, 2, 2, false>(V, X, n, sx, sv, Y, ldy, int8_splits(T, m, n),
-                                                     (int*)ws, s);
+  if (plan.tile == 128)
+    return start_matmul_int8<O, 128, 128, 2, 2, false>(V, X, n, sx, sv, Y, ldy, plan.splits,
+                                                       (int*)ws, s);
+  return start_matmul_int8<O, 64, 64, 2, 2, false>(V, X, n, sx, sv, Y, ldy, plan.splits, (int*)ws, s);
 }
 
 #define BK_INST_Q(X)                                                                        \

@@ -165,8 +165,10 @@ struct TileProduct {
   // A k-major operand lies k by k, 2 B bytes each. Of a transposing read, four
   // lanes take 32 bytes of one k, 16 lanes four k, and the next 16 lanes k that
   // are 8 further; the 32-byte block b of k lies at b ^ swap_at(k), so that 32
-  // lanes cover 256 bytes of banks once.
-  __device__ static inline int swap_at(int k) { return (k & 3) | ((k >> 1) & 4); }
+  // lanes cover 256 bytes of banks once (with B = 64, k and k + 1 share them).
+  template <int B> __device__ static inline int swap_at(int k) {
+    return B >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+  }
 
   // Fragment i of the operand whose wave's rows start at row0.
   template <bool K, int B>
@@ -179,7 +181,7 @@ struct TileProduct {
     typedef __attribute__((address_space(3))) v4s lds_v4s;
     const int k = 8 * q + (r16 >> 2);  // and 4 further, of 32 kk on
     // block row0 / 16 + i, the first a multiple of the wave's fragments
-    const int at = k * (2 * B) + ((row0 / 16) ^ swap_at(k)) * 32 + (r16 & 3) * 8;
+    const int at = k * (2 * B) + ((row0 / 16) ^ swap_at<B>(k)) * 32 + (r16 & 3) * 8;
     const char* a = lds + (at ^ (i * 32)) + kk * 64 * B;
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a);
     const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(a + 8 * B));
@@ -306,7 +308,7 @@ struct TileProduct {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
           const int kr = (j * kWaves + wave) * lanes_k + krow, pos = lane % per;
-          const int chunk = ((pos >> 1) ^ swap_at(kr)) * 2 + (pos & 1);
+          const int chunk = ((pos >> 1) ^ swap_at<B>(kr)) * 2 + (pos & 1);
           off[j] = chunk * 8 < rows ? kr * ld + chunk * 16 : (int)0x80000000;
         }
         krow += wave * lanes_k + (ksteps - 1) * 64 - (int)o.krows;  // >= 0: past the last k
@@ -570,26 +572,46 @@ __device__ inline void store_sums(const TP& tp, int64_t r0, int64_t c0, int64_t 
   }
 }
 
-// A product of few tiles is split along k over workgroups, each range of steps
-// summed apart and the ranges joined by a second kernel. Of 128 x 128 tiles two
-// workgroups run on each of 256 CUs; a range's steps follow one another at 0.5 us,
-// and its sums are written and read again at 2.4 bytes a ps with 3 us for the
-// second kernel (measured over 1024 x 2048 to 28672 x 4096 and 17 to 256
-// columns: 4096 x 14336 with 128 columns 58 us in one range, 28 in 16; 14336 x 4096
-// with 256 columns 24 us in one, 38 in 2). The number of ranges that takes least.
-constexpr int64_t kWorkgroups = 512;
-inline int64_t tiles128(int64_t M, int64_t N) { return ((M + 127) / 128) * ((N + 127) / 128); }
-inline int split_steps(int64_t M, int64_t N, int64_t steps) {
-  if (M <= 0 || N <= 0) return 1;
-  const int64_t most = kWorkgroups / tiles128(M, N);
+// The tile of a product, and the ranges its k is split into. 256 x 256 tiles
+// (one workgroup a CU) need the fewest bytes and are taken where they fill the
+// chip. Below that the choice is by an estimate of the time in us, fitted to
+// measurements over 300 x 700 to 14336 x 4096 and 20 to 2048 columns:
+// - 128 x 128 (two workgroups a CU) and 64 x 64 tiles (four): with c workgroups
+//   on each CU a step takes 0.28 + 0.4 c and 0.19 + 0.175 c (bound by the L2; one
+//   workgroup alone by latency, 0.5 and 0.35), and k-major operands 0.15 more of
+//   the small tile; filling the ring takes 3 and 1;
+// - k split into n ranges, each summed apart: 3 for the kernel that joins them,
+//   and their sums, written and read again, at 2.4 bytes a ps.
+// (int8, 4096 x 4096 and 256 columns: 12 us with 64 x 64 tiles, 20 with 128 x
+// 128; 14336 x 4096 and 256: 27 and 23; 4096 x 14336 and 128: 58 in one range, 22
+// in eight.)
+struct TilePlan {
+  int tile, splits;
+};
+inline int64_t tiles_of(int64_t M, int64_t N, int64_t tile) {
+  return ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
+}
+inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, bool kmajor, bool may_split) {
+  TilePlan best = {128, 1};
+  if (M <= 0 || N <= 0) return best;
+  if (tiles_of(M, N, 256) >= 192) return {256, 1};
+  double least = 1e300;
   const double word = (double)M * (double)N * 8 / 2.4e6;
-  int best = 1;
-  double least = 0.5 * (double)steps;
-  for (int n = 2; n <= most && n <= steps / 2; ++n) {
-    const double t = 0.5 * (double)((steps + n - 1) / n) + 3 + n * word;
-    if (t < least) {
-      least = t;
-      best = n;
+  for (int tile : {128, 64}) {
+    const bool small = tile == 64;
+    const int64_t tiles = tiles_of(M, N, tile), slots = small ? 1024 : 512;
+    for (int n = 1; n == 1 || (may_split && n * tiles <= slots && n <= steps / 2); ++n) {
+      const int64_t rounds = (n * tiles + slots - 1) / slots;
+      const double c = rounds > 1 ? (double)slots / 256 : (double)(n * tiles) / 256;
+      double each = small ? 0.19 + 0.175 * c : 0.28 + 0.4 * c;
+      if (each < (small ? 0.35 : 0.5)) each = small ? 0.35 : 0.5;
+      if (small && kmajor) each += 0.15;
+      const double t = (double)rounds * each * (double)((steps + n - 1) / n) + (small ? 1 : 3) +
+                       (n > 1 ? 3 + n * word : 0);
+      if (t < least) {
+        least = t;
+        best = {tile, n};
+      }
     }
   }
   return best;
