@@ -54,7 +54,8 @@ constexpr size_t kAlign = 256;
 constexpr int64_t kMaxPlaneCols = (int64_t)1 << 20;
 inline bool grad_sizes_ok(int t, int64_t T, int64_t m, int64_t n) {
   return type_ok(t) && T >= 0 && m >= 0 && n >= 0 && T <= INT_MAX && m <= kMaxPlaneCols &&
-         n <= kMaxPlaneCols && T * (m + 64) <= ((int64_t)1 << 41);
+         n <= kMaxPlaneCols && T * (m + 64) <= ((int64_t)1 << 41) &&
+         T + (m + 64) * (n + 64) / 2048 < INT_MAX;
 }
 
 inline bool entropy_sizes_ok(int t, int64_t T, int64_t d, int64_t V) {

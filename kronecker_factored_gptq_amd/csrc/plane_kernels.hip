@@ -11,16 +11,12 @@ struct I8 {
 };
 __device__ inline float to_f32(I8 x) { return (float)x.v; }
 
-// Eight columns of one row per thread, one 16-byte store per plane.
+// Eight columns of one row, one 16-byte store per plane: group `at` of all rows.
 template <typename X, int KIND>
-__global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
-                                                     const X* __restrict__ x, int64_t ldx,
-                                                     const float* __restrict__ rs,
-                                                     const float* __restrict__ cs, Planes out,
-                                                     bool vec) {
+__device__ inline void planes_group(int64_t at, int64_t rows, int64_t cols, const X* x, int64_t ldx,
+                                    const float* rs, const float* cs, const Planes& out, bool vec) {
   constexpr int NP = kPlanes[KIND];
   const int64_t per = out.ld / 16;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= rows * per) return;
   const int64_t r = at / per, c0 = (at - r * per) * 8;
   const Eight<X> t8 = load8(x + r * ldx, c0, cols, vec);
@@ -47,6 +43,15 @@ __global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
 #pragma unroll
   for (int p = 0; p < NP; ++p)
     *(v4i*)(out.w + p * out.plane + r * out.ld + c0 * 2) = __builtin_bit_cast(v4i, w[p]);
+}
+template <typename X, int KIND>
+__global__ __launch_bounds__(256) void planes_kernel(int64_t rows, int64_t cols,
+                                                     const X* __restrict__ x, int64_t ldx,
+                                                     const float* __restrict__ rs,
+                                                     const float* __restrict__ cs, Planes out,
+                                                     bool vec) {
+  planes_group<X, KIND>((int64_t)blockIdx.x * 256 + threadIdx.x, rows, cols, x, ldx, rs, cs, out,
+                        vec);
 }
 
 template <typename X, int KIND>
@@ -214,11 +219,39 @@ hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Plane
 // a bfloat16 output, at the same cost; more bits cost a second product.) A
 // float32 G is three bfloat16 planes, all 24 bits.
 // ---------------------------------------------------------------------------
+// The codes as one plane, m x n: the part of both operands' launch that both
+// types of G share.
+struct GradCodes {
+  const I8* v;
+  int64_t ld, m, n;
+  Planes out;
+  bool vec;
+};
+template <int KIND>
+__device__ inline void grad_codes(int64_t block, const GradCodes& c) {
+  planes_group<I8, KIND>(block * 256 + threadIdx.x, c.m, c.n, c.v, c.ld, nullptr, nullptr, c.out,
+                         c.vec);
+}
+__global__ __launch_bounds__(256) void grad_planes_kernel(int64_t T, int64_t m,
+                                                          const float* __restrict__ g, int64_t ldg,
+                                                          const float* __restrict__ sv, Planes out,
+                                                          bool vec, int64_t blocks, GradCodes c) {
+  if ((int64_t)blockIdx.x < blocks)
+    planes_group<float, kBF16x3>((int64_t)blockIdx.x * 256 + threadIdx.x, T, m, g, ldg, nullptr, sv,
+                                 out, vec);
+  else
+    grad_codes<kBF16x1>(blockIdx.x - blocks, c);
+}
 template <typename G, int NV>
-__global__ __launch_bounds__(256) void grad_tokens_kernel(int64_t m, const G* __restrict__ g,
-                                                          int64_t ldg, const float* __restrict__ sv,
-                                                          Planes out, float* __restrict__ unscale,
-                                                          bool vec, bool vecs) {
+__global__ __launch_bounds__(256) void grad_tokens_kernel(int64_t T, int64_t m,
+                                                          const G* __restrict__ g, int64_t ldg,
+                                                          const float* __restrict__ sv, Planes out,
+                                                          float* __restrict__ unscale, bool vec,
+                                                          bool vecs, GradCodes codes) {
+  if ((int64_t)blockIdx.x >= T) {
+    grad_codes<kF16x1>(blockIdx.x - T, codes);
+    return;
+  }
   __shared__ unsigned red[4];
   const RowOf<G, NV> row(g + (int64_t)blockIdx.x * ldg, m, vec);
   auto values = [&](int64_t c, const Eight<G>& t, float* v) {
@@ -259,21 +292,31 @@ __global__ __launch_bounds__(256) void grad_tokens_kernel(int64_t m, const G* __
   });
 }
 
+// Both operands in one launch: G's tokens, and behind them the codes.
 template <typename G>
-static hipError_t launch_grad_tokens(int64_t T, int64_t m, const G* g, int64_t ldg, const float* sv,
-                                     Planes out, float* unscale, hipStream_t s) {
+static hipError_t launch_grad_operands(int64_t T, int64_t m, const G* g, int64_t ldg,
+                                       const float* sv, Planes out, float* unscale,
+                                       const GradCodes& c, hipStream_t s) {
+  const int64_t blocks = (c.m * (c.out.ld / 16) + 255) / 256;
   const bool vec = load8_ok(g, ldg), vecs = load8_ok(sv, 0);
-#define BK_ROWS(NV)                                                                              \
-  hipLaunchKernelGGL((grad_tokens_kernel<G, NV>), dim3((unsigned)T), dim3(256), 0, s, m, g, ldg, \
-                     sv, out, unscale, vec, vecs)
-  switch (row_groups(out.ld / 2)) {
-    case 1: BK_ROWS(1); break;
-    case 2: BK_ROWS(2); break;
-    case 4: BK_ROWS(4); break;
-    case 8: BK_ROWS(8); break;
-    default: BK_ROWS(0);
-  }
+  if constexpr (sizeof(G) == 4) {
+    const int64_t own = (T * (out.ld / 16) + 255) / 256;
+    if (own + blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(grad_planes_kernel, dim3((unsigned)(own + blocks)), dim3(256), 0, s, T, m, g,
+                       ldg, sv, out, vec, own, c);
+  } else {
+#define BK_ROWS(NV)                                                                             \
+  hipLaunchKernelGGL((grad_tokens_kernel<G, NV>), dim3((unsigned)(T + blocks)), dim3(256), 0, s, \
+                     T, m, g, ldg, sv, out, unscale, vec, vecs, c)
+    switch (row_groups(out.ld / 2)) {
+      case 1: BK_ROWS(1); break;
+      case 2: BK_ROWS(2); break;
+      case 4: BK_ROWS(4); break;
+      case 8: BK_ROWS(8); break;
+      default: BK_ROWS(0);
+    }
 #undef BK_ROWS
+  }
   return hipGetLastError();
 }
 
@@ -300,24 +343,16 @@ hipError_t launch_matmul_int8_grad(int64_t T, int64_t m, int64_t n, const G* g, 
                                    const float* channel, G* dX, int64_t ldx, void* ws,
                                    hipStream_t s) {
   constexpr bool wide = sizeof(G) == 4;
-  constexpr int kind = wide ? kBF16x1 : kF16x1;
   if (T <= 0 || n <= 0) return hipSuccess;
   const GradOffsets o = grad_offsets(sizeof(G), T, m, n);
   char* b = (char*)ws;
   const Planes v = {b + o.v, plane_ld(n), 0}, gp = {b + o.g, plane_ld(m), T * plane_ld(m)};
   float* unscale = (float*)(b + o.unscale);
-  hipError_t e = launch_planes<I8, kind>(m, n, (const I8*)Vq, ldv, nullptr, nullptr, v, s);
+  const GradCodes codes = {(const I8*)Vq, ldv, m, n, v, load8_ok((const I8*)Vq, ldv)};
+  const hipError_t e = launch_grad_operands(T, m, g, ldg, sv, gp, unscale, codes, s);
   if (e != hipSuccess) return e;
-  PlanePairs pairs = {1, 0, 0};
-  PlaneEpilogue ep = {channel, nullptr, nullptr, 1.0f, nullptr, 0};
-  if constexpr (wide) {
-    pairs = {3, 0x000, 0x210};
-    e = launch_planes<G, kBF16x3>(T, m, g, ldg, nullptr, sv, gp, s);
-  } else {
-    ep.col_scale = unscale;
-    e = launch_grad_tokens(T, m, g, ldg, sv, gp, unscale, s);
-  }
-  if (e != hipSuccess) return e;
+  const PlanePairs pairs = wide ? PlanePairs{3, 0x000, 0x210} : PlanePairs{1, 0, 0};
+  const PlaneEpilogue ep = {channel, wide ? nullptr : unscale, nullptr, 1.0f, nullptr, 0};
   return launch_plane_product<G, !wide, false>(n, T, m, v, gp, pairs, ep, dX, ldx,
                                                (float*)(b + o.parts), s);
 }

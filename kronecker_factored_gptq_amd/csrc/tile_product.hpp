@@ -581,7 +581,7 @@ __device__ inline void store_sums(const TP& tp, int64_t r0, int64_t c0, int64_t 
 //   workgroup alone by latency, 0.5 and 0.35), and k-major operands 0.15 more of
 //   the small tile; filling the ring takes 3 and 1;
 // - k split into n ranges, each summed apart: 3 for the kernel that joins them,
-//   and their sums, written and read again, at 2.4 bytes a ps.
+//   and their sums, written and read again, at 3.5 bytes a ps.
 // (int8, 4096 x 4096 and 256 columns: 12 us with 64 x 64 tiles, 20 with 128 x
 // 128; 14336 x 4096 and 256: 27 and 23; 4096 x 14336 and 128: 58 in one range, 22
 // in eight.)
@@ -596,7 +596,7 @@ inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, bool kmajor, boo
   if (M <= 0 || N <= 0) return best;
   if (tiles_of(M, N, 256) >= 192) return {256, 1};
   double least = 1e300;
-  const double word = (double)M * (double)N * 8 / 2.4e6;
+  const double word = (double)M * (double)N * 8 / 3.5e6;
   for (int tile : {128, 64}) {
     const bool small = tile == 64;
     const int64_t tiles = tiles_of(M, N, tile), slots = small ? 1024 : 512;
