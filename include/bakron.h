@@ -33,8 +33,10 @@
  *    before anything is enqueued. Calls on different streams with distinct
  *    workspaces may run concurrently.
  *  - `dtype` selects the element type of every floating-point array of the
- *    call: BAKRON_F32 (float) or BAKRON_F64 (double). Codes are int32.
- *  - m = 0 or n = 0 is accepted and does nothing.
+ *    call: BAKRON_F32 (float) or BAKRON_F64 (double). Codes are int32. (The
+ *    calls from bakron_quantize_tokens on name their types themselves.)
+ *  - m = 0 or n = 0 is accepted and does nothing; an empty sum is zero (the
+ *    8-bit product with n = 0 gives Y = 0, its gradient with m = 0 dX = 0).
  */
 #ifndef BAKRON_H_
 #define BAKRON_H_

@@ -67,6 +67,11 @@ hipError_t launch_planes(int64_t rows, int64_t cols, const X* x, int64_t ldx,
 
 // ---- products -----------------------------------------------------------------
 
+// A tiled product of planes, R k-major. 4096 x 4096 with k = 32768 in bfloat16: 750 to
+// 800 us, 1.37 to 1.47 PFLOP/s (a library's large product reaches 1.48 here); with k =
+// 4096 over eight rounds of tiles 1.2, the ring's filling and the stores
+// standing between tiles.
+//
 // Workgroup b: tile b % (nr nc), of `splits` equal ranges of the steps number
 // b / (nr nc). With more than one range the sums go to parts[range][c][r]
 // (rows ldp apart, ranges `stride`) and the epilogue to plane_join_kernel.
@@ -218,6 +223,8 @@ hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Plane
 // 2^-28 of the largest keep. (One bfloat16 plane would keep 8 bits, as coarse as
 // a bfloat16 output, at the same cost; more bits cost a second product.) A
 // float32 G is three bfloat16 planes, all 24 bits.
+// 8192 x 4096 x 14336 bfloat16: 762 to 800 us, of them 56 for the two operands (bound
+// by memory); 512 x 1024 x 2048 float32: 26 us in three kernels.
 // ---------------------------------------------------------------------------
 // The codes as one plane, m x n: the part of both operands' launch that both
 // types of G share.

@@ -13,6 +13,13 @@ namespace bk {
 // rounded as in the solve's quantizer. The maximum is taken over the bits of
 // |x|, in which a NaN is larger than infinity: a token with an infinity or a
 // NaN gets that as its scale, and codes whose products it makes NaN.
+//
+// Bound by memory. A workgroup keeps its row in registers between the maximum and
+// the codes, so that the row is read once (8192 x 14336 float32: 146 us, 4.0 TB/s,
+// a large copy reaching 5.0; reading it twice took 253). Eight elements to a
+// thread's group make 8-byte stores of codes; groups of four (4-byte stores) took
+// 171 us, groups of sixteen (half the workgroups on a CU) 176, and a multiplication
+// by 1 / s with a division near ties only 161. One token of 4096: 3.4 us.
 // ---------------------------------------------------------------------------
 template <typename X, int NV>
 __global__ __launch_bounds__(256) void quantize_tokens_kernel(
@@ -90,6 +97,8 @@ hipError_t launch_quantize_tokens(int64_t T, int64_t n, const X* x, int64_t ldx,
 // (n <= 131071); one float32 rounding each for the sum and the two scales, one
 // to the output's type. The tile's rows are channels and its columns tokens,
 // so a lane's four accumulators are four consecutive outputs of one token.
+// 8192 x 14336 x 4096 to bfloat16, 256 x 256 tiles: 381 to 404 us from box to box,
+// 2.4 to 2.5e15 op/s (a library's largest int8 product reaches 2.4e15 here).
 // ---------------------------------------------------------------------------
 template <typename O, int BR, int BC, int WR, int WC, bool ANY>
 __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
@@ -210,7 +219,8 @@ static hipError_t start_matmul_int8(const TileOperand& V, const TileOperand& X, 
   return hipGetLastError();
 }
 
-// Few tokens: the codes are read once, by workgroups of 16 RT channels.
+// Few tokens: the codes are read once, by workgroups of 16 RT channels. One token:
+// 4096 x 4096 5.6 us, 14336 x 4096 13.5 us (4.3 TB/s).
 template <typename O, int RT, int NT, bool ANY>
 __global__ __launch_bounds__(512) void skinny_int8_kernel(TileOperand V, TileOperand Xq, int64_t n,
                                                           const float* __restrict__ sx,

@@ -5,8 +5,11 @@
 // A workgroup of 8 waves takes 16 RT rows of R and all columns; its waves
 // divide k between them in blocks of 64 U bytes, so that one workgroup has all
 // of its rows' bytes in flight at once, straight from memory to registers (a
-// lane's 16 bytes are its operand: LDS would add a trip). C comes from the
-// caches, as often as there are workgroups. The waves' sums meet in LDS.
+// lane's 16 bytes are its operand: LDS would add a trip). The next block is on
+// its way while one is multiplied (U = 4 and one block ahead: 14336 x 4096 int8,
+// one column, 13.5 us; U = 8 without: 14.4). C comes from the caches, as often as
+// there are workgroups, which is what bounds more than a few columns. The waves'
+// sums meet in LDS.
 #pragma once
 
 #include "tile_product.hpp"

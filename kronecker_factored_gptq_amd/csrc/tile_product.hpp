@@ -10,6 +10,16 @@
 // inside an instruction does not matter. The result's lane l, register i holds
 // D[4 * (l / 16) + i][l % 16].
 //
+// What bounds a large product: with 256 x 256 tiles a step (128 bytes of k) is 64
+// matrix instructions of 16 cycles on each of two waves a SIMD, 20 LDS reads a wave
+// and 64 KB from the L2. The instructions alone run at 4.3e15 op/s (int8 codes)
+// and 2.2e15 flop/s (bfloat16) here; the loads alone would take 0.85 of the int8
+// product's time and 0.55 of a bfloat16 one's, so they have to flow all the time: the
+// ring of five slots (against two whole steps: 393 -> 380 us for 8192 x 14336 x
+// 4096 int8), the loads spread over the step (cross entropy's gradient 11.8 -> 11.3
+// ms), the LDS reads among the multiplications (412 -> 393). Four waves of 128 x
+// 128 read less LDS but leave one wave to a SIMD and cost register copies: 432 us.
+//
 // Pairs of planes: a float32 operand is held as bfloat16 planes x = x1 + x2 +
 // x3 (exact, 8 bits each, split_bf16), and a product is the sum over the pairs
 // of planes whose terms reach the result's precision, all added into the same
