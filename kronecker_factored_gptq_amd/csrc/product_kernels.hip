@@ -97,7 +97,7 @@ hipError_t launch_quantize_tokens(int64_t T, int64_t n, const X* x, int64_t ldx,
 // (n <= 131071); one float32 rounding each for the sum and the two scales, one
 // to the output's type. The tile's rows are channels and its columns tokens,
 // so a lane's four accumulators are four consecutive outputs of one token.
-// 8192 x 14336 x 4096 to bfloat16, 256 x 256 tiles: 381 to 404 us from box to box,
+// 8192 x 14336 x 4096 to bfloat16, 256 x 256 tiles: 381 to 404 us from card to card,
 // 2.4 to 2.5e15 op/s (a library's largest int8 product reaches 2.4e15 here).
 // ---------------------------------------------------------------------------
 template <typename O, int BR, int BC, int WR, int WC, bool ANY>

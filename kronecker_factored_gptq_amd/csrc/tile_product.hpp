@@ -622,6 +622,7 @@ inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, bool kmajor, boo
         least = t;
         best = {tile, n};
       }
+      if (t > 2 * least) break;  // past the tile's best: the sums only grow
     }
   }
   return best;
