@@ -138,18 +138,21 @@ __device__ inline v4i load_any(const char* row, int64_t k, int64_t kbytes) {
 
 // How an operand lies in memory and in LDS: its rows along k (kbytes of k in
 // each), or k-major (k its rows, `ld` apart, its tile's rows side by side).
-template <class M, int BR, int BC, int WR, int WC, bool RK = false, bool CK = false>
+template <class M, int BR, int BC, int WR, int WC, bool RK = false, bool CK = false,
+          int SLOTS = 5>
 struct TileProduct {
   typedef typename M::acc_t acc_t;
   static constexpr int kWaves = WR * WC;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int FR = BR / WR / 16, FC = BC / WC / 16;
-  // LDS is a ring of five slots, each one step of one operand: step s of R in
-  // slot 2 s mod 5, of C in the next. With two whole steps' slots (four) every
-  // load would have to land before the next goes out; the fifth keeps the next
-  // step but one of R in flight meanwhile, and the memory path busy.
+  // LDS is a ring of SLOTS = 2 D + 1 slots, each one step of one operand: step s of
+  // R in slot 2 s mod SLOTS, of C in the next. With whole steps only, every load
+  // of a step would have to land before the next go out; the odd slot keeps R of
+  // one more step in flight meanwhile, and the memory path busy.
   static constexpr int kSlot = BR * kStepBytes;
-  static constexpr int kLds = 5 * kSlot;
+  static constexpr int kLds = SLOTS * kSlot;
+  static constexpr int D = SLOTS / 2;
+  static_assert(SLOTS % 2 == 1 && D >= 2, "whole steps and one more");
   static_assert(BR == BC, "one slot size");
   static constexpr int LR = BR * kStepBytes / 1024 / kWaves;  // wave loads per step
   static constexpr int LC = BC * kStepBytes / 1024 / kWaves;
@@ -347,7 +350,7 @@ struct TileProduct {
                lds + slot * kSlot + j * kWaves * 1024);
     }
     __device__ inline void advance() {
-      slot = slot >= 3 ? slot - 3 : slot + 2;
+      slot = slot + 2 >= SLOTS ? slot + 2 - SLOTS : slot + 2;
       if (++k == ksteps && pair + 1 < npairs) {
         k = 0;
         ++pair;
@@ -393,27 +396,25 @@ struct TileProduct {
     };
     auto none = [](int) {};
 
-    load_r();
-    load_c();
-    if (total > 1) {
-      load_r();
-      load_c();
+#pragma unroll
+    for (int u = 0; u <= D; ++u) {  // steps 0 to D - 1, and R of step D
+      if (u < total) load_r();
+      if (u < D && u < total) load_c();
     }
-    if (total > 2) load_r();
-    if (total > 2)
-      wait_barrier<2 * LR + LC>();
+    if (total > D)
+      wait_barrier<D * LR + (D - 1) * LC>();
     else
       wait_barrier<0>();
     // A step's second half is multiplied while the next step's first half is
     // read from LDS, and its first half while its second half is read. In
     // between all waves have read the step, and its slots are loaded anew: with C
-    // of the next step but one in this half, R of the one after in the next.
+    // of step s + D in this half, R of step s + D + 1 in the next.
     unsigned slot = 0;  // of this step's R
     const char *pr = lds, *pc = lds + kSlot;
     auto next_slots = [&]() {
-      slot = slot >= 3 ? slot - 3 : slot + 2;
+      slot = slot + 2 >= SLOTS ? slot + 2 - SLOTS : slot + 2;
       pr = lds + slot * kSlot;
-      pc = slot == 4 ? lds : pr + kSlot;
+      pc = slot == SLOTS - 1 ? lds : pr + kSlot;
     };
     Frags a, b;
     read(a, pr, pc, 0);
@@ -421,8 +422,10 @@ struct TileProduct {
     auto next_c = [&](int u) { lc.load(u); };
     int s = 0;
     half_step<0>(a, b, pr, pc, 1, none);
-    for (; s < total - 3; ++s) {
-      wait_barrier<LR>();  // the next step has landed, R of the one after may be in flight
+    // the next step has landed; what was issued after its C may be in flight
+    constexpr int kAhead = (D - 1) * LR + (D - 2) * LC;
+    for (; s < total - D - 1; ++s) {
+      wait_barrier<kAhead>();
       next_slots();
       half_step<LC>(b, a, pr, pc, 0, next_c);
       lc.advance();
@@ -430,12 +433,12 @@ struct TileProduct {
       lr.advance();
     }
     for (; s < total - 1; ++s) {
-      if (s == total - 3)
-        wait_barrier<LR>();
+      if (s == total - D - 1)
+        wait_barrier<kAhead>();
       else
         wait_barrier<0>();
       next_slots();
-      if (s == total - 3) load_c();  // the last step's
+      if (s == total - D - 1) load_c();  // the last step's
       half_step<0>(b, a, pr, pc, 0, none);
       half_step<0>(a, b, pr, pc, 1, none);
     }

@@ -128,6 +128,17 @@ def test_matmul_int8(gpu_lib, T, m, n, t):
     check_product(gpu_lib, int8(T, n, g), int8(m, n, g, -8, 7), n, sx, sv, t)
 
 
+@pytest.mark.parametrize("T,m,n", [
+    (20, 15000, 2560), (9, 13001, 5216), (70, 9000, 2700), (128, 14000, 2689), (900, 4000, 2570), (1000, 3900, 5200),
+])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_matmul_int8_few_tiles_long_rows(gpu_lib, T, m, n, t):
+    """Tiles that have a CU almost to themselves and many steps of n."""
+    g = torch.Generator().manual_seed(T + 3 * m + 7 * n)
+    sx, sv = torch.rand(T, generator=g) + 0.5, torch.rand(m, generator=g) + 0.5
+    check_product(gpu_lib, int8(T, n, g), int8(m, n, g, -8, 7), n, sx, sv, t)
+
+
 @pytest.mark.parametrize("T", [1, 13, 40, 150, 2500])
 @pytest.mark.parametrize("n,pad", [(512, 16), (512, 3), (500, 12), (499, 0), (1, 15), (31, 1)])
 def test_matmul_int8_strides(gpu_lib, T, n, pad):
