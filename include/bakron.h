@@ -472,10 +472,14 @@ int bakron_sample_sqnorms(int dtype, int64_t N, int64_t d, const void *X, int64_
  * the sum, its product with sx and that with sv are rounded to float32 in this
  * order, then once to ytype. Rows that start at multiples of 16 bytes
  * with n a multiple of 16 are read fastest; any alignment and stride works.
- * Y must not overlap the inputs (BAKRON_EINVAL). The workspace query gives 0,
+ * Y must not overlap the inputs (BAKRON_EINVAL; matrices are compared from their
+ * first element to their last, the gaps between rows included, here and
+ * below). The workspace query gives 0,
  * and workspace may be NULL, where the call needs none.
  *
- * Both are asynchronous and deterministic. T, m <= 2^31 - 1.
+ * Both are asynchronous and deterministic. T, m < 2^24; a product of T x m
+ * around 2^38 or of (T + m) x n around 2^36 and beyond, more than one launch
+ * holds, is BAKRON_EINVAL.
  * ------------------------------------------------------------------------ */
 int bakron_quantize_tokens(int xtype, int64_t T, int64_t n, const void *X, int64_t ldx,
                            const float *channel, int8_t *Xq, int64_t ldq, float *sx, void *stream);
@@ -498,8 +502,8 @@ int bakron_matmul_int8(int ytype, int64_t T, int64_t m, int64_t n,
  * G[t][i] sv[i] is rounded to float32 and then, for BF16 and F16, to 11 bits
  * (down to 2^-28 of the token's largest, and to 2^-39 of it below); F32 keeps
  * all 24. Products are exact, sums float32, one rounding to gtype.
- * dX must not overlap the inputs (BAKRON_EINVAL). m, n <= 2^20. Asynchronous,
- * deterministic.
+ * dX must not overlap the inputs (BAKRON_EINVAL). m, n <= 2^20, T < 2^24; T x m
+ * or m x n around 2^35 and beyond is BAKRON_EINVAL. Asynchronous, deterministic.
  * ------------------------------------------------------------------------ */
 size_t bakron_matmul_int8_grad_workspace_bytes(int gtype, int64_t T, int64_t m, int64_t n);
 int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n,
@@ -537,8 +541,9 @@ int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n,
  * float32's bits for F32; sums are float32. A token without a target takes no
  * part, whatever its X, lse or g hold. T = 0 gives dW = 0.
  *
- * Outputs must not overlap the inputs or each other (BAKRON_EINVAL). V >= 1;
- * T, d <= 2^20. Rows that start at multiples of 16 bytes with d a multiple of
+ * Outputs must not overlap the inputs or each other (BAKRON_EINVAL). 1 <= V <
+ * 2^24; T, d <= 2^20; T x V, T x d or V x d beyond what a launch holds (from about
+ * 2^38, 2^35 and 2^35 on) is BAKRON_EINVAL. Rows that start at multiples of 16 bytes with d a multiple of
  * 8 are read fastest (BF16, F16); any alignment and stride works.
  * Asynchronous, deterministic.
  * ------------------------------------------------------------------------ */

@@ -4,7 +4,6 @@
 // nothing here touches data.
 #include <hip/hip_runtime.h>
 
-#include <climits>
 #include <cstdint>
 #include <initializer_list>
 
@@ -37,14 +36,18 @@ inline int status(hipError_t e) { return e == hipSuccess ? BAKRON_OK : BAKRON_EH
 
 // the largest n whose int8 sums fit int32: 128 * 128 * 131071 < 2^31
 constexpr int64_t kMaxInt8Sum = 131071;
-// the most tiles of 128 x 128 one launch covers
+// A launch holds fewer than 2^32 threads: 2^24 - 1 workgroups of 256.
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;
+// whether tiles of 128 x 128 over an a x b output fit one launch
 inline bool tiles_ok(int64_t a, int64_t b) {
-  return ((a + 127) / 128) * ((b + 127) / 128) <= INT_MAX;
+  return ((a + 127) / 128) * ((b + 127) / 128) <= kMaxGroups;
 }
+// the workgroups that lay out `rows` rows of 16-bit planes, eight elements a thread
+inline int64_t plane_groups(int64_t rows, int64_t cols) { return rows * (cols + 64) / 2048 + 1; }
 
 inline bool int8_sizes_ok(int64_t T, int64_t m, int64_t n) {
-  return T >= 0 && m >= 0 && n >= 0 && T <= INT_MAX && m <= INT_MAX && n <= kMaxInt8Sum &&
-         tiles_ok(T, m);
+  return T >= 0 && m >= 0 && n >= 0 && T <= kMaxGroups && m <= kMaxGroups && n <= kMaxInt8Sum &&
+         tiles_ok(T, m) && (T + m) * (n + 128) / 4096 < kMaxGroups;  // rows laid out, 16 bytes a thread
 }
 
 constexpr size_t kAlign = 256;
@@ -53,14 +56,16 @@ constexpr size_t kAlign = 256;
 // product's 32-bit offsets.
 constexpr int64_t kMaxPlaneCols = (int64_t)1 << 20;
 inline bool grad_sizes_ok(int t, int64_t T, int64_t m, int64_t n) {
-  return type_ok(t) && T >= 0 && m >= 0 && n >= 0 && T <= INT_MAX && m <= kMaxPlaneCols &&
-         n <= kMaxPlaneCols && T * (m + 64) <= ((int64_t)1 << 41) &&
-         T + (m + 64) * (n + 64) / 2048 < INT_MAX;
+  return type_ok(t) && T >= 0 && m >= 0 && n >= 0 && T <= kMaxGroups && m <= kMaxPlaneCols &&
+         n <= kMaxPlaneCols && tiles_ok(T, n) &&
+         T + plane_groups(T, m) + plane_groups(m, n) <= kMaxGroups;
 }
 
 inline bool entropy_sizes_ok(int t, int64_t T, int64_t d, int64_t V) {
   return type_ok(t) && T >= 0 && d >= 0 && V >= 1 && T <= kMaxPlaneCols && d <= kMaxPlaneCols &&
-         V <= INT_MAX && tiles_ok(T, V) && tiles_ok(d, V);
+         V <= kMaxGroups && tiles_ok(T, V) && tiles_ok(d, V) && tiles_ok(T, d) &&
+         plane_groups(T, d) <= kMaxGroups &&
+         plane_groups(V < kMaxPlaneCols ? V : kMaxPlaneCols, d) <= kMaxGroups;
 }
 
 }  // namespace
@@ -69,7 +74,7 @@ extern "C" {
 
 int bakron_quantize_tokens(int xtype, int64_t T, int64_t n, const void* X, int64_t ldx,
                            const float* channel, int8_t* Xq, int64_t ldq, float* sx, void* stream) {
-  if (!type_ok(xtype) || T < 0 || n < 0 || T > INT_MAX) return BAKRON_EINVAL;
+  if (!type_ok(xtype) || T < 0 || n < 0 || T > kMaxGroups) return BAKRON_EINVAL;
   if (T == 0) return BAKRON_OK;
   if (!matrix_ok(X, T, n, ldx, type_size(xtype)) || !matrix_ok(Xq, T, n, ldq, 1)) return BAKRON_EINVAL;
   if (!sx || (uintptr_t)sx % 4 || (uintptr_t)channel % 4) return BAKRON_EINVAL;
@@ -128,7 +133,7 @@ int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n, const vo
   if (!grad_sizes_ok(gtype, T, m, n)) return BAKRON_EINVAL;
   if (T == 0 || n == 0) return BAKRON_OK;
   const size_t es = type_size(gtype);
-  if (!tiles_ok(T, n) || !matrix_ok(G, T, m, ldg, es) || !matrix_ok(Vq, m, n, ldv, 1) ||
+  if (!matrix_ok(G, T, m, ldg, es) || !matrix_ok(Vq, m, n, ldv, 1) ||
       !matrix_ok(dX, T, n, ldx, es))
     return BAKRON_EINVAL;
   if ((uintptr_t)sv % 4 || (uintptr_t)channel % 4) return BAKRON_EINVAL;

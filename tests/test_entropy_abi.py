@@ -45,6 +45,15 @@ def _grad(**kw):
                                               a["ws"], a["wsb"], None)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(V=1 << 24), dict(T=1 << 20, V=1 << 18), dict(T=1 << 18, d=1 << 18, ldx=1 << 18, ldw=1 << 18, lddx=1 << 18, lddw=1 << 18),
+    dict(V=1 << 18, d=1 << 18, ldx=1 << 18, ldw=1 << 18, lddx=1 << 18, lddw=1 << 18),
+])
+def test_sizes_past_a_launch_are_refused(kw):
+    assert _grad(**kw) == bk.EINVAL
+    assert _forward(**{k: v for k, v in kw.items() if k not in ("lddx", "lddw")}) == bk.EINVAL
+
+
 @pytest.mark.parametrize("bad", [
     dict(t=bk.F64), dict(t=-1), dict(T=-1), dict(d=-1), dict(V=0), dict(T=(1 << 20) + 1), dict(V=1 << 31),
     dict(X=None), dict(W=None), dict(y=None), dict(lse=None), dict(g=None), dict(ldx=3), dict(ldw=3), dict(lddx=3),

@@ -236,6 +236,26 @@ def test_empty(gpu_lib):
     assert (lse.cpu().double() - math.log(9)).abs().max() <= 2.0 ** -15 and loss[2] == 0
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_no_hidden_size_and_many_tokens(gpu_lib, t):
+    X, W = torch.empty(150, 0, dtype=TYPES[t], device="cuda"), torch.empty(300, 0, dtype=TYPES[t], device="cuda")
+    loss, lse = gpu_lib.cross_entropy(X, W, torch.arange(150, device="cuda"))
+    for v in (loss, lse):  # every logit is 0
+        assert (v.cpu().double() - math.log(300)).abs().max() <= 2.0 ** -15
+    dX, dW = gpu_lib.cross_entropy_grad(X, W, torch.arange(150, device="cuda"), lse, torch.ones(150, device="cuda"))
+    assert dX.shape == (150, 0) and dW.shape == (300, 0)
+
+
+@pytest.mark.parametrize("T", [9, 90])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_rows_far_apart(gpu_lib, T, t):
+    """Rows of W more than 4 MB apart, all aligned."""
+    X, W, y, g = inputs(T, 72, 130, t, T)
+    far = torch.full((130, 2200000), float("nan"), dtype=TYPES[t], device="cuda")
+    far[:, :72] = W
+    check(gpu_lib, X, far[:, :72], y, g, t)
+
+
 @pytest.mark.parametrize("T,V", [(5, 700), (140, 300)])
 def test_gradient_is_the_losses_derivative(gpu_lib, T, V):
     """Differences of the 64-bit loss along random directions against the float32

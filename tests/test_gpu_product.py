@@ -139,6 +139,28 @@ def test_matmul_int8_few_tiles_long_rows(gpu_lib, T, m, n, t):
     check_product(gpu_lib, int8(T, n, g), int8(m, n, g, -8, 7), n, sx, sv, t)
 
 
+@pytest.mark.parametrize("T", [5, 150])
+def test_matmul_int8_rows_far_apart(gpu_lib, T):
+    """Rows of codes more than 4 MB apart, all aligned; the gradient through them."""
+    g = torch.Generator().manual_seed(T)
+    X, V, sx, sv = int8(T, 160, g), int8(90, 160, g), torch.rand(T, generator=g) + 0.5, torch.rand(90, generator=g) + 0.5
+    far = torch.full((90, 4400000), 99, dtype=torch.int8, device="cuda")
+    far[:, :160] = V.cuda()
+    a = gpu_lib.matmul_int8(X.cuda(), sx.cuda(), far[:, :160], sv.cuda())
+    assert torch.equal(a, check_product(gpu_lib, X, V, 160, sx, sv, "f32"))
+    G = torch.randn(T, 90, generator=g).cuda()
+    assert torch.equal(gpu_lib.matmul_int8_grad(G, far[:, :160], sv.cuda()), gpu_lib.matmul_int8_grad(G, V.cuda(), sv.cuda()))
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_matmul_int8_empty_sums_of_many_tokens(gpu_lib, t):
+    e = dict(dtype=torch.int8, device="cuda")
+    Y = gpu_lib.matmul_int8(torch.empty(200, 0, **e), torch.ones(200, device="cuda"), torch.empty(333, 0, **e), out_dtype=TYPES[t])
+    assert Y.shape == (200, 333) and (Y == 0).all()
+    D = gpu_lib.matmul_int8_grad(torch.empty(200, 0, dtype=TYPES[t], device="cuda"), torch.empty(0, 333, **e))
+    assert D.shape == (200, 333) and (D == 0).all()
+
+
 @pytest.mark.parametrize("T", [1, 13, 40, 150, 2500])
 @pytest.mark.parametrize("n,pad", [(512, 16), (512, 3), (500, 12), (499, 0), (1, 15), (31, 1)])
 def test_matmul_int8_strides(gpu_lib, T, n, pad):

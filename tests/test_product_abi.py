@@ -97,6 +97,17 @@ def test_matmul_int8_grad_empty_and_workspace():
     assert q(bk.F64, 64, 64, 64) == q(bk.F32, -1, 64, 64) == q(bk.F32, 64, 1 << 21, 64) == 0
 
 
+def test_sizes_past_a_launch_are_refused():
+    big = 1 << 24
+    assert _quantize(T=big) == bk.EINVAL
+    for kw in (dict(T=big), dict(m=big, ldy=big), dict(T=1 << 20, m=1 << 19, ldy=1 << 19),
+               dict(T=1 << 20, n=100001, ldx=100001, ldv=100001)):
+        assert _matmul(**kw) == bk.EINVAL
+    for kw in (dict(T=big), dict(T=1 << 18, m=1 << 18, ldg=1 << 18),
+               dict(m=1 << 18, n=1 << 18, ldg=1 << 18, ldv=1 << 18, ldx=1 << 18)):
+        assert _grad(**kw) == bk.EINVAL
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 4)
     q = torch.zeros(2, 4, dtype=torch.int8)
