@@ -19,8 +19,8 @@
 // PFLOP/s in 256 x 256 tiles; a tile's epilogue, 65536 exponentials, takes its share
 // of what is missing to a plain product), gradient 10.0 to 10.4 ms (1.25 to 1.29): D
 // 0.89 ms a piece, D W 0.77, D^T X 0.89. One token, d = 2048, 50257 words, float16:
-// 45 us (4.5 TB/s). 333 x 1000 x 10007 float32, gradient: 217 us, of them 16 for W's
-// planes and 180 for six plane products in each of the three products.
+// 45 us (4.5 TB/s). 333 x 1000 x 10007 float32, gradient: 212 us, of them 16 for W's
+// planes and 183 for six plane products in each of the three products.
 #include <initializer_list>
 
 #include "launch.hpp"
@@ -481,8 +481,8 @@ hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t l
         return e;
       wo = {p.w, p.ld, p.plane, rows, 0};
     }
-    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes * pairs.n;
-    const int tile = plan_tiles(rows, T, steps, false, false).tile;
+    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes;
+    const int tile = plan_tiles(rows, T, steps, pairs.n, false, false).tile;
     if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
       e = start_entropy<M, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
     else if (tile == 256)
@@ -546,8 +546,8 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
     }
     const TileOperand wo = {wp.w, wp.ld, wp.plane, rows, 0};
     const Planes P = {b + L.p, plane_ld(rows), T * plane_ld(rows)};
-    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes * pairs.n;
-    const int tile = plan_tiles(rows, T, steps, false, false).tile;
+    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes;
+    const int tile = plan_tiles(rows, T, steps, pairs.n, false, false).tile;
     if (tile == 256)
       e = start_entropy_diff<M, K::split, 256, 256, 2, 4>(wo, xo, kbytes, pairs, y, V, v0, lse,
                                                           dscale<X>(), P, s);

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void plane_join_kernel(int64_t M, int64_t N, i
 }
 
 static TilePlan plane_plan(int64_t M, int64_t N, int64_t K, int npairs) {
-  return plan_tiles(M, N, (K + 63) / 64 * npairs, true, true);
+  return plan_tiles(M, N, (K + 63) / 64, npairs, true, true);
 }
 size_t plane_product_bytes(int64_t M, int64_t N, int64_t K, int npairs) {
   return (size_t)split_words(M, N, plane_plan(M, N, K, npairs).splits) * 4;

@@ -298,7 +298,7 @@ static int64_t skinny_tokens(int64_t m, int64_t n) {
 }
 
 static TilePlan int8_plan(int64_t T, int64_t m, int64_t n) {
-  return plan_tiles(m, T, (n + kStepBytes - 1) / kStepBytes, false, true);
+  return plan_tiles(m, T, (n + kStepBytes - 1) / kStepBytes, 1, false, true);
 }
 static bool int8_packs(int64_t T, int64_t m, int64_t n) {
   return n % 16 != 0 && T > skinny_tokens(m, n);

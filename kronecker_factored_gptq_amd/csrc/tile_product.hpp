@@ -587,40 +587,58 @@ __device__ inline void store_sums(const TP& tp, int64_t r0, int64_t c0, int64_t 
 
 // The tile of a product, and the ranges its k is split into. 256 x 256 tiles
 // (one workgroup a CU) need the fewest bytes and are taken where they fill the
-// chip. Below that the choice is by an estimate of the time in us, fitted to
-// measurements over 300 x 700 to 14336 x 4096 and 20 to 2048 columns:
-// - 128 x 128 (two workgroups a CU) and 64 x 64 tiles (four): with c workgroups
-//   on each CU a step takes 0.28 + 0.4 c and 0.19 + 0.175 c (bound by the L2; one
-//   workgroup alone by latency, 0.5 and 0.35), and k-major operands 0.15 more of
-//   the small tile; filling the ring takes 3 and 1;
-// - k split into n ranges, each summed apart: 3 for the kernel that joins them,
-//   and their sums, written and read again, at 3.5 bytes a ps.
-// (int8, 4096 x 4096 and 256 columns: 12 us with 64 x 64 tiles, 20 with 128 x
-// 128; 14336 x 4096 and 256: 27 and 23; 4096 x 14336 and 128: 58 in one range, 22
-// in eight.)
+// chip. Below that the choice is by an estimate of the time in us, of 128 x 128
+// tiles (two workgroups a CU) and 64 x 64 tiles (four):
+// - with c workgroups on each CU a step takes step + share c (bound by the L2), and
+//   at least `alone` (bound by latency); k-major operands 0.15 more of the
+//   small tile; filling the ring and the epilogue take `fill`;
+// - k split into n ranges, each summed apart: `join` for the kernel that joins
+//   them, and their sums, written and read again, at `rate` bytes a ps.
+// The constants are fitted to measurements: of int8 products over 1000 x 1504 to
+// 28672 x 4096 with 20 to 800 columns, every tile and split of each, weights from
+// memory (the choice is within 0.6% of the best one on average; fitted to fewer
+// it was 5%: 2048 x 16384 and 20 columns 16.1 us, now 13.1; 5120 x 13824 and 128
+// 31.8, now 26.5; a bfloat16 gradient of 4096 x 4096 and 512 51, now 41). For several
+// pairs of planes, which read the same planes again and again, of float32
+// gradients (with the other constants 333 x 1000 x 10007 of the cross entropy's
+// takes 237 us, not 214).
+struct TileCost {
+  double step, share, alone, fill;
+};
+struct PlanCosts {
+  TileCost tile[2];  // 128 x 128, 64 x 64
+  double join, rate;
+};
+constexpr PlanCosts kCostsOne = {{{0.15, 0.48, 0.61, 2.2}, {0.1, 0.26, 0.29, 1.5}}, 2.2, 2.2};
+constexpr PlanCosts kCostsPairs = {{{0.28, 0.4, 0.5, 3}, {0.19, 0.175, 0.35, 1}}, 3, 3.5};
 struct TilePlan {
   int tile, splits;
 };
 inline int64_t tiles_of(int64_t M, int64_t N, int64_t tile) {
   return ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
 }
-inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, bool kmajor, bool may_split) {
+// steps: of one pair.
+inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, int pairs, bool kmajor,
+                           bool may_split) {
   TilePlan best = {128, 1};
   if (M <= 0 || N <= 0) return best;
   if (tiles_of(M, N, 256) >= 192) return {256, 1};
+  const PlanCosts& costs = pairs > 1 ? kCostsPairs : kCostsOne;
+  steps *= pairs;
   double least = 1e300;
-  const double word = (double)M * (double)N * 8 / 3.5e6;
+  const double sums = (double)M * (double)N * 8 / (costs.rate * 1e6);
   for (int tile : {128, 64}) {
     const bool small = tile == 64;
+    const TileCost& cost = costs.tile[small];
     const int64_t tiles = tiles_of(M, N, tile), slots = small ? 1024 : 512;
     for (int n = 1; n == 1 || (may_split && n * tiles <= slots && n <= steps / 2); ++n) {
       const int64_t rounds = (n * tiles + slots - 1) / slots;
       const double c = rounds > 1 ? (double)slots / 256 : (double)(n * tiles) / 256;
-      double each = small ? 0.19 + 0.175 * c : 0.28 + 0.4 * c;
-      if (each < (small ? 0.35 : 0.5)) each = small ? 0.35 : 0.5;
+      double each = cost.step + cost.share * c;
+      if (each < cost.alone) each = cost.alone;
       if (small && kmajor) each += 0.15;
-      const double t = (double)rounds * each * (double)((steps + n - 1) / n) + (small ? 1 : 3) +
-                       (n > 1 ? 3 + n * word : 0);
+      const double t = (double)rounds * each * (double)((steps + n - 1) / n) + cost.fill +
+                       (n > 1 ? costs.join + n * sums : 0);
       if (t < least) {
         least = t;
         best = {tile, n};
