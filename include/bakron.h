@@ -538,7 +538,10 @@ int bakron_matmul_int8_grad(int gtype, int64_t T, int64_t m, int64_t n,
  * both of xtype. The logits are formed again by pieces of the vocabulary whose
  * D is held in the workspace: in bfloat16 for BF16 (an error of 2^-9 to 2^-8 a
  * term, as the outputs' own), in float16 scaled by 2^14 for F16, with all of
- * float32's bits for F32; sums are float32. A token without a target takes no
+ * float32's bits for F32; sums are float32. For dW the product X[t] g[t] / max |g|
+ * is rounded to xtype too, before the sum over tokens (no rounding where every g is
+ * the same or 0; F16: to 11 bits down to 2^-28 of the largest such product, and to
+ * 2^-39 of it below); dX takes g in float32. A token without a target takes no
  * part, whatever its X, lse or g hold. T = 0 gives dW = 0.
  *
  * Outputs must not overlap the inputs or each other (BAKRON_EINVAL). 1 <= V <

@@ -240,13 +240,48 @@ __global__ __launch_bounds__(256) void entropy_join_kernel(
   }
 }
 
+// The largest |x| of each token, for float16's weights below.
+template <typename X>
+__global__ __launch_bounds__(256) void entropy_reach_kernel(int64_t d, const X* __restrict__ x,
+                                                            int64_t ldx, bool vec,
+                                                            float* __restrict__ reach) {
+  __shared__ unsigned red[4];
+  const RowOf<X, 0> row(x + (int64_t)blockIdx.x * ldx, d, vec);
+  unsigned top = 0;
+  row.each(d, [&](int64_t, const Eight<X>& t) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned a = __float_as_uint(to_f32(t.v[e])) & 0x7fffffffu;
+      top = a > top ? a : top;
+    }
+  });
+  top = max_of_256(top, red);
+  if (threadIdx.x == 0) reach[blockIdx.x] = __uint_as_float(top);
+}
+
 // w[t] = g[t] for a token with a target, else 0; top = max |w|; rel = w / top
-// (0 where top is 0). One workgroup. The maximum is taken over bits, in which a
-// NaN is larger than infinity.
+// (0 where top is 0). rel X is rounded to X's type for dW. With `reach`
+// (float16, whose normal numbers end at 2^-14): rel times, and top divided by, the power
+// of two that brings the largest |rel X| to [2^14, 2^15), so that 11 bits are kept down to
+// 2^-28 of it. One workgroup. Maxima are taken over bits, in which a NaN is larger than
+// infinity.
 __global__ __launch_bounds__(1024) void entropy_weights_kernel(
     int64_t T, int64_t V, const int64_t* __restrict__ y, const float* __restrict__ g,
-    float* __restrict__ w, float* __restrict__ rel, float* __restrict__ top) {
+    const float* __restrict__ reach, float* __restrict__ w, float* __restrict__ rel,
+    float* __restrict__ top) {
   __shared__ unsigned red[16];
+  auto largest = [&](unsigned m) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const unsigned u = __shfl_xor(m, o, 64);
+      m = u > m ? u : m;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    for (int k = 0; k < 16; ++k) m = red[k] > m ? red[k] : m;
+    return m;
+  };
   unsigned m = 0;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const float v = y[t] >= 0 && y[t] < V ? g[t] : 0.0f;
@@ -254,17 +289,24 @@ __global__ __launch_bounds__(1024) void entropy_weights_kernel(
     const unsigned a = __float_as_uint(v) & 0x7fffffffu;
     m = a > m ? a : m;
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const unsigned u = __shfl_xor(m, o, 64);
-    m = u > m ? u : m;
-  }
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  for (int k = 0; k < 16; ++k) m = red[k] > m ? red[k] : m;
+  m = largest(m);
   const float mx = __uint_as_float(m);
-  if (threadIdx.x == 0) *top = mx;
-  for (int64_t t = threadIdx.x; t < T; t += 1024) rel[t] = m == 0 ? 0.0f : w[t] / mx;
+  int k = 0;
+  if (reach) {
+    unsigned r = 0;
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+      const float v = w[t] == 0.0f ? 0.0f : w[t] / mx * reach[t];
+      const unsigned a = __float_as_uint(v) & 0x7fffffffu;
+      r = a > r ? a : r;
+    }
+    r = largest(r);
+    const int e = (int)(r >> 23) - 127;
+    k = r == 0 || e > 127 ? 0 : e < -112 ? 126 : 14 - e;  // 2^k and 2^-k normal
+  }
+  const float up = __uint_as_float((unsigned)(127 + k) << 23);
+  if (threadIdx.x == 0) *top = mx * __uint_as_float((unsigned)(127 - k) << 23);
+  for (int64_t t = threadIdx.x; t < T; t += 1024)
+    rel[t] = w[t] == 0.0f ? 0.0f : w[t] / mx * up;
 }
 
 // D's planes of a piece, rows the tokens, written up to the planes' padding, with
@@ -422,7 +464,7 @@ size_t entropy_bytes(int es, int64_t T, int64_t d, int64_t V) {
 }
 
 struct GradLayout {
-  size_t w, rel, top, xp, xs, wp, p, acc, parts, total;
+  size_t w, rel, reach, top, xp, xs, wp, p, acc, parts, total;
   int64_t piece, ldacc;
 };
 static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
@@ -432,7 +474,8 @@ static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
   L.ldacc = (d + 3) / 4 * 4;
   L.w = 0;
   L.rel = L.w + up256((size_t)T * 4);
-  L.top = L.rel + up256((size_t)T * 4);
+  L.reach = L.rel + up256((size_t)T * 4);
+  L.top = L.reach + (es == 2 ? up256((size_t)T * 4) : 0);
   L.xp = L.top + 256;
   L.xs = L.xp + up256((size_t)(np * T * plane_ld(d)));
   L.wp = L.xs + up256((size_t)(np * T * plane_ld(d)));
@@ -532,9 +575,17 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
   float *wt = (float*)(b + L.w), *rel = (float*)(b + L.rel), *top = (float*)(b + L.top);
   float *acc = (float*)(b + L.acc), *parts = (float*)(b + L.parts);
   const PlanePairs pairs = pairs_of<X>();
-  hipLaunchKernelGGL(entropy_weights_kernel, dim3(1), dim3(1024), 0, s, T, V, y, g, wt, rel, top);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e;
+  float* reach = nullptr;
+  if (K::f16 && dW) {
+    reach = (float*)(b + L.reach);
+    hipLaunchKernelGGL(entropy_reach_kernel<X>, dim3((unsigned)T), dim3(256), 0, s, d, x, ldx,
+                       load8_ok(x, ldx), reach);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(entropy_weights_kernel, dim3(1), dim3(1024), 0, s, T, V, y, g, reach, wt, rel,
+                     top);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   // Both operands as they are, where the direct loads can take them (along d for
   // the logits, W also k-major for dX); else as planes.
   constexpr int64_t es = sizeof(X);
