@@ -259,13 +259,13 @@ struct TileProduct {
   // lane. No register is loaded, so the instruction can stand by itself: as a
   // builtin it makes the compiler wait for every such load in flight before a
   // transposing LDS read, which is what run()'s own waits are there to avoid.
+  // m0 holds the LDS address; as an operand the compiler sets it and knows that it did.
   // (s_nop: the wait states from a register write to its use as an address.)
   __device__ static inline void load_lds(v4i rsrc, int voff, int soff, unsigned lds) {
     asm volatile(
-        "s_mov_b32 m0, %3\n\t"
         "s_nop 4\n\t"
         "buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
-        "s"(rsrc), "s"(soff), "s"(lds)
+        "s"(rsrc), "s"(soff), "{m0}"(lds)
         : "memory");
   }
 
