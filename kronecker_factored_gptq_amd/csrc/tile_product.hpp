@@ -11,7 +11,7 @@
 // D[4 * (l / 16) + i][l % 16].
 //
 // What bounds a large product: with 256 x 256 tiles a step (128 bytes of k) is 64
-// matrix instructions of 16 cycles on each of two waves a SIMD, 20 LDS reads a wave
+// matrix instructions of 16 cycles on each of two waves a SIMD, 24 LDS reads a wave
 // and 64 KB from the L2. The instructions alone run at 4.3e15 op/s (int8 codes)
 // and 2.2e15 flop/s (bfloat16) here; the loads alone would take 0.85 of the int8
 // product's time and 0.55 of a bfloat16 one's, so they have to flow all the time: the
@@ -654,11 +654,10 @@ inline int64_t split_words(int64_t M, int64_t N, int splits) {
 }
 
 // ---- planes -----------------------------------------------------------------
-// How a matrix is held for the 16-bit instructions: a float32 value as one, two
-// or three bfloat16 planes, or as float16. Two planes lose at most 2^-16 of the
-// value, three keep all 24 bits.
-enum Split { kBF16x1, kBF16x2, kBF16x3, kF16x1 };
-constexpr int kPlanes[] = {1, 2, 3, 1};
+// How a matrix is held for the 16-bit instructions: as one bfloat16 plane, as three (a
+// float32 value with all of its 24 bits), or as float16.
+enum Split { kBF16x1, kBF16x3, kF16x1 };
+constexpr int kPlanes[] = {1, 3, 1};
 
 // The planes' 16-bit words of x. The first ones are truncated, so that each
 // rest is exact and no finite x overflows; an infinity or a NaN stands in the
@@ -673,19 +672,14 @@ __device__ inline void split16(float x, unsigned short* w) {
     const unsigned u = __float_as_uint(x);
     if ((u & 0x7f800000u) == 0x7f800000u) {
       w[0] = from_f32<BF16>(x).v;
-      w[1] = 0;
-      if (KIND == kBF16x3) w[2] = 0;
+      w[1] = w[2] = 0;
       return;
     }
     w[0] = (unsigned short)(u >> 16);
     const float r = x - __uint_as_float(u & 0xffff0000u);
-    if (KIND == kBF16x2) {
-      w[1] = from_f32<BF16>(r).v;
-    } else {
-      const unsigned v = __float_as_uint(r);
-      w[1] = (unsigned short)(v >> 16);
-      w[2] = from_f32<BF16>(r - __uint_as_float(v & 0xffff0000u)).v;
-    }
+    const unsigned v = __float_as_uint(r);
+    w[1] = (unsigned short)(v >> 16);
+    w[2] = from_f32<BF16>(r - __uint_as_float(v & 0xffff0000u)).v;
   }
 }
 
