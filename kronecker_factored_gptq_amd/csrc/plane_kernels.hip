@@ -133,19 +133,19 @@ __global__ __launch_bounds__(64 * WR * WC) void plane_product_kernel(
              [&](float a, int, int j, int) { return a * sc[j]; });
 }
 
-// The ranges' sums in order, and the epilogue; four columns of one row a thread.
-template <typename O>
+// The ranges' sums in order, and the epilogue; four columns of one row a thread
+// (join_ranges).
+template <typename O, int S>
 __global__ __launch_bounds__(256) void plane_join_kernel(int64_t M, int64_t N, int splits,
                                                          const float* __restrict__ parts,
                                                          int64_t ldp, int64_t stride,
                                                          PlaneEpilogue ep, O* __restrict__ Y,
                                                          int64_t ldy, bool vec) {
-  const int64_t per = ldp / 4;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= N * per) return;
+  __shared__ f32x4 red[S > 1 ? 256 : 1];
+  const int64_t per = ldp / 4, at = JoinAt<S>::at();
   const int64_t c = at / per, r = (at - c * per) * 4;
-  f32x4 a = {0, 0, 0, 0};
-  for (int k = 0; k < splits; ++k) a += *(const f32x4*)(parts + k * stride + c * ldp + r);
+  f32x4 a;
+  if (!join_ranges<S>(parts + c * ldp + r, stride, splits, at < N * per, a, red)) return;
   if (ep.prev) a += *(const f32x4*)(ep.prev + c * ep.ldprev + r);
   const float all = (ep.alpha ? *ep.alpha : 1.0f) * ep.beta;
   const float sc = (ep.col_scale ? ep.col_scale[c] : 1.0f) * all;
@@ -190,8 +190,13 @@ static hipError_t start_plane_product(const TileOperand& R, const TileOperand& C
                      stride);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL(plane_join_kernel<O>, dim3((unsigned)((stride / 4 + 255) / 256)), dim3(256), 0,
-                     s, R.rows, C.rows, splits, parts, ldp, stride, ep, Y, ldy, vec);
+#define BK_JOIN(S)                                                                               \
+  hipLaunchKernelGGL((plane_join_kernel<O, S>),                                                  \
+                     dim3((unsigned)((stride / 4 + 256 / S - 1) / (256 / S))), dim3(256), 0, s,  \
+                     R.rows, C.rows, splits, parts, ldp, stride, ep, Y, ldy, vec)
+  if (join_slices(splits) == 1) BK_JOIN(1);
+  else BK_JOIN(8);
+#undef BK_JOIN
   return hipGetLastError();
 }
 

@@ -150,20 +150,19 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_int8_kernel(
              [&](int a, int i, int j, int e) { return (float)a * st[j] * sr[i][e]; });
 }
 
-// The ranges' sums and the scales; four channels of one token a thread.
-template <typename O>
+// The ranges' sums and the scales; four channels of one token a thread (join_ranges).
+template <typename O, int S>
 __global__ __launch_bounds__(256) void join_int8_kernel(int64_t m, int64_t T, int splits,
                                                         const int* __restrict__ parts, int64_t ldp,
                                                         const float* __restrict__ sx,
                                                         const float* __restrict__ sv,
                                                         O* __restrict__ Y, int64_t ldy, bool vec) {
-  const int64_t per = ldp / 4;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= T * per) return;
+  __shared__ v4i red[S > 1 ? 256 : 1];
+  const int64_t per = ldp / 4, at = JoinAt<S>::at();
   const int64_t t = at / per, r = (at - t * per) * 4;
+  v4i a;
+  if (!join_ranges<S>(parts + t * ldp + r, T * ldp, splits, at < T * per, a, red)) return;
   const float st = sx[t];
-  v4i a = {0, 0, 0, 0};
-  for (int k = 0; k < splits; ++k) a += *(const v4i*)(parts + (k * T + t) * ldp + r);
   O y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e)
@@ -213,9 +212,14 @@ static hipError_t start_matmul_int8(const TileOperand& V, const TileOperand& X, 
                      sv, Y, ldy, vec, (unsigned)nr, (unsigned)nc, splits, parts, ldp);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  const int64_t per = ldp / 4;
-  hipLaunchKernelGGL(join_int8_kernel<O>, dim3((unsigned)((X.rows * per + 255) / 256)), dim3(256), 0,
-                     s, V.rows, X.rows, splits, parts, ldp, sx, sv, Y, ldy, vec);
+  const int64_t groups = X.rows * (ldp / 4);
+#define BK_JOIN(S)                                                                               \
+  hipLaunchKernelGGL((join_int8_kernel<O, S>),                                                   \
+                     dim3((unsigned)((groups + 256 / S - 1) / (256 / S))), dim3(256), 0, s,      \
+                     V.rows, X.rows, splits, parts, ldp, sx, sv, Y, ldy, vec)
+  if (join_slices(splits) == 1) BK_JOIN(1);
+  else BK_JOIN(8);
+#undef BK_JOIN
   return hipGetLastError();
 }
 
