@@ -562,6 +562,14 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
                               void *dX, int64_t lddx, void *dW, int64_t lddw,
                               void *workspace, size_t workspace_bytes, void *stream);
 
+/* Test hook: how a tiled product of M x N outputs over `steps` steps (128 bytes
+ * of k) of each of `pairs` pairs of planes is divided. With *tile = 0: sets *tile and
+ * *splits (ranges of k) to what a call takes; else leaves them. Returns the estimate of its
+ * time in us: 0 for 256 x 256 tiles, which are taken without one, and
+ * infinity for a division that no call may take. Host only. */
+double bakron_debug_plan(int64_t M, int64_t N, int64_t steps, int pairs, int kmajor, int may_split,
+                         int32_t *tile, int32_t *splits);
+
 #ifdef __cplusplus
 }
 #endif

@@ -156,6 +156,8 @@ def lib() -> ctypes.CDLL:
     L.bakron_cross_entropy_grad.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
                                             _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
     L.bakron_cross_entropy_grad.restype = _int
+    L.bakron_debug_plan.argtypes = [_i64, _i64, _i64, _int, _int, _int, _vp, _vp]
+    L.bakron_debug_plan.restype = ctypes.c_double
     _lib = L
     return L
 
@@ -974,6 +976,15 @@ def debug_set_wait_polls(polls: int) -> int:
     """Test hook: the poll bound of the leaf blocks' waits for solves enqueued
     from now on (negative: the default); returns the previous bound."""
     return int(lib().bakron_debug_set_wait_polls(int(polls)))
+
+
+def debug_plan(M: int, N: int, steps: int, pairs: int = 1, kmajor: bool = False, may_split: bool = True,
+               tile: int = 0, splits: int = 0) -> Tuple[int, int, float]:
+    """Test hook: (tile, ranges of k, estimated us) of a tiled product, as a call
+    divides it, or of the division given. Host only."""
+    t, n = _i32(tile), _i32(splits)
+    us = lib().bakron_debug_plan(M, N, steps, pairs, int(kmajor), int(may_split), ctypes.byref(t), ctypes.byref(n))
+    return t.value, n.value, us
 
 
 def solve_schedule(dtype: int, m: int, n: int):

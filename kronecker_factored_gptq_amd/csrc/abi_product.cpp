@@ -231,4 +231,19 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V, const 
                                     (F16*)dX, lddx, (F16*)dW, lddw, workspace, s));
 }
 
+double bakron_debug_plan(int64_t M, int64_t N, int64_t steps, int pairs, int kmajor, int may_split,
+                         int32_t* tile, int32_t* splits) {
+  if (M < 1 || N < 1 || steps < 0 || pairs < 1 || !tile || !splits) return __builtin_inf();
+  if (*tile == 0) {
+    const TilePlan p = plan_tiles(M, N, steps, pairs, kmajor, may_split);
+    *tile = p.tile;
+    *splits = p.splits;
+  }
+  if (*tile == 256) return 0;
+  if ((*tile != 128 && *tile != 64) || *splits < 1 ||
+      !plan_allowed(M, N, steps * pairs, may_split, *tile, *splits))
+    return __builtin_inf();
+  return plan_us(M, N, steps * pairs, pairs, kmajor, *tile, *splits);
+}
+
 }  // extern "C"

@@ -645,29 +645,53 @@ inline int join_slices(int splits) { return splits < 12 ? 1 : 8; }
 //   at least `alone` (bound by latency); k-major operands 0.15 more of the
 //   small tile; filling the ring and the epilogue take `fill`;
 // - k split into n ranges, each summed apart: `join` for the kernel that joins
-//   them, and their sums, written and read again, at `rate` bytes a ps.
+//   them, `range` for each of them, and their sums, written and read again, at `rate` bytes a ps.
 // The constants are fitted to measurements: of int8 products over 1000 x 1504 to
-// 28672 x 4096 with 20 to 800 columns, every tile and split of each, weights from
-// memory (the choice is within 0.6% of the best one on average; fitted to fewer
-// it was 5%: 2048 x 16384 and 20 columns 16.1 us, now 13.1; 5120 x 13824 and 128
-// 31.8, now 26.5; a bfloat16 gradient of 4096 x 4096 and 512 51, now 41). For several
-// pairs of planes, which read the same planes again and again, of float32
-// gradients (with the other constants 333 x 1000 x 10007 of the cross entropy's
-// takes 237 us, not 214).
+// 28672 x 4096 with 20 to 800 columns, the 128 and 64 tiles of each with up to 16 ranges,
+// weights from memory (of those the choice is within 0.6% of the best one on average; fitted to
+// fewer it was 5%). For several pairs of planes, which read the same planes again and
+// again, they are of float32 gradients: with the other constants the cross entropy's of 333 x
+// 1000 x 10007 takes 237 us, not 214, and that of 2048 x 512 x 8000 382, not 354, though that of
+// 512 x 1024 x 32000 takes 663, not 701. Every division that may be taken is compared: over
+// 60 sizes each, a search that gave a tile up once it was twice as slow as the other tile's best
+// cost int8 products 1.2 % on average (304 x 113 x 14592: 11.1 us, now 9.2), float32 input
+// gradients 3 % (1 x 9664 x 256: 17.0, now 14.3), the float32 cross entropy gradient 1.5 %.
 struct TileCost {
   double step, share, alone, fill;
 };
 struct PlanCosts {
   TileCost tile[2];  // 128 x 128, 64 x 64
-  double join, rate;
+  double join, range, rate;
 };
-constexpr PlanCosts kCostsOne = {{{0.15, 0.48, 0.61, 2.2}, {0.1, 0.26, 0.29, 1.5}}, 2.2, 2.2};
-constexpr PlanCosts kCostsPairs = {{{0.28, 0.4, 0.5, 3}, {0.19, 0.175, 0.35, 1}}, 3, 3.5};
+constexpr PlanCosts kCostsOne = {{{0.15, 0.48, 0.61, 2.2}, {0.1, 0.26, 0.29, 1.5}}, 2.2, 0.02, 2.2};
+constexpr PlanCosts kCostsPairs = {{{0.28, 0.4, 0.5, 3}, {0.19, 0.175, 0.35, 1}}, 3, 0.02, 3.5};
 struct TilePlan {
   int tile, splits;
 };
 inline int64_t tiles_of(int64_t M, int64_t N, int64_t tile) {
   return ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
+}
+// Whether tiles of 128 or 64 may have their k in n ranges: all at once on the chip, two steps
+// of all pairs each at least.
+inline bool plan_allowed(int64_t M, int64_t N, int64_t steps, bool may_split, int tile, int64_t n) {
+  return n == 1 || (may_split && n * tiles_of(M, N, tile) <= (tile == 64 ? 1024 : 512) && n <= steps / 2);
+}
+// The estimate, for `steps` of all pairs; `joining`: the part of it that grows with n.
+inline double plan_us(int64_t M, int64_t N, int64_t steps, int pairs, bool kmajor, int tile, int64_t n,
+                      double* joining = nullptr) {
+  const PlanCosts& costs = pairs > 1 ? kCostsPairs : kCostsOne;
+  const bool small = tile == 64;
+  const TileCost& cost = costs.tile[small];
+  const int64_t work = n * tiles_of(M, N, tile), slots = small ? 1024 : 512;
+  const int64_t rounds = (work + slots - 1) / slots;
+  const double c = (double)(rounds > 1 ? slots : work) / 256;
+  double each = cost.step + cost.share * c;
+  if (each < cost.alone) each = cost.alone;
+  if (small && kmajor) each += 0.15;
+  const double sums = (double)M * (double)N * 8 / (costs.rate * 1e6);
+  const double join = cost.fill + (n > 1 ? costs.join + (double)n * (sums + costs.range) : 0);
+  if (joining) *joining = join;
+  return (double)rounds * each * (double)((steps + n - 1) / n) + join;
 }
 // steps: of one pair.
 inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, int pairs, bool kmajor,
@@ -675,29 +699,18 @@ inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, int pairs, bool 
   TilePlan best = {128, 1};
   if (M <= 0 || N <= 0) return best;
   if (tiles_of(M, N, 256) >= 192) return {256, 1};
-  const PlanCosts& costs = pairs > 1 ? kCostsPairs : kCostsOne;
   steps *= pairs;
   double least = 1e300;
-  const double sums = (double)M * (double)N * 8 / (costs.rate * 1e6);
-  for (int tile : {128, 64}) {
-    const bool small = tile == 64;
-    const TileCost& cost = costs.tile[small];
-    const int64_t tiles = tiles_of(M, N, tile), slots = small ? 1024 : 512;
-    for (int n = 1; n == 1 || (may_split && n * tiles <= slots && n <= steps / 2); ++n) {
-      const int64_t rounds = (n * tiles + slots - 1) / slots;
-      const double c = rounds > 1 ? (double)slots / 256 : (double)(n * tiles) / 256;
-      double each = cost.step + cost.share * c;
-      if (each < cost.alone) each = cost.alone;
-      if (small && kmajor) each += 0.15;
-      const double t = (double)rounds * each * (double)((steps + n - 1) / n) + cost.fill +
-                       (n > 1 ? costs.join + n * sums : 0);
+  for (int tile : {128, 64})
+    for (int n = 1; plan_allowed(M, N, steps, may_split, tile, n); ++n) {
+      double joining;
+      const double t = plan_us(M, N, steps, pairs, kmajor, tile, n, &joining);
       if (t < least) {
         least = t;
         best = {tile, n};
       }
-      if (t > 2 * least) break;  // past the tile's best: the sums only grow
+      if (joining > least) break;  // and so for every larger n
     }
-  }
   return best;
 }
 // words of the ranges' sums, rows of M padded to four

@@ -1,0 +1,41 @@
+"""The division of a tiled product over tiles and ranges of k, against an exhaustive
+search of its own estimate (no GPU)."""
+import math
+import random
+
+import pytest
+
+import kronecker_factored_gptq_amd as bk
+
+
+def sizes(seed, count):
+    """Outputs M x N and steps of products of every size, spread over their logarithm."""
+    r = random.Random(seed)
+    any_of = lambda hi: int(math.exp(r.uniform(0, math.log(hi))))
+    return [(any_of(130000), any_of(8192), any_of(2100)) for _ in range(count)]
+
+
+@pytest.mark.parametrize("pairs,kmajor", [(1, False), (1, True), (3, True), (6, True), (6, False)])
+def test_plan_is_the_least_of_its_estimate(pairs, kmajor):
+    for M, N, steps in sizes(pairs, 250) + [(16384, 20, 128), (2048, 20, 128), (64, 1, 2004), (1, 1, 1), (1, 1, 0)]:
+        tile, splits, us = bk.debug_plan(M, N, steps, pairs, kmajor)
+        if tile == 256:
+            continue
+        for t in (128, 64):
+            n = 1
+            while True:
+                other = bk.debug_plan(M, N, steps, pairs, kmajor, True, t, n)[2]
+                if other == math.inf:
+                    break
+                assert us <= other, (M, N, steps, (tile, splits, us), (t, n, other))
+                n += 1
+        unsplit = bk.debug_plan(M, N, steps, pairs, kmajor, False)
+        assert unsplit[1] == 1 and unsplit[2] >= us
+
+
+def test_hook_refuses_what_no_call_takes():
+    assert bk.debug_plan(100, 100, 40, tile=96, splits=1)[2] == math.inf
+    assert bk.debug_plan(100, 100, 40, tile=64, splits=21)[2] == math.inf  # less than two steps each
+    assert bk.debug_plan(4096, 4096, 4000, tile=128, splits=2)[2] == math.inf  # more than the chip holds
+    assert bk.debug_plan(100, 100, 40, tile=64, splits=0)[2] == math.inf
+    assert bk.debug_plan(0, 100, 40)[2] == math.inf
