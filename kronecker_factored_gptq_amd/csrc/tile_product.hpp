@@ -639,8 +639,11 @@ inline int join_slices(int splits) { return splits < 12 ? 1 : 8; }
 
 // The tile of a product, and the ranges its k is split into. 256 x 256 tiles
 // (one workgroup a CU) need the fewest bytes and are taken where they fill the
-// chip. Below that the choice is by an estimate of the time in us, of 128 x 128
-// tiles (two workgroups a CU) and 64 x 64 tiles (four):
+// chip without more than a quarter of empty rows and columns beyond those of 128 x 128
+// (131072 x 2048 int8, us with 256 and without: 20 columns 61 and 45, 128 71 and 59, 300 143
+// and 132; 256 85 and 86; float32 input gradient 1 x 1024 x 65536 108 and 96, the cross
+// entropy's of 1 x 512 x 128256 521 and 457). Otherwise the choice is by an estimate of the
+// time in us, of 128 x 128 tiles (two workgroups a CU) and 64 x 64 tiles (four):
 // - with c workgroups on each CU a step takes step + share c (bound by the L2), and
 //   at least `alone` (bound by latency); k-major operands 0.15 more of the
 //   small tile; filling the ring and the epilogue take `fill`;
@@ -698,7 +701,8 @@ inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, int pairs, bool 
                            bool may_split) {
   TilePlan best = {128, 1};
   if (M <= 0 || N <= 0) return best;
-  if (tiles_of(M, N, 256) >= 192) return {256, 1};
+  const int64_t large = tiles_of(M, N, 256);
+  if (large >= 192 && 32 * large <= 10 * tiles_of(M, N, 128)) return {256, 1};
   steps *= pairs;
   double least = 1e300;
   for (int tile : {128, 64})

@@ -33,6 +33,17 @@ def test_plan_is_the_least_of_its_estimate(pairs, kmajor):
         assert unsplit[1] == 1 and unsplit[2] >= us
 
 
+@pytest.mark.parametrize("pairs", [1, 3, 6])
+def test_large_tiles_are_not_mostly_empty(pairs):
+    """256 x 256 tiles multiply at most a quarter more than 128 x 128 ones, and are taken where
+    they fill the chip so."""
+    up = lambda x, t: -(-x // t) * t
+    for M, N, steps in sizes(7, 400) + [(128256, n, 8) for n in (1, 64, 65, 100, 128, 129, 256, 300, 1000)] + [(20, 131072, 9)]:
+        tile = bk.debug_plan(M, N, steps, pairs, True)[0]
+        large, small = up(M, 256) * up(N, 256), up(M, 128) * up(N, 128)
+        assert (tile == 256) == (large >= 192 * 65536 and large <= 1.25 * small), (M, N, steps)
+
+
 def test_hook_refuses_what_no_call_takes():
     assert bk.debug_plan(100, 100, 40, tile=96, splits=1)[2] == math.inf
     assert bk.debug_plan(100, 100, 40, tile=64, splits=21)[2] == math.inf  # less than two steps each
