@@ -422,21 +422,26 @@ static hipError_t start_entropy_diff(const TileOperand& W, const TileOperand& X,
 }
 
 // ---- workspaces -------------------------------------------------------------
-// Rows of W whose planes (float32 operands) are held at once: 512 MiB of them.
-static int64_t plane_piece(int64_t d, int64_t V) {
-  const int64_t per = 3 * plane_ld(d);
-  int64_t p = per ? ((int64_t)512 << 20) / per / 256 * 256 : V;
+// Rows at once of what takes `per` bytes a row, `room` in all.
+static int64_t rows_in(int64_t room, int64_t per, int64_t V) {
+  int64_t p = per ? room / per / 256 * 256 : V;
   if (p < 256) p = 256;
   return p < V ? p : V;
 }
-// Columns of D held at once: 256 MiB, what the last-level cache holds.
-static int64_t diff_piece(int es, int64_t T, int64_t d, int64_t V) {
+// Rows of a float32 W whose planes are held at once: 512 MiB of them.
+static int64_t plane_piece(int64_t d, int64_t V) {
+  return rows_in((int64_t)512 << 20, 3 * plane_ld(d), V);
+}
+// Columns of D held at once: 256 MiB, what the last-level cache holds. `direct`: W is read as
+// it is. A 16-bit W that is laid out shares them with D, so that misaligned operands need
+// little more than aligned ones (of 4096 tokens, d 4096, 128256 words 384 MiB, not 672, and of one
+// token 256, not 1002; misaligned 10.77 ms against 10.61 and 1.40 against 1.38).
+static int64_t diff_piece(int es, int64_t T, int64_t d, int64_t V, bool direct) {
   const int64_t per = 2 * T * (es == 4 ? 3 : 1);
-  int64_t p = per ? ((int64_t)256 << 20) / per / 256 * 256 : V;
-  if (p < 256) p = 256;
+  int64_t p = rows_in((int64_t)256 << 20, per + (es == 4 || direct ? 0 : plane_ld(d)), V);
   if (p > ((int64_t)1 << 20)) p = (int64_t)1 << 20;  // rows the direct loads can step over
   if (es == 4 && p > plane_piece(d, V)) p = plane_piece(d, V);
-  return p < V ? p : V;
+  return p;
 }
 
 // The most tokens the forward's skinny kernel takes.
@@ -446,17 +451,31 @@ constexpr int64_t kSkinnyTokens = 64;
 struct EntropyLayout {
   size_t parts, zy, xp, wp, total;
 };
+// Of the forward: parts of a launch over `rows` of W, two waves of rows in each tile.
+static int64_t entropy_parts(int64_t rows, int64_t tile) { return 2 * ((rows + tile - 1) / tile); }
+static int entropy_tile(int es, int64_t rows, int64_t T, int64_t d) {
+  const int64_t kbytes = es == 4 ? (d + 7) / 8 * 16 : d * es;
+  return plan_tiles(rows, T, (kbytes + kStepBytes - 1) / kStepBytes, es == 4 ? 6 : 1, false, false)
+      .tile;
+}
 static EntropyLayout entropy_layout(int es, int64_t T, int64_t d, int64_t V) {
   EntropyLayout L;
   L.parts = 0;
-  // two waves of rows in each tile, of at least 64 rows; or every 16 rows
-  const bool skinny = T <= kSkinnyTokens;
-  const int64_t nparts = skinny ? (V + 15) / 16 : 2 * ((V + 63) / 64);
+  const bool skinny = T <= kSkinnyTokens, planes = es == 4 && !skinny;
+  const int64_t piece = planes ? plane_piece(d, V) : V;
+  int64_t nparts = (V + 15) / 16;  // every 16 rows
+  if (!skinny) {
+    const int64_t whole = V / piece, rest = V % piece;
+    nparts = whole * entropy_parts(piece, entropy_tile(es, piece, T, d)) +
+             (rest ? entropy_parts(rest, entropy_tile(es, rest, T, d)) : 0);
+    // 16-bit operands that the direct loads cannot take go through tiles of 128
+    const int64_t any = entropy_parts(V, 128);
+    if (!planes && any > nparts) nparts = any;
+  }
   L.zy = L.parts + up256((size_t)(nparts * T) * sizeof(MaxSum));
   L.xp = L.zy + up256((size_t)T * 4);
-  const bool planes = es == 4 && !skinny;
   L.wp = L.xp + (planes ? (size_t)(3 * T * plane_ld(d)) : 0);
-  L.total = L.wp + (planes ? (size_t)(3 * plane_piece(d, V) * plane_ld(d)) : 0);
+  L.total = L.wp + (planes ? (size_t)(3 * piece * plane_ld(d)) : 0);
   return L;
 }
 size_t entropy_bytes(int es, int64_t T, int64_t d, int64_t V) {
@@ -467,19 +486,20 @@ struct GradLayout {
   size_t w, rel, reach, top, xp, xs, wp, p, acc, parts, total;
   int64_t piece, ldacc;
 };
-static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
+// direct: X and W are read as they are, and no planes of them are held.
+static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V, bool direct) {
   GradLayout L;
   const int64_t np = es == 4 ? 3 : 1;
-  L.piece = diff_piece(es, T, d, V);
+  L.piece = diff_piece(es, T, d, V, direct);
   L.ldacc = (d + 3) / 4 * 4;
   L.w = 0;
   L.rel = L.w + up256((size_t)T * 4);
   L.reach = L.rel + up256((size_t)T * 4);
   L.top = L.reach + (es == 2 ? up256((size_t)T * 4) : 0);
   L.xp = L.top + 256;
-  L.xs = L.xp + up256((size_t)(np * T * plane_ld(d)));
+  L.xs = L.xp + (direct ? 0 : up256((size_t)(np * T * plane_ld(d))));
   L.wp = L.xs + up256((size_t)(np * T * plane_ld(d)));
-  L.p = L.wp + up256((size_t)(np * L.piece * plane_ld(d)));
+  L.p = L.wp + (direct ? 0 : up256((size_t)(np * L.piece * plane_ld(d))));
   L.acc = L.p + up256((size_t)(np * T * plane_ld(L.piece)));
   L.parts = L.acc + (L.piece < V ? up256((size_t)(T * L.ldacc) * 4) : 0);
   // both products, of whole pieces and of the last one
@@ -492,7 +512,10 @@ static GradLayout grad_layout(int es, int64_t T, int64_t d, int64_t V) {
   return L;
 }
 size_t entropy_grad_bytes(int es, int64_t T, int64_t d, int64_t V) {
-  return grad_layout(es, T, d, V).total;
+  // a query knows the sizes alone: 16-bit rows may be aligned or not
+  const size_t laid = grad_layout(es, T, d, V, false).total;
+  const size_t direct = es == 2 && d % 8 == 0 ? grad_layout(es, T, d, V, true).total : 0;
+  return direct > laid ? direct : laid;
 }
 
 // ---- calls --------------------------------------------------------------------
@@ -540,8 +563,7 @@ hipError_t launch_entropy(int64_t T, int64_t d, int64_t V, const X* x, int64_t l
         return e;
       wo = {p.w, p.ld, p.plane, rows, 0};
     }
-    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes;
-    const int tile = plan_tiles(rows, T, steps, pairs.n, false, false).tile;
+    const int tile = entropy_tile(sizeof(X), rows, T, d);
     if (!tile_direct(wo, kbytes) || !tile_direct(xo, kbytes))
       e = start_entropy<M, 128, 128, 2, 2, true>(wo, xo, kbytes, pairs, y, v0, parts, nparts, zy, s);
     else if (tile == 256)
@@ -570,7 +592,14 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
                                                       lddw, nullptr, s)
               : hipSuccess;
   }
-  const GradLayout L = grad_layout(sizeof(X), T, d, V);
+  // Both operands as they are, where the direct loads can take them (along d for
+  // the logits, W also k-major for dX); else as planes.
+  constexpr int64_t es = sizeof(X);
+  const int64_t kbytes = (d + 7) / 8 * 16;
+  TileOperand xo = {(const char*)x, ldx * es, 0, T, 0};
+  const bool direct = es == 2 && d % 8 == 0 && tile_direct(xo, kbytes) &&
+                      tile_direct({(const char*)w, ldw * es, 0, V, 0}, kbytes);
+  const GradLayout L = grad_layout(es, T, d, V, direct);
   char* b = (char*)ws;
   float *wt = (float*)(b + L.w), *rel = (float*)(b + L.rel), *top = (float*)(b + L.top);
   float *acc = (float*)(b + L.acc), *parts = (float*)(b + L.parts);
@@ -586,13 +615,6 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
   hipLaunchKernelGGL(entropy_weights_kernel, dim3(1), dim3(1024), 0, s, T, V, y, g, reach, wt, rel,
                      top);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  // Both operands as they are, where the direct loads can take them (along d for
-  // the logits, W also k-major for dX); else as planes.
-  constexpr int64_t es = sizeof(X);
-  const int64_t kbytes = (d + 7) / 8 * 16;
-  TileOperand xo = {(const char*)x, ldx * es, 0, T, 0};
-  const bool direct = es == 2 && d % 8 == 0 && tile_direct(xo, kbytes) &&
-                      tile_direct({(const char*)w, ldw * es, 0, V, 0}, kbytes);
   if (!direct) {
     const Planes p = {b + L.xp, plane_ld(d), T * plane_ld(d)};
     if ((e = launch_planes<X, K::split>(T, d, x, ldx, nullptr, nullptr, p, s)) != hipSuccess)
@@ -613,8 +635,7 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
     }
     const TileOperand wo = {wp.w, wp.ld, wp.plane, rows, 0};
     const Planes P = {b + L.p, plane_ld(rows), T * plane_ld(rows)};
-    const int64_t steps = (kbytes + kStepBytes - 1) / kStepBytes;
-    const int tile = plan_tiles(rows, T, steps, pairs.n, false, false).tile;
+    const int tile = entropy_tile(sizeof(X), rows, T, d);
     if (tile == 256)
       e = start_entropy_diff<M, K::split, 256, 256, 2, 4>(wo, xo, kbytes, pairs, y, V, v0, lse,
                                                           dscale<X>(), P, s);

@@ -100,3 +100,16 @@ def test_binding_checks(monkeypatch):
                 lambda: bk.cross_entropy_grad(X, W, y, f[:2], f), lambda: bk.cross_entropy_grad(X, W, y, f, f[:2])):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_gradient_workspaces_of_few_tokens():
+    """Pieces of W, 256 MiB with D's, not W: one bfloat16 token of 4096 on 128256 words (1002 MiB
+    of output layer), and three of 2048 on 1.1 million (4.2 GiB); and the planes of operands that are
+    read as they are take no room beside D's 256 MiB."""
+    q = bk.lib().bakron_cross_entropy_grad_workspace_bytes
+    for t in (bk.BF16, bk.F16):
+        assert q(t, 1, 4096, 128256) < 264 << 20 and q(t, 3, 2048, 1100000) < 264 << 20
+        assert q(t, 4096, 4096, 128256) < 400 << 20
+    # the forward's maxima and sums: 8 bytes a token for every 64 words at most of these sizes
+    f = bk.lib().bakron_cross_entropy_workspace_bytes
+    assert f(bk.BF16, 4096, 4096, 128256) <= 4096 * 8 * (128256 // 64 + 2)
