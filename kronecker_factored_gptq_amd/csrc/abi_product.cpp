@@ -241,7 +241,7 @@ double bakron_debug_plan(int64_t M, int64_t N, int64_t steps, int pairs, int kma
   }
   if (*tile == 256) return 0;
   if ((*tile != 128 && *tile != 64) || *splits < 1 ||
-      !plan_allowed(M, N, steps * pairs, may_split, *tile, *splits))
+      !plan_allowed(M, N, steps * pairs, pairs, may_split, *tile, *splits))
     return __builtin_inf();
   return plan_us(M, N, steps * pairs, pairs, kmajor, *tile, *splits);
 }

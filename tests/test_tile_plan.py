@@ -22,13 +22,11 @@ def test_plan_is_the_least_of_its_estimate(pairs, kmajor):
         if tile == 256:
             continue
         for t in (128, 64):
-            n = 1
-            while True:
+            for n in range(1, 1025):
                 other = bk.debug_plan(M, N, steps, pairs, kmajor, True, t, n)[2]
-                if other == math.inf:
-                    break
+                if other == math.inf and n % 3 == 0:
+                    break  # too many, and so is any more
                 assert us <= other, (M, N, steps, (tile, splits, us), (t, n, other))
-                n += 1
         unsplit = bk.debug_plan(M, N, steps, pairs, kmajor, False)
         assert unsplit[1] == 1 and unsplit[2] >= us
 
@@ -50,3 +48,6 @@ def test_hook_refuses_what_no_call_takes():
     assert bk.debug_plan(4096, 4096, 4000, tile=128, splits=2)[2] == math.inf  # more than the chip holds
     assert bk.debug_plan(100, 100, 40, tile=64, splits=0)[2] == math.inf
     assert bk.debug_plan(0, 100, 40)[2] == math.inf
+    # several pairs of planes: ranges that meet the same k
+    assert bk.debug_plan(100, 100, 40, 3, tile=64, splits=4)[2] == math.inf
+    assert bk.debug_plan(100, 100, 40, 3, tile=64, splits=6)[2] < math.inf
