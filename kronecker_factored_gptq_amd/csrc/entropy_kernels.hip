@@ -15,11 +15,11 @@
 // float32 operands are three bfloat16 planes each (exact), and a product the six
 // pairs of planes whose terms reach float32's precision.
 //
-// 4096 tokens, d = 4096, 128256 words, bfloat16: forward 3.1 to 3.25 ms (1.33 to 1.38
+// 4096 tokens, d = 4096, 128256 words, bfloat16: forward 3.15 to 3.25 ms (1.32 to 1.37
 // PFLOP/s in 256 x 256 tiles; a tile's epilogue, 65536 exponentials, takes its share
-// of what is missing to a plain product), gradient 10.0 to 10.4 ms (1.25 to 1.29): D
-// 0.89 ms a piece, D W 0.77, D^T X 0.89. One token, d = 2048, 50257 words, float16:
-// 45 us (4.5 TB/s). 333 x 1000 x 10007 float32, gradient: 212 us, of them 16 for W's
+// of what is missing to a plain product), gradient 10.1 to 10.7 ms (1.21 to 1.28): D
+// 0.91 ms a piece, D W 0.78, D^T X 0.90. One token, d = 2048, 50257 words, float16:
+// 45 us (4.5 TB/s). 333 x 1000 x 10007 float32, gradient: 211 to 220 us, of them 16 for W's
 // planes and 183 for six plane products in each of the three products.
 #include <initializer_list>
 

@@ -228,7 +228,7 @@ hipError_t launch_plane_product(int64_t M, int64_t N, int64_t K, Planes R, Plane
 // 2^-28 of the largest keep. (One bfloat16 plane would keep 8 bits, as coarse as
 // a bfloat16 output, at the same cost; more bits cost a second product.) A
 // float32 G is three bfloat16 planes, all 24 bits.
-// 8192 x 4096 x 14336 bfloat16: 762 to 800 us, of them 56 for the two operands (bound
+// 8192 x 4096 x 14336 bfloat16: 775 to 815 us, of them 56 to 60 for the two operands (bound
 // by memory); 512 x 1024 x 2048 float32: 26 us in three kernels.
 // ---------------------------------------------------------------------------
 // The codes as one plane, m x n: the part of both operands' launch that both
