@@ -40,3 +40,33 @@ def test_tokens_of_little_weight_in_float16(gpu_lib, ratio, size):
     assert not over[:, 1:].any()
     err = torch.where(over, 0.0, (dW.double() - want).abs())
     assert (want[:, 1:].abs().amax() >= 2.0 ** -6) and (err <= tol).all(), (err / tol).max()
+
+
+def test_captured_with_weights_that_change(gpu_lib):
+    """The float16 gradient in a HIP graph: the power of two comes from each replay's own tokens."""
+    bk = gpu_lib
+    gen = torch.Generator(device="cuda").manual_seed(8)
+
+    def inputs():
+        X = torch.randn(90, 136, device="cuda", generator=gen) * 2.0 ** torch.randint(-6, 6, (90, 1), device="cuda", generator=gen)
+        W = torch.randn(500, 136, device="cuda", generator=gen) * 0.05
+        y = torch.randint(0, 500, (90,), device="cuda", generator=gen)
+        y[::7] = -100
+        g = torch.randn(90, device="cuda", generator=gen) * 2.0 ** torch.randint(-20, 6, (90,), device="cuda", generator=gen)
+        X, W = X.half(), W.half()
+        return X, W, y, bk.cross_entropy(X, W, y)[1], g
+
+    static = inputs()
+    bk.cross_entropy_grad(*static)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = bk.cross_entropy_grad(*static)
+    for _ in range(4):
+        new = inputs()
+        for t, v in zip(static, new):
+            t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(got, bk.cross_entropy_grad(*new)):
+            assert torch.equal(u, v)
