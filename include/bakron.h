@@ -36,7 +36,7 @@
  *    call: BAKRON_F32 (float) or BAKRON_F64 (double). Codes are int32. (The
  *    calls from bakron_quantize_tokens on name their types themselves.)
  *  - m = 0 or n = 0 is accepted and does nothing; an empty sum is zero (the
- *    8-bit product with n = 0 gives Y = 0, its gradient with m = 0 dX = 0).
+ *    8-bit products with n = 0 give Y = 0, their gradients with m = 0 dX = 0).
  */
 #ifndef BAKRON_H_
 #define BAKRON_H_
@@ -57,8 +57,8 @@ extern "C" {
 #define BAKRON_EWAIT (-4)   /* a solve's bounded wait inside a leaf block gave up
                                (bakron_solve_status): its outputs are invalid */
 
-/* Element types. The calls of the solve take F32 and F64; the 8-bit product
- * and the cross entropy take F32, BF16 and F16. */
+/* Element types. The calls of the solve take F32 and F64; those from
+ * bakron_quantize_tokens on take F32, BF16 and F16. */
 #define BAKRON_F32 0
 #define BAKRON_F64 1
 #define BAKRON_BF16 2
@@ -561,6 +561,130 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
                               const int64_t *targets, const float *lse, const float *g,
                               void *dX, int64_t lddx, void *dW, int64_t lddw,
                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point: matrices as e4m3 codes (one sign, four exponent, three
+ * fraction bits; largest 448, smallest 2^-9; no infinity, NaN 0x7f and 0xff) with a
+ * float32 scale for each block, and products of them. The common format of weights and
+ * tokens that the solve's codes are measured against.
+ *
+ * bakron_quantize_fp8: `batch` matrices of rows x n in blocks of block_rows x 128,
+ * block_rows 1 (tokens) or 128 (weights); the last blocks of a row or column are
+ * shorter. With a the largest |x| of a block,
+ *   s    = a / 448, at least 2^-126; 1 for a block of zeros,
+ *   code = x / s to the nearest code, ties to even,
+ * in float32, both divisions correctly rounded. A block that holds an infinity or a NaN
+ * gets a scale that is not finite and codes whose products with it are NaN.
+ *   xtype  BAKRON_F32, BAKRON_BF16 or BAKRON_F16.
+ *   X      row r of matrix z at X + z * stride_x + r * ldx; Xq out, likewise (columns
+ *          past n are not written).
+ *   s      out: block (a, b) of matrix z at s[z * stride_s + a * s_row + b * s_block].
+ *          For tokens s_row = 1, s_block = rows are read fastest by the product.
+ *
+ * bakron_matmul_fp8: row r of Y is a token times the weights of the row's group,
+ *   Y[r][i] = sum_b sx[t][b] * sw[i / 128][b] * sum_{j in block b} Xq[t][j] * Wq[i][j],
+ * T tokens (Xq T x n, ldx; sx[t][b] at sx[t * sx_token + b * sx_block]) and `experts`
+ * layers (Wq[e] m x n at Wq + e * stride_w, ldw; sw[e] at sw + e * stride_sw, a row of
+ * ceil(n / 128) scales, ldsw apart, for each 128 rows).
+ *   offsets  int32, length experts + 1, or NULL (one layer for all rows). Group e is rows
+ *            [offsets[e], offsets[e + 1]) of the R rows of Y (offsets are held inside [0, R], and
+ *            one below an earlier one counts as it); rows in no group are left as they were.
+ *   order    int32, length R, or NULL (t = r; T = R). t = order[r] / per_token, the
+ *            order of bakron_sort_tokens, so that no sorted copy of the tokens is needed. A
+ *            row whose order names no token (below 0, or its t not below T) becomes 0.
+ *   ytype    the type of Y (R x m, ldy >= m): F32, BF16 or F16.
+ * For BF16 and F16 the products of a block are added by the 8-bit instructions, which cut
+ * each of eight neighbouring products below 2^-13 of the largest of the eight before they
+ * add them: 7 * 2^-13 of sum_j |Xq Wq| at most, 1.5e-5 of the result for Gaussian codes,
+ * nothing where the codes' exponents differ by at most 3 in either operand. For F32 products
+ * are exact and added in float32. Blocks are scaled and added in float32 in either case,
+ * and Y is rounded once.
+ *
+ * bakron_matmul_fp8_grad: the input gradient, the tokens' rounding passed straight through,
+ *   dX[r][j] = sum_i G[r][i] * sw[i / 128][j / 128] * Wq[i][j],
+ * rows in groups as above (rows in no group are left as they were). G (R x m, ldg) and dX
+ * (R x n, ldx) are of gtype: F32, BF16 or F16. For BF16 and F16 G is taken at 11 bits
+ * (down to 2^-28 of the row's largest, and to 2^-39 of it below), all that they
+ * have; F32 keeps its 24. Products are exact, sums float32, one rounding to gtype. The codes
+ * are what the layer holds: there is no gradient with respect to them.
+ *
+ * Outputs must not overlap the inputs (BAKRON_EINVAL; arrays are compared from their first
+ * element to their last). Rows that start at multiples of 16 bytes with n (and, for
+ * the gradient, m) a multiple of 16 are read fastest; any alignment and stride works. 1 <=
+ * experts <= 1024; T, R < 2^24; m, n <= 2^20; around 2^36 elements of Xq and Wq, 2^35 of the
+ * gradient's operands and 2^36 of Y and beyond, more than one launch holds, are
+ * BAKRON_EINVAL. Asynchronous, deterministic.
+ * ------------------------------------------------------------------------ */
+int bakron_quantize_fp8(int xtype, int64_t batch, int64_t rows, int64_t n,
+                        const void *X, int64_t ldx, int64_t stride_x, int block_rows,
+                        uint8_t *Xq, int64_t ldq, int64_t stride_q,
+                        float *s, int64_t s_row, int64_t s_block, int64_t stride_s, void *stream);
+size_t bakron_matmul_fp8_workspace_bytes(int ytype, int64_t T, int64_t R, int64_t experts,
+                                         int64_t m, int64_t n);
+int bakron_matmul_fp8(int ytype, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n,
+                      const uint8_t *Xq, int64_t ldx,
+                      const float *sx, int64_t sx_token, int64_t sx_block,
+                      const uint8_t *Wq, int64_t ldw, int64_t stride_w,
+                      const float *sw, int64_t ldsw, int64_t stride_sw,
+                      const int32_t *offsets, const int32_t *order, int64_t per_token,
+                      void *Y, int64_t ldy,
+                      void *workspace, size_t workspace_bytes, void *stream);
+size_t bakron_matmul_fp8_grad_workspace_bytes(int gtype, int64_t R, int64_t experts, int64_t m,
+                                              int64_t n);
+int bakron_matmul_fp8_grad(int gtype, int64_t R, int64_t experts, int64_t m, int64_t n,
+                           const void *G, int64_t ldg,
+                           const uint8_t *Wq, int64_t ldw, int64_t stride_w,
+                           const float *sw, int64_t ldsw, int64_t stride_sw,
+                           const int32_t *offsets, void *dX, int64_t ldx,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The tokens of a layer of experts, each token routed to k of them. Route p = t k + j is
+ * choice j of token t.
+ *
+ * bakron_sort_tokens: the routes in the order of their experts, those of one expert in
+ * the order of p.
+ *   ids      int64, T x k (ld >= k): the experts; one outside [0, experts) (-1 by custom)
+ *            marks a dropped route.
+ *   order    out, int32, length T k: the routes in their order, -1 past offsets[experts].
+ *   slots    out, int32, length T k: the place of route p in `order`, -1 if it is dropped.
+ *   offsets  out, int32, length experts + 1: expert e's routes are
+ *            order[offsets[e]] .. order[offsets[e + 1] - 1].
+ * T k < 2^31 - 4096; experts <= 1024. workspace may be NULL where the query gives 0.
+ *
+ * bakron_gather_tokens: Xs[s] = X[order[s] / per_token] (R x n from T x n), zeros where
+ * order[s] is below 0 or names no token: the samples of each expert side by side, for
+ * bakron_gram for instance. Its gradient is bakron_combine_tokens without weights.
+ *
+ * bakron_combine_tokens: Y[t] = sum_j weights[t][j] * Ys[slots[t][j]] (T x n from R x n),
+ * in float32 in the order of j, rounded once. Slots outside [0, R) take no part; weights
+ * (float32, T x k) may be NULL (all 1).
+ *
+ * bakron_combine_tokens_grad: with G (T x n) the gradient of Y,
+ *   dYs[slots[t][j]] = weights[t][j] * G[t]              (R x n; nullable),
+ *   dweights[t][j]   = sum_c G[t][c] * Ys[slots[t][j]][c] (float32, T x k; nullable; 0 for
+ *                      a slot outside [0, R)).
+ * Rows of dYs that no slot names are left as they were; a slot may be named once. Ys is read
+ * for dweights alone, and may be NULL without them.
+ *
+ * Element types F32, BF16 and F16. Outputs must not overlap the inputs or each other
+ * (BAKRON_EINVAL). T < 2^24 for the last two, R <= 2^26 for the gather; more columns or choices than one
+ * launch holds (T n around 2^35, T k around 2^26) are BAKRON_EINVAL. Asynchronous, deterministic.
+ * ------------------------------------------------------------------------ */
+size_t bakron_sort_tokens_workspace_bytes(int64_t T, int64_t k, int64_t experts);
+int bakron_sort_tokens(int64_t T, int64_t k, int64_t experts, const int64_t *ids, int64_t ld,
+                       int32_t *order, int32_t *slots, int32_t *offsets,
+                       void *workspace, size_t workspace_bytes, void *stream);
+int bakron_gather_tokens(int xtype, int64_t T, int64_t n, const void *X, int64_t ldx,
+                         int64_t per_token, int64_t R, const int32_t *order,
+                         void *Xs, int64_t ldxs, void *stream);
+int bakron_combine_tokens(int ytype, int64_t T, int64_t k, int64_t n, int64_t R,
+                          const void *Ys, int64_t ldys, const int32_t *slots, const float *weights,
+                          void *Y, int64_t ldy, void *stream);
+int bakron_combine_tokens_grad(int ytype, int64_t T, int64_t k, int64_t n, int64_t R,
+                               const void *G, int64_t ldg, const void *Ys, int64_t ldys,
+                               const int32_t *slots, const float *weights,
+                               void *dYs, int64_t lddys, float *dweights, void *stream);
 
 /* Test hook: how a tiled product of M x N outputs over `steps` steps (128 bytes
  * of k) of each of `pairs` pairs of planes is divided. With *tile = 0: sets *tile and

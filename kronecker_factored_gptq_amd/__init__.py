@@ -22,7 +22,9 @@ __all__ = ["F32", "F64", "BF16", "F16", "SCALE_NONE", "SCALE_ROW", "SCALE_COL", 
            "solve", "solve_antidiag", "solve_noalloc", "factor_blockdiag", "solve_blockdiag",
            "loss_blockdiag", "solve_batched", "loss", "loss_batched", "row_scales", "row_scales_mse", "gram",
            "sample_sqnorms", "kfac_factors", "shampoo_factors", "quantize_tokens", "matmul_int8",
-           "matmul_int8_grad", "cross_entropy", "cross_entropy_grad", "solve_schedule", "tile_size", "workspace_bytes"]
+           "matmul_int8_grad", "cross_entropy", "cross_entropy_grad", "quantize_fp8", "matmul_fp8", "matmul_fp8_grad",
+           "sort_tokens", "gather_tokens", "combine_tokens", "combine_tokens_grad", "solve_schedule", "tile_size",
+           "workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libbakron.so")
@@ -156,6 +158,30 @@ def lib() -> ctypes.CDLL:
     L.bakron_cross_entropy_grad.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
                                             _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
     L.bakron_cross_entropy_grad.restype = _int
+    L.bakron_quantize_fp8.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _i64, _int, _vp, _i64, _i64, _vp, _i64,
+                                      _i64, _i64, _vp]
+    L.bakron_quantize_fp8.restype = _int
+    L.bakron_matmul_fp8_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _i64, _i64]
+    L.bakron_matmul_fp8_workspace_bytes.restype = _sz
+    L.bakron_matmul_fp8.argtypes = [_int, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
+                                    _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
+    L.bakron_matmul_fp8.restype = _int
+    L.bakron_matmul_fp8_grad_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _i64]
+    L.bakron_matmul_fp8_grad_workspace_bytes.restype = _sz
+    L.bakron_matmul_fp8_grad.argtypes = [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
+                                         _vp, _vp, _i64, _vp, _sz, _vp]
+    L.bakron_matmul_fp8_grad.restype = _int
+    L.bakron_sort_tokens_workspace_bytes.argtypes = [_i64, _i64, _i64]
+    L.bakron_sort_tokens_workspace_bytes.restype = _sz
+    L.bakron_sort_tokens.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
+    L.bakron_sort_tokens.restype = _int
+    L.bakron_gather_tokens.argtypes = [_int, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp]
+    L.bakron_gather_tokens.restype = _int
+    L.bakron_combine_tokens.argtypes = [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]
+    L.bakron_combine_tokens.restype = _int
+    L.bakron_combine_tokens_grad.argtypes = [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                                             _vp, _vp]
+    L.bakron_combine_tokens_grad.restype = _int
     L.bakron_debug_plan.argtypes = [_i64, _i64, _i64, _int, _int, _int, _vp, _vp]
     L.bakron_debug_plan.restype = ctypes.c_double
     _lib = L
@@ -970,6 +996,234 @@ def cross_entropy_grad(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, 
           None if dX is None else dX.data_ptr(), max(d, 1), None if dW is None else dW.data_ptr(),
           max(d, 1), pw, nw)
     return dX, dW
+
+
+E4M3 = torch.float8_e4m3fn
+_BLOCK = 128
+
+
+def quantize_fp8(X: torch.Tensor, block_rows: int = 1):
+    """X as 8-bit floating point with a float32 scale for each block of block_rows x
+    128 (bakron_quantize_fp8): 1 for tokens, 128 for weights. X is rows x n, or a
+    batch of them (experts x rows x n), in float32, bfloat16 or float16. With a the
+    largest |x| of a block its scale is s = a / 448 (at least 2^-126; 1 for zeros) and its
+    codes x / s to the nearest. Returns the codes (torch.float8_e4m3fn, of X's shape,
+    rows starting at multiples of 16 bytes) and the scales (... x ceil(rows /
+    block_rows) x ceil(n / 128); for block_rows = 1 a block's scales of all rows lie side by
+    side). Asynchronous."""
+    dev = _check_device(X)
+    code = _ft(X.dtype, "X")
+    if block_rows not in (1, _BLOCK):
+        raise ValueError(f"block_rows must be 1 or {_BLOCK}, got {block_rows}")
+    batch, rows, n, ldx, sX = _matrices(X, "X")
+    ldq, nb, na = (n + 15) // 16 * 16, -(-n // _BLOCK), -(-rows // block_rows)
+    lead = X.shape[:-2]
+    Xq = torch.empty((*lead, rows, ldq), dtype=E4M3, device=dev)
+    if ldq != n:
+        Xq = Xq[..., :n]
+    if block_rows == 1:
+        s = torch.empty((*lead, nb, na), dtype=torch.float32, device=dev).transpose(-1, -2)
+        srow, sblock = 1, na
+    else:
+        s = torch.empty((*lead, na, nb), dtype=torch.float32, device=dev)
+        srow, sblock = nb, 1
+    _call("bakron_quantize_fp8", dev, lib().bakron_quantize_fp8, code, batch, rows, n, X.data_ptr(), ldx, sX,
+          block_rows, Xq.data_ptr(), ldq, rows * ldq, s.data_ptr(), srow, sblock, na * nb)
+    return Xq, s
+
+
+def _matrices(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None):
+    """(batch, rows, columns, leading dimension, stride) of a row-major matrix, or of a
+    batch of them (3-D) any distance apart."""
+    if t.dim() != 3:
+        rows, cols, ld = _matrix(t, name, dtype)
+        return 1, rows, cols, ld, 0
+    if t.size(0) == 0:
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        return 0, t.size(1), t.size(2), max(t.size(2), 1), 0
+    rows, cols, ld = _matrix(t[0], name, dtype)
+    return t.size(0), rows, cols, ld, t.stride(0) if t.size(0) > 1 else 0
+
+
+def _fp8_weights(Wq: torch.Tensor, sw: torch.Tensor, offsets: Optional[torch.Tensor]):
+    """(experts, m, n, Wq, ldw, stride, sw, ldsw, stride, offsets): a layer's codes
+    and scales, or those of each expert with the offsets of their rows."""
+    experts, m, n, ldw, stride = _matrices(Wq, "Wq", E4M3)
+    if (Wq.dim() == 3) != (offsets is not None):
+        raise ValueError("Wq is experts x m x n with offsets, and m x n without")
+    if experts < 1:
+        raise ValueError("Wq must have an expert")
+    want = (*Wq.shape[:-2], -(-m // _BLOCK), -(-n // _BLOCK))
+    if sw.shape != want:
+        raise ValueError(f"sw must have shape {want}, got {tuple(sw.shape)}")
+    _, _, _, ldsw, stride_s = _matrices(sw, "sw", torch.float32)
+    return (experts, m, n, Wq.data_ptr(), ldw, stride, sw.data_ptr(), ldsw, stride_s,
+            _vector(offsets, experts + 1, "offsets", torch.int32))
+
+
+def matmul_fp8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor,
+               offsets: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None, per_token: int = 1,
+               out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Tokens times weights, both as ``quantize_fp8`` gives them (bakron_matmul_fp8):
+    Y[r][i] = sum_b sx[t][b] sw[i // 128][b] sum_{j in block b} Xq[t][j] Wq[i][j].
+
+    Xq is T x n and sx T x ceil(n / 128), with any strides; Wq m x n with sw
+    ceil(m / 128) x ceil(n / 128). For a layer of experts Wq is experts x m x n, sw likewise,
+    and ``offsets`` (int32, experts + 1) says which rows of Y are whose: rows
+    [offsets[e], offsets[e + 1]) are multiplied by expert e, rows past the last are not
+    written. Row r is token r, or with ``order`` (int32; ``sort_tokens`` makes it and the
+    offsets) token order[r] // per_token, so that the tokens need not be copied into
+    order; Y then has a row for each of ``order``. Y is rows x m in ``out_dtype`` (float32,
+    bfloat16 or float16), or ``out`` and its type. Asynchronous."""
+    dev = _check_device(Xq, sx, Wq, sw, offsets, order, out, workspace)
+    T, n, ldx = _matrix(Xq, "Xq", E4M3)
+    experts, m, nw, pw, ldw, stride, ps, ldsw, stride_s, po = _fp8_weights(Wq, sw, offsets)
+    if nw != n:
+        raise ValueError(f"Xq and Wq must have rows of one length, got {n} and {nw}")
+    if sx.dtype != torch.float32:
+        raise TypeError(f"sx must be torch.float32, got {sx.dtype}")
+    if sx.shape != (T, -(-n // _BLOCK)):
+        raise ValueError(f"sx must have shape {(T, -(-n // _BLOCK))}, got {tuple(sx.shape)}")
+    per_token = int(per_token)
+    if per_token < 1:
+        raise ValueError("per_token must be positive")
+    R, pr = T, None
+    if order is not None:
+        if order.dim() != 1:
+            raise ValueError("order must be a vector")
+        R = order.size(0)
+        pr = _vector(order, R, "order", torch.int32)
+    dtype = out_dtype if out is None else out.dtype
+    code = _ft(dtype, "out_dtype")
+    out, ldy = _output(out, R, m, dtype, "out", dev)
+    L = lib()
+    ws, pws, nws = _scratch(L.bakron_matmul_fp8_workspace_bytes(code, T, R, experts, m, n), dev, workspace)
+    _call("bakron_matmul_fp8", dev, L.bakron_matmul_fp8, code, T, R, experts, m, n, Xq.data_ptr(), ldx,
+          sx.data_ptr(), *sx.stride(), pw, ldw, stride, ps, ldsw, stride_s, po, pr, per_token, out.data_ptr(), ldy,
+          pws, nws)
+    return out
+
+
+def matmul_fp8_grad(G: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The input gradient of ``matmul_fp8`` (bakron_matmul_fp8_grad): dX[r][j] =
+    sum_i G[r][i] sw[i // 128][j // 128] Wq[i][j], with the rounding of the tokens
+    passed straight through. G is rows x m in float32, bfloat16 or float16 and dX, rows x n, of
+    its type. With experts the rows are in their order, as Y's were (``combine_tokens`` adds
+    up those of one token), and rows past the last expert's are not written.
+    Asynchronous."""
+    dev = _check_device(G, Wq, sw, offsets, workspace, out)
+    code = _ft(G.dtype, "G")
+    R, m, ldg = _matrix(G, "G")
+    experts, mw, n, pw, ldw, stride, ps, ldsw, stride_s, po = _fp8_weights(Wq, sw, offsets)
+    if mw != m:
+        raise ValueError(f"G must have a column for each row of Wq, got {m} and {mw}")
+    out, ldx = _output(out, R, n, G.dtype, "out", dev)
+    L = lib()
+    ws, pws, nws = _scratch(L.bakron_matmul_fp8_grad_workspace_bytes(code, R, experts, m, n), dev, workspace)
+    _call("bakron_matmul_fp8_grad", dev, L.bakron_matmul_fp8_grad, code, R, experts, m, n, G.data_ptr(), ldg, pw, ldw,
+          stride, ps, ldsw, stride_s, po, out.data_ptr(), ldx, pws, nws)
+    return out
+
+
+def sort_tokens(experts: torch.Tensor, num_experts: int, workspace: Optional[torch.Tensor] = None):
+    """Routes in the order of their experts (bakron_sort_tokens). ``experts`` (int64,
+    T x k) holds the k experts of each token; one outside [0, num_experts) (-1 by custom)
+    drops that route. Returns int32 ``order`` (T k: the routes t k + j by expert, those of
+    one expert in their own order, -1 past the last), ``slots`` (T x k: each route's place
+    in it, -1 if dropped) and ``offsets`` (num_experts + 1: where each expert's begin).
+    Asynchronous."""
+    dev = _check_device(experts, workspace)
+    T, k, ld = _matrix(experts, "experts", torch.int64)
+    E = int(num_experts)
+    if k < 1 or E < 1:
+        raise ValueError("a token must have an expert")
+    order = torch.empty(T * k, dtype=torch.int32, device=dev)
+    slots = torch.empty((T, k), dtype=torch.int32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    L = lib()
+    ws, pws, nws = _scratch(L.bakron_sort_tokens_workspace_bytes(T, k, E), dev, workspace)
+    _call("bakron_sort_tokens", dev, L.bakron_sort_tokens, T, k, E, experts.data_ptr(), ld, order.data_ptr(),
+          slots.data_ptr(), offsets.data_ptr(), pws, nws)
+    return order, slots, offsets
+
+
+def gather_tokens(X: torch.Tensor, order: torch.Tensor, per_token: int = 1,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Xs[s] = X[order[s] // per_token] (bakron_gather_tokens), zeros where order[s]
+    names no token (-1): the tokens of ``sort_tokens``'s experts side by side, for instance
+    the samples of each for ``gram``. X is float32, bfloat16 or float16. Its gradient is
+    ``combine_tokens(dXs, slots)``. Asynchronous."""
+    dev = _check_device(X, order, out)
+    code = _ft(X.dtype, "X")
+    T, n, ldx = _matrix(X, "X")
+    if order.dim() != 1:
+        raise ValueError("order must be a vector")
+    R, per_token = order.size(0), int(per_token)
+    if per_token < 1:
+        raise ValueError("per_token must be positive")
+    po = _vector(order, R, "order", torch.int32)
+    out, ldo = _output(out, R, n, X.dtype, "out", dev)
+    _call("bakron_gather_tokens", dev, lib().bakron_gather_tokens, code, T, n, X.data_ptr(), ldx, per_token, R, po,
+          out.data_ptr(), ldo)
+    return out
+
+
+def _routes(slots: torch.Tensor, weights: Optional[torch.Tensor]):
+    """(T, k, slots, weights) of contiguous T x k tensors."""
+    if slots.dtype != torch.int32:
+        raise TypeError(f"slots must be torch.int32, got {slots.dtype}")
+    if slots.dim() != 2 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous T x k tensor")
+    if weights is not None:
+        if weights.dtype != torch.float32:
+            raise TypeError(f"weights must be torch.float32, got {weights.dtype}")
+        if weights.shape != slots.shape or not weights.is_contiguous():
+            raise ValueError("weights must be contiguous, of slots' shape")
+    return slots.size(0), slots.size(1), slots.data_ptr(), None if weights is None else weights.data_ptr()
+
+
+def combine_tokens(Ys: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[t] = sum_j weights[t][j] Ys[slots[t][j]] (bakron_combine_tokens): the experts'
+    results back at their tokens. Ys has a row for each of ``sort_tokens``'s order, in
+    float32, bfloat16 or float16, and Y (T x n) its type; slots is its second result (slots
+    outside Ys' rows, -1 by custom, take no part), weights float32 T x k, None for 1. Sums
+    are float32. Asynchronous."""
+    dev = _check_device(Ys, slots, weights, out)
+    code = _ft(Ys.dtype, "Ys")
+    R, n, ldys = _matrix(Ys, "Ys")
+    T, k, ps, pw = _routes(slots, weights)
+    out, ldy = _output(out, T, n, Ys.dtype, "out", dev)
+    _call("bakron_combine_tokens", dev, lib().bakron_combine_tokens, code, T, k, n, R, Ys.data_ptr(), ldys, ps, pw,
+          out.data_ptr(), ldy)
+    return out
+
+
+def combine_tokens_grad(G: torch.Tensor, Ys: torch.Tensor, slots: torch.Tensor,
+                        weights: Optional[torch.Tensor] = None, need_dYs: bool = True, need_dweights: bool = True):
+    """The gradient of ``combine_tokens`` (bakron_combine_tokens_grad): (dYs, dweights)
+    with dYs[slots[t][j]] = weights[t][j] G[t], of Ys' shape and type, and
+    dweights[t][j] = G[t] . Ys[slots[t][j]], float32 T x k (0 for a dropped route); None
+    where not needed. G is T x n of Ys' type. Rows of dYs that no slot names are not
+    written; no slot may be named twice. Asynchronous."""
+    dev = _check_device(G, Ys, slots, weights)
+    code = _ft(Ys.dtype, "Ys")
+    T, n, ldg = _matrix(G, "G", Ys.dtype)
+    R, ny, ldys = _matrix(Ys, "Ys")
+    if ny != n:
+        raise ValueError(f"G and Ys must have rows of one length, got {n} and {ny}")
+    Ts, k, ps, pw = _routes(slots, weights)
+    if Ts != T:
+        raise ValueError(f"G must have a row for each of slots, got {T} and {Ts}")
+    dYs = torch.empty((R, n), dtype=Ys.dtype, device=dev) if need_dYs else None
+    dw = torch.empty((T, k), dtype=torch.float32, device=dev) if need_dweights else None
+    _call("bakron_combine_tokens_grad", dev, lib().bakron_combine_tokens_grad, code, T, k, n, R, G.data_ptr(), ldg,
+          Ys.data_ptr(), ldys, ps, pw, None if dYs is None else dYs.data_ptr(), max(n, 1),
+          None if dw is None else dw.data_ptr())
+    return dYs, dw
 
 
 def debug_set_wait_polls(polls: int) -> int:

@@ -20,7 +20,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libbakron.so")
 
-SOURCES = ["abi.cpp", "abi_product.cpp", "product_kernels.hip", "plane_kernels.hip",
+SOURCES = ["abi.cpp", "abi_product.cpp", "abi_experts.cpp", "product_kernels.hip", "plane_kernels.hip",
+           "fp8_kernels.hip", "expert_kernels.hip",
            "entropy_kernels.hip", "solve_kernels.hip", "band_kernels.hip", "factor_kernels.hip", "gemm64.hip", "loss_kernels.hip",
            "scale_kernels.hip", "gram_kernels.hip", "antidiag_kernels.hip"]
 

@@ -351,4 +351,47 @@ hipError_t launch_entropy_grad(int64_t T, int64_t d, int64_t V, const X* x, int6
                                int64_t ldw, const int64_t* y, const float* lse, const float* g,
                                X* dX, int64_t lddx, X* dW, int64_t lddw, void* ws, hipStream_t s);
 
+// ---- 8-bit floating point with block scales (fp8_kernels.hip) ----------------
+template <typename X>
+hipError_t launch_quantize_fp8(int64_t batch, int64_t rows, int64_t n, const X* x, int64_t ldx,
+                               int64_t sX, int block_rows, uint8_t* q, int64_t ldq, int64_t sQ,
+                               float* s, int64_t srow, int64_t sblock, int64_t sS, hipStream_t st);
+// Y (R x m), its rows in groups with weights of their own where offsets is not null; ws
+// holds matmul_fp8_bytes (es: the element size of Y).
+size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n);
+template <typename O>
+hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n,
+                             const uint8_t* Xq, int64_t ldx, const float* sx, int64_t sx_token,
+                             int64_t sx_block, const uint8_t* Wq, int64_t ldw, int64_t stride_w,
+                             const float* sw, int64_t ldsw, int64_t stride_sw,
+                             const int32_t* offsets, const int32_t* order, int64_t per_token, O* Y,
+                             int64_t ldy, void* ws, hipStream_t s);
+// dX (R x n); ws holds matmul_fp8_grad_bytes (es: the element size of G).
+size_t matmul_fp8_grad_bytes(int es, int64_t R, int64_t experts, int64_t m, int64_t n);
+template <typename G>
+hipError_t launch_matmul_fp8_grad(int64_t R, int64_t experts, int64_t m, int64_t n, const G* g,
+                                  int64_t ldg, const uint8_t* Wq, int64_t ldw, int64_t stride_w,
+                                  const float* sw, int64_t ldsw, int64_t stride_sw,
+                                  const int32_t* offsets, G* dX, int64_t ldx, void* ws,
+                                  hipStream_t s);
+
+// ---- tokens of experts (expert_kernels.hip) -----------------------------------
+size_t sort_tokens_bytes(int64_t N, int64_t E);  // N = T k routes
+hipError_t launch_sort_tokens(int64_t T, int64_t k, int64_t E, const int64_t* ids, int64_t ld,
+                              int32_t* order, int32_t* slots, int32_t* offsets, void* ws,
+                              hipStream_t s);
+template <typename X>
+hipError_t launch_gather_tokens(int64_t T, int64_t n, const X* x, int64_t ldx, int64_t k, int64_t R,
+                                const int32_t* order, X* xs, int64_t lds, hipStream_t s);
+template <typename X>
+hipError_t launch_combine_tokens(int64_t T, int64_t k, int64_t n, int64_t R, const X* ys,
+                                 int64_t ldys, const int32_t* slots, const float* w, X* y,
+                                 int64_t ldy, hipStream_t s);
+// dys (R x n) and dw (T x k), each nullable
+template <typename X>
+hipError_t launch_combine_tokens_grad(int64_t T, int64_t k, int64_t n, int64_t R, const X* g,
+                                      int64_t ldg, const X* ys, int64_t ldys, const int32_t* slots,
+                                      const float* w, X* dys, int64_t lddys, float* dw,
+                                      hipStream_t s);
+
 }  // namespace bk
