@@ -39,7 +39,8 @@ COMMON = [
 # per-source options: MFMA accumulators in ordinary VGPRs (the leaf sweep
 # reads its accumulator every in-tile step, and accumulation registers would
 # need a copy per read; measured slightly faster for the band products too)
-EXTRA = {"solve_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+EXTRA = {"fp8_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "solve_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "band_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "antidiag_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 

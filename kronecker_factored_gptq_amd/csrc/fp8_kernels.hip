@@ -1,6 +1,7 @@
 // 8-bit floating point on gfx950: matrices quantised to e4m3 codes with a float32
 // scale for each block of 1 x 128 or 128 x 128, and the product of such tokens with
 // such weights, for one layer or for groups of tokens with weights of their own.
+#include "block_tile.hpp"
 #include "fp8_product.hpp"
 #include "launch.hpp"
 
@@ -238,7 +239,180 @@ __global__ __launch_bounds__(256) void matmul_fp8_kernel(Groups groups, Fp8Token
       }
 }
 
-size_t matmul_fp8_bytes(int, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+// The same on pipelined tiles, for operands whose rows the direct loads can take. With
+// `splits` ranges of the steps (one layer only) their sums go to parts[range].
+template <class Mul, typename O, int B, int WR, int WC>
+__global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_tile_kernel(
+    Groups groups, Fp8Tokens X, Fp8Weights W, int64_t n, O* __restrict__ Y, int64_t ldy, bool vec,
+    int splits, float* __restrict__ parts, int64_t ldp) {
+  typedef BlockTile<Mul, B, WR, WC> TP;
+  extern __shared__ char lds[];
+  const unsigned nr = (unsigned)((W.m + B - 1) / B);
+  const unsigned nc = groups.offsets ? (unsigned)groups.tiles<B>() : (unsigned)((groups.R + B - 1) / B);
+  const int range = splits > 1 ? blockIdx.x / (nr * nc) : 0;
+  if (!splits || blockIdx.x - range * nr * nc >= nr * nc) return;
+  int tr, tc;
+  tile_of(blockIdx.x - range * nr * nc, nr, nc, tr, tc);
+  int64_t group = 0, c0 = (int64_t)tc * B, cols = groups.R - c0;
+  if (groups.offsets && !groups.tile<B>(tc, group, c0, cols)) return;
+  cols = cols < B ? cols : B;
+  const int64_t r0 = (int64_t)tr * B, rows = W.m - r0 < B ? W.m - r0 : B;
+  const int lane = threadIdx.x & 63, wave = TP::wave();
+
+  typename TP::Side R, C;
+  const int total = (int)((n + kStepBytes - 1) / kStepBytes);
+  const int s0 = (int)((int64_t)total * range / splits), s1 = (int)((int64_t)total * (range + 1) / splits);
+  R.init(W.p + group * W.stride + r0 * W.ld, (int)((rows - 1) * W.ld + n), n, s0,
+         [&](int row) { return (row < (int)rows ? row : (int)rows - 1) * (int)W.ld; });
+  // the token of a tile's column: its offset in rows from `first`, -1 if none
+  const int64_t first = X.order ? 0 : c0;
+  auto token = [&](int col) {
+    col = col < (int)cols ? col : (int)cols - 1;
+    return X.order ? (int)X.token(c0 + col) : col;
+  };
+  C.init(X.p + first * X.ld, (int)(((X.order ? X.T : cols) - 1) * X.ld + n), n, s0, [&](int col) {
+    const int t = token(col);
+    return t < 0 ? TP::kNone : t * (int)X.ld;
+  });
+  const char* scale;
+  int per;
+  if (wave < B / 64) {
+    const int t = token(wave * 64 + lane);
+    scale = (const char*)(X.s + first * X.st);
+    per = t < 0 ? TP::kNone : t * (int)X.st * 4;
+  } else {
+    const int last = (int)((rows - 1) / kBlock);
+    scale = (const char*)(W.s + group * W.strides + r0 / kBlock * W.lds);
+    per = (lane < last ? lane : last) * (int)W.lds * 4;
+  }
+  TP tp;
+  tp.zero();
+  tp.run(R, C, scale, per, (wave < B / 64 ? X.sb : 1) * 4, 1, s0, s1, lds);
+  if (splits > 1) {
+    store_sums(tp, r0, c0, groups.R, parts + range * groups.R * ldp, ldp);
+    return;
+  }
+  if (X.order) {  // rows without a token are 0 whatever the weights' scales are
+#pragma unroll
+    for (int j = 0; j < TP::FC; ++j)
+      if (token(tp.wave_c() + j * 16 + (lane & 15)) < 0) {
+#pragma unroll
+        for (int i = 0; i < TP::FR; ++i) tp.acc[i][j] = f32x4{0, 0, 0, 0};
+      }
+  }
+  store_tile(tp, r0, c0, W.m, c0 + cols, Y, ldy, vec, [](float a, int, int, int) { return a; });
+}
+
+// The ranges' sums; four channels of one row a thread (join_ranges).
+template <typename O, int S>
+__global__ __launch_bounds__(256) void join_fp8_kernel(int64_t m, int64_t R, int splits,
+                                                       const float* __restrict__ parts, int64_t ldp,
+                                                       O* __restrict__ Y, int64_t ldy, bool vec) {
+  __shared__ f32x4 red[S > 1 ? 256 : 1];
+  const int64_t per = ldp / 4, at = JoinAt<S>::at();
+  const int64_t t = at / per, r = (at - t * per) * 4;
+  f32x4 a;
+  if (!join_ranges<S>(parts + t * ldp + r, R * ldp, splits, at < R * per, a, red)) return;
+  O y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = from_f32<O>(a[e]);
+  if (vec && r + 4 <= m) {
+    *(typename Vec4<O>::type*)(Y + t * ldy + r) = __builtin_bit_cast(typename Vec4<O>::type, y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r + e < m) Y[t * ldy + r + e] = y[e];
+  }
+}
+
+// Rows whose length is no multiple of 16 are copied to zero-padded lines first, 16 bytes a
+// thread: the tokens', and behind them every expert's.
+__global__ __launch_bounds__(256) void pack_fp8_kernel(Fp8Tokens X, Fp8Weights W, int64_t experts,
+                                                       int64_t n, char* __restrict__ px,
+                                                       char* __restrict__ pw, int64_t ldp) {
+  const int64_t per = ldp / 16, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  int64_t r = at / per;
+  const int64_t k = (at - r * per) * 16;
+  const char* row;
+  char* to;
+  if (r < X.T) {
+    row = X.p + r * X.ld;
+    to = px + r * ldp;
+  } else {
+    r -= X.T;
+    if (r >= experts * W.m) return;
+    const int64_t e = r / W.m;
+    row = W.p + e * W.stride + (r - e * W.m) * W.ld;
+    to = pw + r * ldp;
+  }
+  *(v4i*)(to + k) = load_any<1>(row, k, n);
+}
+
+static inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+static int64_t packed_ld(int64_t n) { return (n + kStepBytes - 1) / kStepBytes * kStepBytes; }
+static TilePlan fp8_plan(int es, int64_t R, int64_t m, int64_t n) {
+  TilePlan p = plan_tiles(m, R, (n + kStepBytes - 1) / kStepBytes, 1, false, true);
+  if (es == 4 && p.tile == 256) p.tile = 128;
+  return p;
+}
+static TilePlan fp8_plan(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool grouped) {
+  if (!grouped) return fp8_plan(es, R, m, n);
+  const int64_t each = R / experts;
+  return {each >= 128 ? (es == 4 || each < 256 ? 128 : 256) : 64, 1};
+}
+struct Fp8Offsets {
+  size_t x, w, parts, total;
+};
+static Fp8Offsets fp8_offsets(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n) {
+  const bool packs = n % 16 != 0;
+  Fp8Offsets o;
+  o.x = 0;
+  o.w = o.x + up256(packs ? (size_t)(T * packed_ld(n)) : 0);
+  o.parts = o.w + up256(packs ? (size_t)(experts * m * packed_ld(n)) : 0);
+  // with one expert the call may or may not be by groups
+  o.total = o.parts + (experts == 1 ? (size_t)split_words(m, R, fp8_plan(es, R, m, n).splits) * 4 : 0);
+  return o;
+}
+size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n) {
+  return fp8_offsets(es, T, R, experts, m, n).total;
+}
+
+template <class Mul, typename O, int B, int WR, int WC>
+static hipError_t start_fp8_tile(const Groups& groups, const Fp8Tokens& X, const Fp8Weights& W,
+                                 int64_t n, O* Y, int64_t ldy, int splits, float* parts,
+                                 hipStream_t s) {
+  typedef BlockTile<Mul, B, WR, WC> TP;
+  auto* k = matmul_fp8_tile_kernel<Mul, O, B, WR, WC>;
+  if (TP::kLds > 65536) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, TP::kLds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t tiles = (W.m + B - 1) / B * groups.most(B), ldp = (W.m + 3) / 4 * 4;
+  const bool vec = vec4_ok(Y, ldy);
+  hipLaunchKernelGGL(k, dim3((unsigned)(tiles * splits)), dim3(TP::kThreads), TP::kLds, s, groups, X,
+                     W, n, Y, ldy, vec, splits, parts, ldp);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t four = groups.R * (ldp / 4);
+#define BK_JOIN(S)                                                                              \
+  hipLaunchKernelGGL((join_fp8_kernel<O, S>),                                                   \
+                     dim3((unsigned)((four + 256 / S - 1) / (256 / S))), dim3(256), 0, s, W.m,  \
+                     groups.R, splits, parts, ldp, Y, ldy, vec)
+  if (join_slices(splits) == 1) BK_JOIN(1);
+  else BK_JOIN(8);
+#undef BK_JOIN
+  return hipGetLastError();
+}
+
+// Whether the direct loads can take the operands: rows on 16 bytes, and 32-bit offsets.
+static bool fp8_direct(const Fp8Tokens& X, const Fp8Weights& W, int64_t n) {
+  const int64_t kMost = (int64_t)1 << 31;
+  const int64_t reach = X.order ? X.T : 256;
+  return ((uintptr_t)X.p | X.ld | (uintptr_t)W.p | W.ld | W.stride | n) % 16 == 0 &&
+         W.ld <= kTileMaxLd && reach * X.ld + n < kMost && reach * X.st * 4 < kMost &&
+         W.lds * 8 < kMost;
+}
 
 template <typename O>
 hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n,
@@ -246,16 +420,42 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
                              int64_t sx_block, const uint8_t* Wq, int64_t ldw, int64_t stride_w,
                              const float* sw, int64_t ldsw, int64_t stride_sw,
                              const int32_t* offsets, const int32_t* order, int64_t per_token, O* Y,
-                             int64_t ldy, void*, hipStream_t s) {
+                             int64_t ldy, void* ws, hipStream_t s) {
   if (R <= 0 || m <= 0) return hipSuccess;
-  const Groups groups = {offsets, experts, R};
-  const Fp8Tokens X = {(const char*)Xq, ldx, T, sx, sx_token, sx_block, order, per_token};
-  const Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
   typedef typename std::conditional<sizeof(O) == 4, MulFP8Exact, MulFP8>::type Mul;
-  const int64_t tiles = (m + 63) / 64 * groups.most(64);
-  hipLaunchKernelGGL((matmul_fp8_kernel<Mul, O>), dim3((unsigned)tiles), dim3(256), 0, s, groups, X,
-                     W, n, Y, ldy);
-  return hipGetLastError();
+  const Groups groups = {offsets, experts, R};
+  Fp8Tokens X = {(const char*)Xq, ldx, T, sx, sx_token, sx_block, order, per_token};
+  Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
+  const Fp8Offsets o = fp8_offsets(sizeof(O), T, R, experts, m, n);
+  if (n % 16) {
+    const int64_t ld = packed_ld(n);
+    char *px = (char*)ws + o.x, *pw = (char*)ws + o.w;
+    hipLaunchKernelGGL(pack_fp8_kernel,
+                       dim3((unsigned)(((T + experts * m) * (ld / 16) + 255) / 256)), dim3(256), 0,
+                       s, X, W, experts, n, px, pw, ld);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    X.p = px;
+    W.p = pw;
+    X.ld = W.ld = ld;
+    W.stride = m * ld;
+    n = (n + 15) / 16 * 16;
+  }
+  if (!fp8_direct(X, W, n)) {
+    const int64_t tiles = (m + 63) / 64 * groups.most(64);
+    hipLaunchKernelGGL((matmul_fp8_kernel<Mul, O>), dim3((unsigned)tiles), dim3(256), 0, s, groups,
+                       X, W, n, Y, ldy);
+    return hipGetLastError();
+  }
+  float* parts = (float*)((char*)ws + o.parts);
+  const TilePlan plan = fp8_plan(sizeof(O), R, experts, m, n, offsets != nullptr);
+  if constexpr (sizeof(O) != 4) {
+    if (plan.tile == 256)
+      return start_fp8_tile<Mul, O, 256, 2, 4>(groups, X, W, n, Y, ldy, 1, parts, s);
+  }
+  if (plan.tile == 128)
+    return start_fp8_tile<Mul, O, 128, 2, 2>(groups, X, W, n, Y, ldy, plan.splits, parts, s);
+  return start_fp8_tile<Mul, O, 64, 2, 2>(groups, X, W, n, Y, ldy, plan.splits, parts, s);
 }
 
 // ---------------------------------------------------------------------------

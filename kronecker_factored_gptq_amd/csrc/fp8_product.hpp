@@ -22,7 +22,6 @@ struct MulFP8 {
   typedef f32x4 acc_t;
   static constexpr int kElem = 1;
   __device__ static inline f32x4 block(v4i a0, v4i a1, v4i b0, v4i b1) {
-    typedef int v8i __attribute__((ext_vector_type(8)));
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
         __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7),
         __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7), f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0,
@@ -67,6 +66,7 @@ struct Groups {
     const int64_t a = offsets ? offsets[e] : e == 0 ? 0 : R;
     return (int)(a < 0 ? 0 : a > R ? R : a);
   }
+  __device__ static inline int lane_of(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
   // Groups e0 to e0 + 63, one to a lane: first rows and numbers of rows (0 past the last group).
   // `before`: the largest offset before e0 (uniform), which is brought up to date.
   __device__ inline void ranges(int64_t e0, int& before, int& first, int& rows) const {
@@ -81,7 +81,7 @@ struct Groups {
     a = a > before ? a : before;
     first = a;
     rows = has && b > a ? b - a : 0;
-    before = __shfl(a, 63, 64);
+    before = lane_of(a, 63);
   }
   // The group that tile number `at` belongs to when every group is cut into tiles of B
   // rows: its number (uniform over the wave), the tile's first row and the rows from there to
@@ -105,12 +105,12 @@ struct Groups {
       if (past) {
         const int l = __builtin_ctzll(past);
         group = e0 + l;
-        const int skip = ((int)at - (__shfl(sum, l, 64) - __shfl(tiles, l, 64))) * B;
-        first = __shfl(a, l, 64) + skip;
-        rows = __shfl(n, l, 64) - skip;
+        const int skip = ((int)at - (lane_of(sum, l) - lane_of(tiles, l))) * B;
+        first = lane_of(a, l) + skip;
+        rows = lane_of(n, l) - skip;
         return true;
       }
-      at -= __shfl(sum, 63, 64);
+      at -= lane_of(sum, 63);
     }
     return false;
   }
@@ -124,7 +124,7 @@ struct Groups {
       int sum = (n + B - 1) / B;
 #pragma unroll
       for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-      all += sum;
+      all += lane_of(sum, 0);
     }
     return all;
   }
