@@ -270,7 +270,8 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_tile_kernel(
     col = col < (int)cols ? col : (int)cols - 1;
     return X.order ? (int)X.token(c0 + col) : col;
   };
-  C.init(X.p + first * X.ld, (int)(((X.order ? X.T : cols) - 1) * X.ld + n), n, s0, [&](int col) {
+  const int64_t last_row = X.order ? (X.T > 0 ? X.T - 1 : 0) : cols - 1;
+  C.init(X.p + first * X.ld, (int)(last_row * X.ld + n), n, s0, [&](int col) {
     const int t = token(col);
     return t < 0 ? TP::kNone : t * (int)X.ld;
   });
@@ -348,6 +349,190 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(Fp8Tokens X, Fp8Weights W
   *(v4i*)(to + k) = load_any<1>(row, k, n);
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: bound by reading the weights once. A workgroup of 8 waves takes 16 RT channels of
+// one layer and all of its rows, 16 NT at a time; its waves divide k between them, U blocks
+// a turn, straight from memory to registers with the next turn on its way, and their
+// sums meet in LDS (skinny_product.hpp, with the blocks' scales). Grid: channels x (tiles of
+// rows, or experts).
+// ---------------------------------------------------------------------------
+template <class Mul, typename O, int RT, int NT, int U, bool ANY>
+__global__ __launch_bounds__(512) void skinny_fp8_kernel(Groups groups, Fp8Tokens X, Fp8Weights W,
+                                                         int64_t n, O* __restrict__ Y, int64_t ldy,
+                                                         bool vec) {
+  constexpr int kWaves = 8, kTiles = RT * NT, kCols = 16 * NT;
+  static_assert(kTiles <= kWaves, "a wave to each tile");
+  __shared__ f32x4 lds[kWaves * kTiles * 64];
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t group = 0, c0 = (int64_t)blockIdx.y * kCols, end = groups.R;
+  if (groups.offsets) {
+    group = blockIdx.y;
+    int before = 0, a, rows;
+    for (int64_t e0 = 0;; e0 += 64) {
+      groups.ranges(e0, before, a, rows);
+      if (group < e0 + 64) break;
+    }
+    const int l = (int)(group & 63);
+    c0 = Groups::lane_of(a, l);
+    end = c0 + Groups::lane_of(rows, l);
+  } else {
+    end = c0 + kCols < end ? c0 + kCols : end;
+  }
+  const int64_t r0 = (int64_t)blockIdx.x * (16 * RT);
+  const char* pr[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int64_t r = r0 + 16 * i + r16;
+    pr[i] = W.p + group * W.stride + (r < W.m ? r : W.m - 1) * W.ld;
+  }
+  const float* sw = W.s + group * W.strides + r0 / kBlock * W.lds;  // one block of rows: 16 RT divides 128
+  const int nb = (int)((n + kBlock - 1) / kBlock);
+  auto load = [&](const char* row, int64_t k) {
+    if (ANY) return load_any<1>(row, k, n);
+    return k < n ? *(const v4i*)(row + k) : v4i{0, 0, 0, 0};
+  };
+  for (; c0 < end; c0 += kCols) {
+    const char* pc[NT];
+    const float* ps[NT];
+    bool has[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t c = c0 + 16 * j + r16, t = X.token(c < end ? c : end - 1);
+      has[j] = t >= 0;
+      pc[j] = X.p + (has[j] ? t : 0) * X.ld;
+      ps[j] = X.s + (has[j] ? t : 0) * X.st;
+    }
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    struct Turn {
+      v4i a[U][RT][2], b[U][NT][2];
+      float f[U][NT], w[U];
+    };
+    auto read = [&](Turn& t, int b0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t k = (int64_t)(b0 + u) * kBlock + 16 * q;
+        const int b = b0 + u < nb ? b0 + u : nb - 1;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          t.a[u][i][0] = load(pr[i], k);
+          t.a[u][i][1] = load(pr[i], k + 64);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          t.b[u][j][0] = load(pc[j], k);
+          t.b[u][j][1] = load(pc[j], k + 64);
+          t.f[u][j] = ps[j][b * X.sb];
+        }
+        t.w[u] = sw[b];
+      }
+    };
+    auto multiply = [&](const Turn& t, int b0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (b0 + u >= nb) break;  // nothing, but for a scale that is not finite
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float f = has[j] ? t.f[u][j] * t.w[u] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const f32x4 p = Mul::block(t.a[u][i][0], t.a[u][i][1], t.b[u][j][0], t.b[u][j][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i][j][e] = __builtin_fmaf(has[j] ? p[e] : 0.0f, f, acc[i][j][e]);
+          }
+        }
+      }
+    };
+    int b = wave * U;
+    if (b < nb) {
+      Turn x, y;
+      read(x, b);
+      while (b + kWaves * U < nb) {
+        read(y, b + kWaves * U);
+        multiply(x, b);
+        b += kWaves * U;
+        if (b + kWaves * U >= nb) {
+          x = y;
+          break;
+        }
+        read(x, b + kWaves * U);
+        multiply(y, b);
+        b += kWaves * U;
+      }
+      multiply(x, b);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) lds[(wave * kTiles + i * NT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    if (wave < kTiles) {
+      f32x4 sum = lds[wave * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += lds[(w * kTiles + wave) * 64 + lane];
+      const int64_t c = c0 + wave % NT * 16 + r16, r = r0 + wave / NT * 16 + 4 * q;
+      if (c < end && r < W.m) {
+        O y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = from_f32<O>(sum[e]);
+        if (vec && r + 4 <= W.m) {
+          *(typename Vec4<O>::type*)(Y + c * ldy + r) = __builtin_bit_cast(typename Vec4<O>::type, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e < W.m) Y[c * ldy + r + e] = y[e];
+        }
+      }
+    }
+    __syncthreads();  // the sums were read: the next rows' may be written
+  }
+}
+
+// Whether the kernel above takes a call. Of one layer as many rows as the int8 product's takes
+// (4096 x 4096, 64 rows: 12.6 us against 14.6 of tiles). Of experts, whose number of rows each is
+// not known here, up to 8 on average where k is long enough for eight waves: 2048 x 4096 of 64
+// experts, f16, 1 / 4 / 8 / 16 rows each on average 46 / 104 / 116 / 162 us against 39 / 143 / 129 / 133 of
+// tiles; 4096 x 1024 of 16, 2 / 8 / 32 rows: 19 / 21 / 33 against 14.7 / 15.6 / 17.6.
+static bool fp8_skinny(int64_t R, int64_t experts, int64_t m, int64_t n) {
+  if (experts == 1) return R <= (m * n <= (1 << 24) ? 64 : m * n <= (1 << 26) ? 16 : 8);
+  return R <= 8 * experts && n >= 2048;
+}
+template <class Mul, typename O, bool ANY>
+static hipError_t start_skinny_fp8(const Groups& groups, const Fp8Tokens& X, const Fp8Weights& W,
+                                   int64_t n, O* Y, int64_t ldy, hipStream_t s) {
+  const bool vec = vec4_ok(Y, ldy);
+  // rows at a time; channels a workgroup, more where that leaves nearly every CU one: the rows
+  // are then read less often (14336 x 4096, one row: 13.9 us with 64 channels, 15.1 with 16; 4096 x
+  // 14336 30.8 and 12.8; 64 experts of 2048 x 4096, 256 rows: 104 with 64, 116 with 32, 122 with 16)
+  const int64_t each = (groups.R + groups.count - 1) / groups.count;
+  const int nt = each > 32 ? 4 : each > 16 ? 2 : 1;
+  const int64_t work = W.m * (groups.offsets ? groups.count : (groups.R + 16 * nt - 1) / (16 * nt));
+  const int rt = work >= 64 * 192 ? 4 : work >= 32 * 192 ? 2 : 1;
+#define BK_SKINNY(RT, NT, U)                                                                   \
+  hipLaunchKernelGGL(                                                                          \
+      (skinny_fp8_kernel<Mul, O, RT, NT, U, ANY>),                                             \
+      dim3((unsigned)((W.m + 16 * RT - 1) / (16 * RT)),                                        \
+           (unsigned)(groups.offsets ? groups.count : (groups.R + 16 * NT - 1) / (16 * NT))),  \
+      dim3(512), 0, s, groups, X, W, n, Y, ldy, vec)
+  if (nt == 1) {
+    if (rt == 4) BK_SKINNY(4, 1, 1);
+    else if (rt == 2) BK_SKINNY(2, 1, 2);
+    else BK_SKINNY(1, 1, 2);
+  } else if (nt == 2) {
+    if (rt >= 2) BK_SKINNY(2, 2, 1);
+    else BK_SKINNY(1, 2, 2);
+  } else {
+    BK_SKINNY(1, 4, 1);
+  }
+#undef BK_SKINNY
+  return hipGetLastError();
+}
+
 static inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 static int64_t packed_ld(int64_t n) { return (n + kStepBytes - 1) / kStepBytes * kStepBytes; }
 static TilePlan fp8_plan(int es, int64_t R, int64_t m, int64_t n) {
@@ -364,13 +549,13 @@ struct Fp8Offsets {
   size_t x, w, parts, total;
 };
 static Fp8Offsets fp8_offsets(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n) {
-  const bool packs = n % 16 != 0;
+  const bool skinny = fp8_skinny(R, experts, m, n), packs = n % 16 != 0 && !skinny;
   Fp8Offsets o;
   o.x = 0;
   o.w = o.x + up256(packs ? (size_t)(T * packed_ld(n)) : 0);
   o.parts = o.w + up256(packs ? (size_t)(experts * m * packed_ld(n)) : 0);
   // with one expert the call may or may not be by groups
-  o.total = o.parts + (experts == 1 ? (size_t)split_words(m, R, fp8_plan(es, R, m, n).splits) * 4 : 0);
+  o.total = o.parts + (experts == 1 && !skinny ? (size_t)split_words(m, R, fp8_plan(es, R, m, n).splits) * 4 : 0);
   return o;
 }
 size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n) {
@@ -426,6 +611,16 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
   const Groups groups = {offsets, experts, R};
   Fp8Tokens X = {(const char*)Xq, ldx, T, sx, sx_token, sx_block, order, per_token};
   Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
+  if (T == 0) {  // rows without a token read one all the same: readable memory of that size
+    X.p = W.p;
+    X.ld = W.ld;
+    X.s = W.s;
+    X.st = 0;
+    X.sb = 1;
+  }
+  if (fp8_skinny(R, experts, m, n))
+    return n % 16 == 0 && fp8_direct(X, W, n) ? start_skinny_fp8<Mul, O, false>(groups, X, W, n, Y, ldy, s)
+                                              : start_skinny_fp8<Mul, O, true>(groups, X, W, n, Y, ldy, s);
   const Fp8Offsets o = fp8_offsets(sizeof(O), T, R, experts, m, n);
   if (n % 16) {
     const int64_t ld = packed_ld(n);

@@ -210,6 +210,11 @@ def test_matmul_empty(gpu_lib):
         assert (Y == 0).all()
         D = bk.matmul_fp8_grad(o(T, 0), z(0, 150), o(0, 2), out=torch.full((T, 150), 3.0, device="cuda"))
         assert (D == 0).all()
+    for T, R in ((0, 3), (0, 300), (1, 300)):  # an order that names no token, of none
+        order = torch.full((R,), T, dtype=torch.int32, device="cuda")
+        for n in (400, 401):
+            Y = bk.matmul_fp8(z(T, n), o(T, 4), z(130, n), torch.full((2, 4), float("nan"), device="cuda"), order=order)
+            assert Y.shape == (R, 130) and (Y == 0).all()
     assert bk.matmul_fp8_grad(o(0, 5), z(5, 8), o(1, 1)).shape == (0, 8)
     assert bk.matmul_fp8_grad(o(4, 5), z(5, 0), o(1, 0)).shape == (4, 0)
 
@@ -288,9 +293,12 @@ def test_odd_groups(gpu_lib, t):
     plain = bk.matmul_fp8(X, S, W, SW, offsets=off, out_dtype=TYPES[t])
     plain[[3, 70, 149]] = 0
     assert torch.equal(Y, plain)
-    shared = bk.matmul_fp8(X, S, W[:1].expand(E, m, n), SW[:1].expand(E, 2, 2), offsets=off, out_dtype=TYPES[t])
-    assert torch.equal(shared, bk.matmul_fp8(X, S, W[:1].contiguous(), SW[:1].contiguous(),
-                                             offsets=off[[0, 4]].contiguous(), out_dtype=TYPES[t]))
+    # one layer's weights for all groups, and as one group (sums may be ordered otherwise: the definition's
+    # tolerance for each)
+    for w, v, o in ((W[:1].expand(E, m, n), SW[:1].expand(E, 2, 2), off),
+                    (W[:1].contiguous(), SW[:1].contiguous(), off[[0, 4]].contiguous())):
+        err = (bk.matmul_fp8(X, S, w, v, offsets=o, out_dtype=TYPES[t]).cpu().double() - each[0][0]).abs()
+        assert (err <= tolerance(each[0][0], each[0][1], n, TYPES[t], True)).all()
 
 
 def check_grad(bk, G, wb, n, sw, out=None):
