@@ -141,108 +141,12 @@ hipError_t launch_quantize_fp8(int64_t batch, int64_t rows, int64_t n, const X* 
 
 // ---------------------------------------------------------------------------
 // Y[r][i] = sum over blocks b of k of sx[t][b] sw[i / 128][b] sum_{j in b} Xq[t][j] Wq[i][j],
-// t the token of row r, W its group's. Tiles of 64 channels x 64 rows, a block of k a
-// step, read to registers while the step before is computed.
+// t the token of row r, W its group's: tiles of channels x rows. With `splits` ranges of the
+// steps (one layer only) their sums go to parts[range]. ANY: operands that the direct loads
+// cannot take.
 // ---------------------------------------------------------------------------
-template <class Mul, typename O>
-__global__ __launch_bounds__(256) void matmul_fp8_kernel(Groups groups, Fp8Tokens X, Fp8Weights W,
-                                                         int64_t n, O* __restrict__ Y, int64_t ldy) {
-  constexpr int B = 64, F = 2;  // four waves of 32 x 32
-  __shared__ __attribute__((aligned(16))) char lds[2 * 2 * B * kBlock];
-  const unsigned nr = (unsigned)((W.m + B - 1) / B);
-  const unsigned nc = (unsigned)groups.tiles<B>();
-  if (blockIdx.x >= nr * nc) return;
-  int tr, tc;
-  tile_of(blockIdx.x, nr, nc, tr, tc);
-  int64_t group, c0, cols;
-  if (!groups.tile<B>(tc, group, c0, cols)) return;
-  const int64_t r0 = (int64_t)tr * B;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane & 15, q = lane >> 4;
-  const int wr = (wave >> 1) * 32, wc = (wave & 1) * 32;
-  const char* w = W.p + group * W.stride;
-  const float* sw = W.s + group * W.strides + r0 / kBlock * W.lds;
-  const char *pw[2], *px[2];  // this thread's chunks: of rows tid / 8 and 32 further
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int64_t e = u * 32 + (tid >> 3), i = r0 + e;
-    pw[u] = w + (i < W.m ? i : W.m - 1) * W.ld;
-    const int64_t t = X.token(c0 + (e < cols ? e : cols - 1));
-    px[u] = t < 0 ? nullptr : X.p + t * X.ld;
-  }
-  const float* ps[F];
-#pragma unroll
-  for (int j = 0; j < F; ++j) {
-    const int64_t e = wc + j * 16 + r16, t = X.token(c0 + (e < cols ? e : cols - 1));
-    ps[j] = t < 0 ? nullptr : X.s + t * X.st;
-  }
-  f32x4 acc[F][F];
-#pragma unroll
-  for (int i = 0; i < F; ++i)
-#pragma unroll
-    for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  auto at = [&](int row, int chunk) { return row * kBlock + (chunk ^ ((row >> 1) & 7)) * 16; };
-  const int64_t nb = (n + kBlock - 1) / kBlock;
-  v4i vw[2], vx[2];
-  auto read = [&](int64_t b) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      vw[u] = load_any<1>(pw[u], b * kBlock + (tid & 7) * 16, n);
-      vx[u] = px[u] ? load_any<1>(px[u], b * kBlock + (tid & 7) * 16, n) : v4i{0, 0, 0, 0};
-    }
-  };
-  auto write = [&](int slot) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      *(v4i*)(lds + slot * 2 * B * kBlock + at(u * 32 + (tid >> 3), tid & 7)) = vw[u];
-      *(v4i*)(lds + (slot * 2 + 1) * B * kBlock + at(u * 32 + (tid >> 3), tid & 7)) = vx[u];
-    }
-  };
-  if (nb > 0) {
-    read(0);
-    write(0);
-  }
-  __syncthreads();
-  for (int64_t b = 0; b < nb; ++b) {
-    if (b + 1 < nb) read(b + 1);
-    const char *lw = lds + (b & 1) * 2 * B * kBlock, *lx = lw + B * kBlock;
-    const float fw = sw[b];
-    v4i x[F][2], y[F][2];
-    float f[F];
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        x[i][h] = *(const v4i*)(lw + at(wr + i * 16 + r16, h * 4 + q));
-        y[i][h] = *(const v4i*)(lx + at(wc + i * 16 + r16, h * 4 + q));
-      }
-#pragma unroll
-    for (int j = 0; j < F; ++j) f[j] = ps[j] ? ps[j][b * X.sb] * fw : 0.0f;
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) {
-        const f32x4 p = Mul::block(x[i][0], x[i][1], y[j][0], y[j][1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], f[j], acc[i][j][e]);
-      }
-    if (b + 1 < nb) write((b + 1) & 1);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int j = 0; j < F; ++j)
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t c = wc + j * 16 + r16, r = r0 + wr + i * 16 + 4 * q + e;
-        if (c < cols && r < W.m) Y[(c0 + c) * ldy + r] = from_f32<O>(acc[i][j][e]);
-      }
-}
-
-// The same on pipelined tiles, for operands whose rows the direct loads can take. With
-// `splits` ranges of the steps (one layer only) their sums go to parts[range].
-template <class Mul, typename O, int B, int WR, int WC>
-__global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_tile_kernel(
+template <class Mul, typename O, int B, int WR, int WC, bool ANY>
+__global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
     Groups groups, Fp8Tokens X, Fp8Weights W, int64_t n, O* __restrict__ Y, int64_t ldy, bool vec,
     int splits, float* __restrict__ parts, int64_t ldp) {
   typedef BlockTile<Mul, B, WR, WC> TP;
@@ -250,7 +154,7 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_tile_kernel(
   const unsigned nr = (unsigned)((W.m + B - 1) / B);
   const unsigned nc = groups.offsets ? (unsigned)groups.tiles<B>() : (unsigned)((groups.R + B - 1) / B);
   const int range = splits > 1 ? blockIdx.x / (nr * nc) : 0;
-  if (!splits || blockIdx.x - range * nr * nc >= nr * nc) return;
+  if (blockIdx.x - range * nr * nc >= nr * nc) return;
   int tr, tc;
   tile_of(blockIdx.x - range * nr * nc, nr, nc, tr, tc);
   int64_t group = 0, c0 = (int64_t)tc * B, cols = groups.R - c0;
@@ -258,11 +162,32 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_tile_kernel(
   cols = cols < B ? cols : B;
   const int64_t r0 = (int64_t)tr * B, rows = W.m - r0 < B ? W.m - r0 : B;
   const int lane = threadIdx.x & 63, wave = TP::wave();
-
-  typename TP::Side R, C;
   const int total = (int)((n + kStepBytes - 1) / kStepBytes);
+  TP tp;
+  tp.zero();
+  if constexpr (ANY) {
+    const char* w = W.p + group * W.stride + r0 * W.ld;
+    const float* sw = W.s + group * W.strides + (r0 + tp.wave_r() < W.m ? r0 + tp.wave_r() : W.m - 1) / kBlock * W.lds;
+    auto token = [&](int col) { return X.token(c0 + (col < (int)cols ? col : (int)cols - 1)); };
+    tp.run_any(
+        total, lds,
+        [&](int s, int row) {
+          return typename TP::Bytes{w + (row < (int)rows ? row : (int)rows - 1) * W.ld, (int64_t)s * kBlock, n};
+        },
+        [&](int s, int col) {
+          const int64_t t = token(col);
+          return typename TP::Bytes{t < 0 ? nullptr : X.p + t * X.ld, (int64_t)s * kBlock, n};
+        },
+        [&](int s, int j) {
+          const int64_t t = token(tp.wave_c() + j * 16 + (lane & 15));
+          return t < 0 ? 0.0f : X.s[t * X.st + s * X.sb] * sw[s];
+        });
+    store_tile(tp, r0, c0, W.m, c0 + cols, Y, ldy, vec, [](float a, int, int, int) { return a; });
+    return;
+  }
+  typename TP::Side R, C;
   const int s0 = (int)((int64_t)total * range / splits), s1 = (int)((int64_t)total * (range + 1) / splits);
-  R.init(W.p + group * W.stride + r0 * W.ld, (int)((rows - 1) * W.ld + n), n, s0,
+  R.init(W.p + group * W.stride + r0 * W.ld, (int)((rows - 1) * W.ld + n), n, 0, s0,
          [&](int row) { return (row < (int)rows ? row : (int)rows - 1) * (int)W.ld; });
   // the token of a tile's column: its offset in rows from `first`, -1 if none
   const int64_t first = X.order ? 0 : c0;
@@ -271,7 +196,7 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_tile_kernel(
     return X.order ? (int)X.token(c0 + col) : col;
   };
   const int64_t last_row = X.order ? (X.T > 0 ? X.T - 1 : 0) : cols - 1;
-  C.init(X.p + first * X.ld, (int)(last_row * X.ld + n), n, s0, [&](int col) {
+  C.init(X.p + first * X.ld, (int)(last_row * X.ld + n), n, 0, s0, [&](int col) {
     const int t = token(col);
     return t < 0 ? TP::kNone : t * (int)X.ld;
   });
@@ -286,9 +211,7 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_tile_kernel(
     scale = (const char*)(W.s + group * W.strides + r0 / kBlock * W.lds);
     per = (lane < last ? lane : last) * (int)W.lds * 4;
   }
-  TP tp;
-  tp.zero();
-  tp.run(R, C, scale, per, (wave < B / 64 ? X.sb : 1) * 4, 1, s0, s1, lds);
+  tp.run(R, C, scale, per, (wave < B / 64 ? X.sb : 1) * 4, s0, s1, lds);
   if (splits > 1) {
     store_sums(tp, r0, c0, groups.R, parts + range * groups.R * ldp, ldp);
     return;
@@ -324,6 +247,20 @@ __global__ __launch_bounds__(256) void join_fp8_kernel(int64_t m, int64_t R, int
     for (int e = 0; e < 4; ++e)
       if (r + e < m) Y[t * ldy + r + e] = y[e];
   }
+}
+
+template <typename O>
+static hipError_t join_fp8(int64_t m, int64_t R, int splits, const float* parts, int64_t ldp, O* Y,
+                           int64_t ldy, bool vec, hipStream_t s) {
+  const int64_t four = R * (ldp / 4);
+#define BK_JOIN(S)                                                                             \
+  hipLaunchKernelGGL((join_fp8_kernel<O, S>),                                                  \
+                     dim3((unsigned)((four + 256 / S - 1) / (256 / S))), dim3(256), 0, s, m, R, \
+                     splits, parts, ldp, Y, ldy, vec)
+  if (join_slices(splits) == 1) BK_JOIN(1);
+  else BK_JOIN(8);
+#undef BK_JOIN
+  return hipGetLastError();
 }
 
 // Rows whose length is no multiple of 16 are copied to zero-padded lines first, 16 bytes a
@@ -562,32 +499,25 @@ size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m
   return fp8_offsets(es, T, R, experts, m, n).total;
 }
 
-template <class Mul, typename O, int B, int WR, int WC>
+template <class Mul, typename O, int B, int WR, int WC, bool ANY = false>
 static hipError_t start_fp8_tile(const Groups& groups, const Fp8Tokens& X, const Fp8Weights& W,
                                  int64_t n, O* Y, int64_t ldy, int splits, float* parts,
                                  hipStream_t s) {
   typedef BlockTile<Mul, B, WR, WC> TP;
-  auto* k = matmul_fp8_tile_kernel<Mul, O, B, WR, WC>;
-  if (TP::kLds > 65536) {
+  auto* k = matmul_fp8_kernel<Mul, O, B, WR, WC, ANY>;
+  constexpr int lds = ANY ? TP::kAnyLds : TP::kLds;
+  if (lds > 65536) {
     const hipError_t e =
-        hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, TP::kLds);
+        hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
   const int64_t tiles = (W.m + B - 1) / B * groups.most(B), ldp = (W.m + 3) / 4 * 4;
   const bool vec = vec4_ok(Y, ldy);
-  hipLaunchKernelGGL(k, dim3((unsigned)(tiles * splits)), dim3(TP::kThreads), TP::kLds, s, groups, X,
+  hipLaunchKernelGGL(k, dim3((unsigned)(tiles * splits)), dim3(TP::kThreads), lds, s, groups, X,
                      W, n, Y, ldy, vec, splits, parts, ldp);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  const int64_t four = groups.R * (ldp / 4);
-#define BK_JOIN(S)                                                                              \
-  hipLaunchKernelGGL((join_fp8_kernel<O, S>),                                                   \
-                     dim3((unsigned)((four + 256 / S - 1) / (256 / S))), dim3(256), 0, s, W.m,  \
-                     groups.R, splits, parts, ldp, Y, ldy, vec)
-  if (join_slices(splits) == 1) BK_JOIN(1);
-  else BK_JOIN(8);
-#undef BK_JOIN
-  return hipGetLastError();
+  return join_fp8(W.m, groups.R, splits, parts, ldp, Y, ldy, vec, s);
 }
 
 // Whether the direct loads can take the operands: rows on 16 bytes, and 32-bit offsets.
@@ -636,13 +566,9 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
     W.stride = m * ld;
     n = (n + 15) / 16 * 16;
   }
-  if (!fp8_direct(X, W, n)) {
-    const int64_t tiles = (m + 63) / 64 * groups.most(64);
-    hipLaunchKernelGGL((matmul_fp8_kernel<Mul, O>), dim3((unsigned)tiles), dim3(256), 0, s, groups,
-                       X, W, n, Y, ldy);
-    return hipGetLastError();
-  }
   float* parts = (float*)((char*)ws + o.parts);
+  if (!fp8_direct(X, W, n))
+    return start_fp8_tile<Mul, O, 64, 2, 2, true>(groups, X, W, n, Y, ldy, 1, parts, s);
   const TilePlan plan = fp8_plan(sizeof(O), R, experts, m, n, offsets != nullptr);
   if constexpr (sizeof(O) != 4) {
     if (plan.tile == 256)
@@ -654,51 +580,178 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
 }
 
 // ---------------------------------------------------------------------------
-// dX[r][j] = sum_i G[r][i] sw[i / 128][j / 128] Wq[i][j]: a thread to an output, its sum
-// over the channels in order.
+// dX[r][j] = sum_i G[r][i] sw[i / 128][j / 128] Wq[i][j]: tiles of columns j x rows r, the codes
+// k-major and made 16-bit in registers (BlockTile, kTransposed). A bfloat16 or float16 G is
+// multiplied as it is, a float32 one as its three bfloat16 planes, one after the other
+// over all of k. With `splits` ranges of the steps (one layer only) their sums go to
+// parts[range].
 // ---------------------------------------------------------------------------
-template <typename G>
-__global__ __launch_bounds__(256) void matmul_fp8_grad_kernel(Groups groups, int64_t m, int64_t n,
-                                                              const G* __restrict__ g, int64_t ldg,
-                                                              Fp8Weights W, G* __restrict__ dX,
-                                                              int64_t ldx) {
-  const int64_t per = (n + 255) / 256, r = blockIdx.x / per;
-  const int64_t j = (blockIdx.x - r * per) * 256 + threadIdx.x;
-  int64_t e = 0, first = 0;
-  for (; e < groups.count; ++e) {
-    const int64_t a = groups.offset(e);
-    first = a > first ? a : first;
-    if (r >= first && r < groups.offset(e + 1)) break;
+struct Fp8Gradient {
+  const char* p;
+  int64_t ld, plane;  // bytes
+};
+template <class Mul, typename O, int B, int WR, int WC, bool ANY>
+__global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_grad_kernel(
+    Groups groups, Fp8Gradient G, Fp8Weights W, int64_t n, O* __restrict__ dX, int64_t ldx,
+    bool vec, int splits, float* __restrict__ parts, int64_t ldp) {
+  typedef BlockTile<Mul, B, WR, WC> TP;
+  extern __shared__ char lds[];
+  const unsigned nr = (unsigned)((n + B - 1) / B);
+  const unsigned nc = groups.offsets ? (unsigned)groups.tiles<B>() : (unsigned)((groups.R + B - 1) / B);
+  const int range = splits > 1 ? blockIdx.x / (nr * nc) : 0;
+  if (blockIdx.x - range * nr * nc >= nr * nc) return;
+  int tr, tc;
+  tile_of(blockIdx.x - range * nr * nc, nr, nc, tr, tc);
+  int64_t group = 0, c0 = (int64_t)tc * B, cols = groups.R - c0;
+  if (groups.offsets && !groups.tile<B>(tc, group, c0, cols)) return;
+  cols = cols < B ? cols : B;
+  const int64_t r0 = (int64_t)tr * B, rows = n - r0 < B ? n - r0 : B;
+  const int lane = threadIdx.x & 63;
+  const int64_t kbytes = (W.m + 7) / 8 * 16;  // whole chunks: G's rows are zero up to them
+  const int64_t total = (kbytes + kStepBytes - 1) / kStepBytes * Mul::kPlanes;
+  const int s0 = (int)(total * range / splits), s1 = (int)(total * (range + 1) / splits);
+  const int last = (int)((rows - 1) / kBlock);
+  TP tp;
+  tp.zero();
+  if constexpr (ANY) {
+    const char* w = W.p + group * W.stride + r0;
+    const int block = tp.wave_r() / kBlock;
+    const float* sw = W.s + group * W.strides + r0 / kBlock + (block < last ? block : last);
+    const int64_t each = total / Mul::kPlanes;
+    tp.run_any(
+        (int)total, lds,
+        [&](int s, int k) {
+          const int64_t i = s % each * 64 + k;
+          return typename TP::Bytes{i < W.m ? w + i * W.ld : nullptr, 0, rows};
+        },
+        [&](int s, int col) {
+          const int64_t c = c0 + (col < (int)cols ? col : (int)cols - 1);
+          return typename TP::Bytes{G.p + s / each * G.plane + c * G.ld, s % each * kStepBytes, W.m * 2};
+        },
+        [&](int s, int) { return sw[s % each / 2 * W.lds]; });
+    store_tile(tp, r0, c0, n, c0 + cols, dX, ldx, vec, [](float a, int, int, int) { return a; });
+    return;
   }
-  if (e == groups.count) return;
-  if (j >= n) return;
-  const unsigned char* w = (const unsigned char*)W.p + e * W.stride + j;
-  const float* sw = W.s + e * W.strides + j / kBlock;
-  float sum = 0.0f;
-  for (int64_t i0 = 0; i0 < m; i0 += kBlock) {
-    float part = 0.0f;
-    for (int64_t i = i0; i < i0 + kBlock && i < m; ++i)
-      part = __builtin_fmaf(to_f32(g[r * ldg + i]),
-                            __builtin_amdgcn_cvt_f32_fp8((int)w[i * W.ld], 0), part);
-    sum = __builtin_fmaf(part, sw[i0 / kBlock * W.lds], sum);
+  typename TP::SideR R;
+  typename TP::Side C;
+  R.init(W.p + group * W.stride + r0, W.ld, W.m, (int)rows, s0);
+  C.init(G.p + c0 * G.ld, (int)((cols - 1) * G.ld + kbytes), kbytes, G.plane, s0,
+         [&](int col) { return (col < (int)cols ? col : (int)cols - 1) * (int)G.ld; });
+  tp.run(R, C, (const char*)(W.s + group * W.strides + r0 / kBlock), (lane < last ? lane : last) * 4,
+         W.lds * 4, s0, s1, lds);
+  if (splits > 1) {
+    store_sums(tp, r0, c0, groups.R, parts + range * groups.R * ldp, ldp);
+    return;
   }
-  dX[r * ldx + j] = from_f32<G>(sum);
+  store_tile(tp, r0, c0, n, c0 + cols, dX, ldx, vec, [](float a, int, int, int) { return a; });
 }
 
-size_t matmul_fp8_grad_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+// Codes whose rows are no multiple of 16 long or do not start on 16 bytes, and a 16-bit G
+// likewise, are copied to zero-padded lines first.
+template <int E>
+__global__ __launch_bounds__(256) void pack_rows_kernel(const char* __restrict__ p, int64_t ld,
+                                                        int64_t stride, int64_t per_batch,
+                                                        int64_t rows, int64_t bytes,
+                                                        char* __restrict__ to, int64_t ldp) {
+  const int64_t per = ldp / 16, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = at / per, k = (at - r * per) * 16;
+  if (r >= rows) return;
+  const int64_t z = r / per_batch;
+  *(v4i*)(to + r * ldp + k) = load_any<E>(p + z * stride + (r - z * per_batch) * ld, k, bytes);
+}
+template <int E>
+static hipError_t pack_rows(const char* p, int64_t ld, int64_t stride, int64_t per_batch,
+                            int64_t rows, int64_t bytes, char* to, int64_t ldp, hipStream_t s) {
+  const int64_t n = rows * (ldp / 16);
+  if (n <= 0) return hipSuccess;
+  hipLaunchKernelGGL(pack_rows_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p, ld,
+                     stride, per_batch, rows, bytes, to, ldp);
+  return hipGetLastError();
+}
+
+static TilePlan fp8_grad_plan(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool grouped) {
+  if (!grouped) return plan_tiles(n, R, (m + 63) / 64, es == 4 ? 3 : 1, true, true);
+  const int64_t each = R / experts;
+  return {each >= 256 ? 256 : each >= 128 ? 128 : 64, 1};
+}
+struct Fp8GradOffsets {
+  size_t w, g, parts, total;
+};
+static Fp8GradOffsets fp8_grad_offsets(int es, int64_t R, int64_t experts, int64_t m, int64_t n) {
+  Fp8GradOffsets o;
+  o.w = 0;
+  o.g = o.w + up256(n % 16 ? (size_t)(experts * m * packed_ld(n)) : 0);
+  o.parts = o.g + up256(es == 4 ? (size_t)(3 * R * plane_ld(m)) : m % 8 ? (size_t)(R * plane_ld(m)) : 0);
+  o.total = o.parts + (experts == 1 ? (size_t)split_words(n, R, fp8_grad_plan(es, R, 1, m, n, false).splits) * 4 : 0);
+  return o;
+}
+size_t matmul_fp8_grad_bytes(int es, int64_t R, int64_t experts, int64_t m, int64_t n) {
+  return fp8_grad_offsets(es, R, experts, m, n).total;
+}
+
+template <class Mul, typename O, int B, int WR, int WC, bool ANY = false>
+static hipError_t start_fp8_grad(const Groups& groups, const Fp8Gradient& G, const Fp8Weights& W,
+                                 int64_t n, O* dX, int64_t ldx, int splits, float* parts,
+                                 hipStream_t s) {
+  typedef BlockTile<Mul, B, WR, WC> TP;
+  auto* k = matmul_fp8_grad_kernel<Mul, O, B, WR, WC, ANY>;
+  constexpr int lds = ANY ? TP::kAnyLds : TP::kLds;
+  if (lds > 65536) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t tiles = (n + B - 1) / B * groups.most(B), ldp = (n + 3) / 4 * 4;
+  const bool vec = vec4_ok(dX, ldx);
+  hipLaunchKernelGGL(k, dim3((unsigned)(tiles * splits)), dim3(TP::kThreads), lds, s, groups, G,
+                     W, n, dX, ldx, vec, splits, parts, ldp);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  return join_fp8(n, groups.R, splits, parts, ldp, dX, ldx, vec, s);
+}
 
 template <typename G>
 hipError_t launch_matmul_fp8_grad(int64_t R, int64_t experts, int64_t m, int64_t n, const G* g,
                                   int64_t ldg, const uint8_t* Wq, int64_t ldw, int64_t stride_w,
                                   const float* sw, int64_t ldsw, int64_t stride_sw,
-                                  const int32_t* offsets, G* dX, int64_t ldx, void*,
+                                  const int32_t* offsets, G* dX, int64_t ldx, void* ws,
                                   hipStream_t s) {
   if (R <= 0 || n <= 0) return hipSuccess;
+  constexpr bool wide = sizeof(G) == 4;
+  typedef MulWide<typename std::conditional<std::is_same<G, F16>::value, MmaF16, MmaBF16>::type, wide ? 3 : 1> Mul;
   const Groups groups = {offsets, experts, R};
-  const Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
-  hipLaunchKernelGGL(matmul_fp8_grad_kernel<G>, dim3((unsigned)(R * ((n + 255) / 256))), dim3(256),
-                     0, s, groups, m, n, g, ldg, W, dX, ldx);
-  return hipGetLastError();
+  Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
+  const Fp8GradOffsets o = fp8_grad_offsets(sizeof(G), R, experts, m, n);
+  char* b = (char*)ws;
+  hipError_t e = hipSuccess;
+  if (n % 16) {
+    e = pack_rows<1>(W.p, ldw, stride_w, m > 0 ? m : 1, experts * m, n, b + o.w, packed_ld(n), s);
+    if (e != hipSuccess) return e;
+    W.p = b + o.w;
+    W.ld = packed_ld(n);
+    W.stride = m * W.ld;
+  }
+  Fp8Gradient x = {(const char*)g, ldg * (int64_t)sizeof(G), 0};
+  if (wide) {
+    const Planes planes = {b + o.g, plane_ld(m), R * plane_ld(m)};
+    e = launch_planes<float, kBF16x3>(R, m, (const float*)g, ldg, nullptr, nullptr, planes, s);
+    x = {planes.w, planes.ld, planes.plane};
+  } else if (m % 8) {
+    e = pack_rows<2>(x.p, x.ld, 0, R, R, m * 2, b + o.g, plane_ld(m), s);
+    x = {b + o.g, plane_ld(m), 0};
+  }
+  if (e != hipSuccess) return e;
+  float* parts = (float*)(b + o.parts);
+  // 16-byte rows and 32-bit offsets
+  if (((uintptr_t)W.p | W.ld | W.stride | (uintptr_t)x.p | x.ld | x.plane) % 16 != 0 ||
+      W.ld > kTileMaxLd || x.ld > kTileMaxLd)
+    return start_fp8_grad<Mul, G, 64, 2, 2, true>(groups, x, W, n, dX, ldx, 1, parts, s);
+  const TilePlan plan = fp8_grad_plan(sizeof(G), R, experts, m, n, offsets != nullptr);
+  if (plan.tile == 256)
+    return start_fp8_grad<Mul, G, 256, 2, 4>(groups, x, W, n, dX, ldx, 1, parts, s);
+  if (plan.tile == 128)
+    return start_fp8_grad<Mul, G, 128, 2, 2>(groups, x, W, n, dX, ldx, plan.splits, parts, s);
+  return start_fp8_grad<Mul, G, 64, 2, 2>(groups, x, W, n, dX, ldx, plan.splits, parts, s);
 }
 
 #define BK_INST(X)                                                                               \

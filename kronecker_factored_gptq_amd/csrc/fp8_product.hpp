@@ -19,8 +19,8 @@ constexpr int kBlock = 128;  // k (and rows of weights) under one scale
 // 32 k does the same at half the rate). Sums of Gaussian codes are off by 1.5e-5 in the
 // 2-norm, a sixteenth of a float16's rounding and less of a bfloat16's.
 struct MulFP8 {
-  typedef f32x4 acc_t;
-  static constexpr int kElem = 1;
+  static constexpr bool kTransposed = false;
+  static constexpr int kPlanes = 1;
   __device__ static inline f32x4 block(v4i a0, v4i a1, v4i b0, v4i b1) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
         __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7),
@@ -39,9 +39,17 @@ __device__ inline v8h fp8_to_f16(int lo, int hi) {
   const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
   return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
+__device__ inline v8bf fp8_to_bf16(int lo, int hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
 struct MulFP8Exact {
-  typedef f32x4 acc_t;
-  static constexpr int kElem = 1;
+  static constexpr bool kTransposed = false;
+  static constexpr int kPlanes = 1;
   __device__ static inline f32x4 block(v4i a0, v4i a1, v4i b0, v4i b1) {
     f32x4 c = {0, 0, 0, 0};
 #pragma unroll
@@ -53,6 +61,27 @@ struct MulFP8Exact {
       c = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp8_to_f16(a1[i], a1[i + 1]),
                                                  fp8_to_f16(b1[i], b1[i + 1]), c, 0, 0, 0);
     return c;
+  }
+};
+
+// e4m3 codes, made 16-bit where they are used, times 16-bit values: 64 k, eight neighbouring
+// ones to a lane and instruction. Exact in either type (e4m3 has 4 bits, and its exponents lie
+// in both types' normal range). PLANES: of the values (three bfloat16 hold a float32).
+template <class M, int PLANES>
+struct MulWide {
+  static constexpr bool kTransposed = true;
+  static constexpr int kPlanes = PLANES;
+  __device__ static inline void widen(v4i codes, v4i& a, v4i& b) {
+    if (std::is_same<M, MmaF16>::value) {
+      a = __builtin_bit_cast(v4i, fp8_to_f16(codes[0], codes[1]));
+      b = __builtin_bit_cast(v4i, fp8_to_f16(codes[2], codes[3]));
+    } else {
+      a = __builtin_bit_cast(v4i, fp8_to_bf16(codes[0], codes[1]));
+      b = __builtin_bit_cast(v4i, fp8_to_bf16(codes[2], codes[3]));
+    }
+  }
+  __device__ static inline f32x4 block(v4i a0, v4i a1, v4i b0, v4i b1) {
+    return M::mma(a1, b1, M::mma(a0, b0, f32x4{0, 0, 0, 0}));
   }
 };
 

@@ -334,6 +334,33 @@ def test_grad_strides(gpu_lib, pad, first, t):
     buf = torch.full((70, 311), 7.0, dtype=TYPES[t], device="cuda")
     check_grad(gpu_lib, G[:, 5:185], wb, 300, scales(2, 3, g), out=buf[:, 3:303])
     assert (buf[:, :3] == 7).all() and (buf[:, 303:] == 7).all()
+    # rows of whole groups of 16 that do not start on 16 bytes, of the codes, of G, of both
+    wb, sw = codes(184, 304 + 7, g, False), scales(2, 3, g)
+    for a, b in ((0, 0), (0, 7), (3, 0), (3, 7)):
+        W, H = torch.empty(184, 320 + 7, dtype=torch.uint8), torch.empty(70, 192 + 3, dtype=TYPES[t])
+        W[:, b:b + 304], H[:, a:a + 184] = wb[:, :304], G[:, 1:185]
+        W, H = W.cuda()[:, b:b + 304].view(F8), H.cuda()[:, a:a + 184]
+        D = gpu_lib.matmul_fp8_grad(H, W, sw.cuda())
+        E = gpu_lib.matmul_fp8_grad(H.contiguous(), W.contiguous(), sw.cuda())
+        V = values(wb, 304) * spread(sw, 128, 184, 304).double()
+        ref, S = G[:, 1:185].double() @ V, G[:, 1:185].double().abs() @ V.abs()
+        tol = S * (3 * 184 * 2.0 ** -23 + 3 * E32) + ref.abs() * half_step(TYPES[t]) * (1 + 2.0 ** -8) + smallest(TYPES[t])
+        assert ((D.cpu().double() - ref).abs() <= tol).all() and ((E.cpu().double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_grad_small_values(gpu_lib, t):
+    """Subnormal and small gradients count as they are."""
+    g = torch.Generator().manual_seed(2)
+    least = 2.0 ** -24 if t == "f16" else 2.0 ** -133
+    G = (torch.randint(-40, 41, (20, 256), generator=g) * least).to(TYPES[t])
+    wb = torch.full((256, 64), 0x78, dtype=torch.uint8)  # 256
+    wb[:, 1::2] = 0xf8
+    sw = torch.full((2, 1), 2.0 ** 16 if t == "f16" else 2.0 ** 100)
+    D = gpu_lib.matmul_fp8_grad(G.cuda(), wb.cuda().view(F8), sw.cuda()).cpu().double()
+    ref = G.double() @ (values(wb, 64) * sw[0, 0].double())
+    assert (ref != 0).any()
+    assert ((D - ref).abs() <= ref.abs() * half_step(TYPES[t])).all()  # sums of few whole multiples: exact
 
 
 @pytest.mark.parametrize("T,k,E,m,n", GROUPS)
