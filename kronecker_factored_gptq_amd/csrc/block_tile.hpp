@@ -41,6 +41,7 @@ struct BlockTile {
   static constexpr int kLoads = kStepUnits * LU + 1;          // a wave's loads to a step
   static constexpr int kAhead = T ? kLoads : LU;              // in flight at a step's barrier
   static constexpr int kEarly = kLoads / 3;                   // of them, those that go out first
+  static constexpr int kLate = T ? 3 : 2;                     // products between a product and its sums' addition
   static_assert(LU * 1024 * kWaves == kUnit && kWaves % 2 == 0, "a unit's bytes divide over the waves");
   static_assert(FR % NB == 0 && P < FR && P <= NB, "rows' fragments go round");
   static_assert(B / WR >= 32 && B / WR <= 128 && B / WC <= B / 2, "a wave's rows and columns lie in one unit");
@@ -119,9 +120,10 @@ struct BlockTile {
                    lds + j * kWaves * 1024);
     }
     __device__ inline void next() {
-      if (Mul::kPlanes > 1 && k == last) {
-        k = 0;
-        p += plane;
+      if (Mul::kPlanes > 1) {  // without a branch, which would split the order of instructions
+        const bool wrap = k == last;
+        k = wrap ? 0 : k + 1;
+        p += wrap ? plane : 0;
         rsrc = buffer(p, bytes);
       } else {
         ++k;
@@ -162,13 +164,9 @@ struct BlockTile {
                    lds + j * kWaves * 1024);
     }
     __device__ inline void next() {
-      if (Mul::kPlanes > 1 && k == last) {
-        k = 0;
-        p = first;
-      } else {
-        ++k;
-        p += stride;
-      }
+      const bool wrap = Mul::kPlanes > 1 && k == last;
+      k = wrap ? 0 : k + 1;
+      p = wrap ? first : p + stride;
       rsrc = buffer(p, bytes);
     }
   };
@@ -203,13 +201,9 @@ struct BlockTile {
     auto load_scale = [&]() {
       load_lds<4>(buffer(scale, 0x7fffffff), per, 0, smine + us * kScaleSlot);
       us = us == kScaleSlots - 1 ? 0 : us + 1;
-      if (Mul::kPlanes > 1 && ks == C.last) {
-        ks = 0;
-        scale = scale0;
-      } else {
-        ++ks;
-        if (kEach == 1 || ks % kEach == 0) scale += stride;
-      }
+      const bool wrap = Mul::kPlanes > 1 && ks == C.last;
+      ks = wrap ? 0 : ks + 1;
+      scale = wrap ? scale0 : scale + (ks % kEach == 0 ? stride : 0);
     };
     // The n-th load after a step's barrier. R's second half, C and the scales of the step
     // after the next, and R's first half of the one behind it; kTransposed: all of the third
@@ -275,8 +269,8 @@ struct BlockTile {
       pc = lds + b * kUnit + lc;
       ps = lds + kUnits * kUnit + sslot * kScaleSlot;
     };
-    v4i r[NB][T ? 1 : 2], c[FC][2], wide[T ? P : 1][2];
-    float sx[FC], sw, f[FC];
+    v4i r[NB][T ? 1 : 2], c[FC][2], wide[4][2];
+    float sx[FC], sw, f[FC], old[kLate];
     auto read_r = [&](int i, int h) {
       if constexpr (T) {
         // 32 k further on swap_at is the same, and so it is in the rows of one wave, whose first
@@ -290,9 +284,10 @@ struct BlockTile {
         r[i % NB][h] = *(const v4i*)(pr + i * 16 * kStepBytes + at[h]);
       }
     };
-    // row i made 16-bit, in place x
-    auto widen = [&](int i, int x) {
-      if constexpr (T) Mul::widen(r[i % NB][0], wide[x][0], wide[x][1]);
+    // Row i made 16-bit: rows before the barrier in two places in turn, those after it in two others.
+    auto place = [](int i) { return i < FR - P ? i % 2 : 2 + i - (FR - P); };
+    auto widen = [&](int i) {
+      if constexpr (T) Mul::widen(r[i % NB][0], wide[place(i)][0], wide[place(i)][1]);
     };
     auto read_c = [&](int j, int h) { c[j][h] = *(const v4i*)(pc + j * 16 * kStepBytes + at[h]); };
     auto read_s = [&](int j) {
@@ -301,33 +296,38 @@ struct BlockTile {
       else if (!T)
         sx[j] = *(const float*)(ps + (w % WC * FC * 16 + j * 16 + r16) * 4);
     };
-    // Instruction n of a step is of row_of(n) and column_of(n): the first rows row by row, the
-    // others column by column. Its sums are added when two more have been started.
+    // Product n of a step is of row_of(n) and column_of(n): the first rows row by row, the
+    // others column by column. kTransposed ones are two instructions, the second of them issued after the
+    // next product's first, since it waits for its own first. Sums are added kLate products
+    // later, those of a step's last ones in the next step, with the scales that were theirs.
     constexpr int kFirst = (FR - P) * FC, kAll = FR * FC;
     auto row_of = [](int n) { return n < kFirst ? n / FC : FR - P + (n - kFirst) % P; };
     auto column_of = [](int n) { return n < kFirst ? n % FC : (n - kFirst) / P; };
-    f32x4 part[3];
-    auto add = [&](int n) {
+    f32x4 part[4];
+    static_assert(kAll % 4 == 0 && kLate <= 3, "sums that wait are not overwritten");
+    auto add = [&](int n, float by) {
       const int i = row_of(n), j = column_of(n);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        acc[i][j][e] = __builtin_fmaf(part[n % 3][e], T ? f[0] : f[j], acc[i][j][e]);
+        acc[i][j][e] = __builtin_fmaf(part[n % 4][e], by, acc[i][j][e]);
+    };
+    auto finish = [&](int n) {
+      const int x = place(row_of(n)), j = column_of(n);
+      if constexpr (T) part[n % 4] = Mul::second(wide[x][1], c[j][1], part[n % 4]);
     };
     auto multiply = [&](int n) {
       const int i = row_of(n), j = column_of(n);
-      if constexpr (T) {
-        const int x = n < kFirst ? 0 : i - (FR - P);
-        if (j == 0) widen(i, x);
-        part[n % 3] = Mul::block(wide[x][0], wide[x][1], c[j][0], c[j][1]);
-      } else {
-        part[n % 3] = Mul::block(r[i % NB][0], r[i % NB][1], c[j][0], c[j][1]);
-      }
-      if (n >= 2) add(n - 2);
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (T)
+        part[n % 4] = Mul::first(wide[place(i)][0], c[j][0]);
+      else
+        part[n % 4] = Mul::block(r[i % NB][0], r[i % NB][1], c[j][0], c[j][1]);
+      if (n >= 1) finish(n - 1);
+      if (n >= kLate) add(n - kLate, T ? f[0] : f[column_of(n - kLate)]);
     };
-    // the rows before the barrier; rows up to i + NB - 1 are read by the end of row i
-    auto first_rows = [&](auto loads) {
-      constexpr bool LOADS = decltype(loads)::value;
+    // the rows before the barrier; rows up to i + NB - 1 are read by the end of row i, and widened in
+    // the row before their own
+    auto first_rows = [&](auto loads, auto later) {
+      constexpr bool LOADS = decltype(loads)::value, LATER = decltype(later)::value;
       constexpr int kRest = kLoads - kEarly, kEvery = kFirst / kRest > 0 ? kFirst / kRest : 1;
 #pragma unroll
       for (int j = 0; j < FC; ++j) f[j] = T ? sw : sx[j] * sw;
@@ -339,6 +339,14 @@ struct BlockTile {
         for (int x = j; x < 2 * (want - have); x += FC) read_r(have + x / 2, x & 1);
         if (LOADS && n % kEvery == 0 && n / kEvery < kRest) load_n(kEarly + n / kEvery);
         multiply(n);
+        if (LATER && n < kLate) add(kAll - kLate + n, old[n]);
+        if (T && j == FC / 2 && i + 1 <= FR - P) widen(i + 1);
+        if (T && j == FC - 1 && i == FR - P - 1 && P == 2) widen(FR - 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (LATER) {
+#pragma unroll
+        for (int n = kFirst; n < kLate; ++n) add(kAll - kLate + n, old[n]);
       }
       if (LOADS) {
 #pragma unroll
@@ -359,17 +367,29 @@ struct BlockTile {
       for (int n = kFirst; n < kAll; ++n) {
         if (LOADS && n - kFirst < kEarly) load_n(n - kFirst);
         multiply(n);
+        // a column's last product: its first half may be read anew, its second one product later
+        // if that is still to be multiplied
         if (NEXT && (n - kFirst) % P == P - 1) {
           read_c(column_of(n), 0);
-          read_c(column_of(n), 1);
+          if (!T) read_c(column_of(n), 1);
         }
+        if (T && NEXT && n > kFirst && (n - 1 - kFirst) % P == P - 1) read_c(column_of(n - 1), 1);
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (LOADS) {
 #pragma unroll
         for (int x = kAll - kFirst; x < kEarly; ++x) load_n(x);
       }
-      add(kAll - 2);
-      add(kAll - 1);
+      finish(kAll - 1);
+      if (NEXT) {
+        if (T) read_c(FC - 1, 1);
+        widen(0);
+#pragma unroll
+        for (int x = 0; x < kLate; ++x) old[x] = T ? f[0] : f[column_of(kAll - kLate + x)];
+      } else {
+#pragma unroll
+        for (int n = kAll - kLate; n < kAll; ++n) add(n, T ? f[0] : f[column_of(n)]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     };
     const std::true_type yes;
@@ -384,18 +404,19 @@ struct BlockTile {
     }
 #pragma unroll
     for (int j = 0; j <= FC; ++j) read_s(j);
+    widen(0);
     auto advance = [&]() {
       step = step + kStepUnits >= kUnits ? step + kStepUnits - kUnits : step + kStepUnits;
       sslot = sslot == kScaleSlots - 1 ? 0 : sslot + 1;
       point();
     };
-    first_rows(no);
+    first_rows(no, no);
     int s = 0;
     for (; s + 3 < total; ++s) {
       wait_barrier<kAhead>();
       advance();
       last_rows(yes, yes);
-      first_rows(yes);
+      first_rows(yes, yes);
     }
     for (; s + 1 < total; ++s) {
       if (s + 2 < total)
@@ -405,7 +426,7 @@ struct BlockTile {
       advance();
       if (!T && s + 2 < total) load_step(false);
       last_rows(no, yes);
-      first_rows(no);
+      first_rows(no, yes);
     }
     last_rows(no, no);
   }
@@ -488,7 +509,7 @@ struct BlockTile {
               codes[e / 4] |= (int)*(const unsigned char*)(lr + k * B + at * 16 + r16) << (8 * (e % 4));
             }
             v4i none;
-            Mul::widen(codes, x[h], none);
+            Mul::widen(codes, x[h], none);  // the first 8 k of the two
           } else {
             x[h] = *(const v4i*)(lr + (wr + i * 16 + r16) * kStepBytes + chunk_at(r16, h * 4 + q) * 16);
           }

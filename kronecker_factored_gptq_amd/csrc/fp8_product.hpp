@@ -80,8 +80,10 @@ struct MulWide {
       b = __builtin_bit_cast(v4i, fp8_to_bf16(codes[2], codes[3]));
     }
   }
+  __device__ static inline f32x4 first(v4i a, v4i b) { return M::mma(a, b, f32x4{0, 0, 0, 0}); }
+  __device__ static inline f32x4 second(v4i a, v4i b, f32x4 c) { return M::mma(a, b, c); }
   __device__ static inline f32x4 block(v4i a0, v4i a1, v4i b0, v4i b1) {
-    return M::mma(a1, b1, M::mma(a0, b0, f32x4{0, 0, 0, 0}));
+    return second(a1, b1, first(a0, b0));
   }
 };
 
