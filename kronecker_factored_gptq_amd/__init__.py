@@ -1016,17 +1016,13 @@ def quantize_fp8(X: torch.Tensor, block_rows: int = 1):
     if block_rows not in (1, _BLOCK):
         raise ValueError(f"block_rows must be 1 or {_BLOCK}, got {block_rows}")
     batch, rows, n, ldx, sX = _matrices(X, "X")
-    ldq, nb, na = (n + 15) // 16 * 16, -(-n // _BLOCK), -(-rows // block_rows)
-    lead = X.shape[:-2]
+    ldq, nb, na = (n + 15) // 16 * 16, (n + 127) // 128, (rows + block_rows - 1) // block_rows
+    lead, steps = ((), ()) if len(X.shape) == 2 else ((batch,), (na * nb,))
     Xq = torch.empty((*lead, rows, ldq), dtype=E4M3, device=dev)
     if ldq != n:
         Xq = Xq[..., :n]
-    if block_rows == 1:
-        s = torch.empty((*lead, nb, na), dtype=torch.float32, device=dev).transpose(-1, -2)
-        srow, sblock = 1, na
-    else:
-        s = torch.empty((*lead, na, nb), dtype=torch.float32, device=dev)
-        srow, sblock = nb, 1
+    srow, sblock = (1, na) if block_rows == 1 else (nb, 1)
+    s = torch.empty_strided((*lead, na, nb), (*steps, srow, sblock), dtype=torch.float32, device=dev)
     _call("bakron_quantize_fp8", dev, lib().bakron_quantize_fp8, code, batch, rows, n, X.data_ptr(), ldx, sX,
           block_rows, Xq.data_ptr(), ldq, rows * ldq, s.data_ptr(), srow, sblock, na * nb)
     return Xq, s
@@ -1035,31 +1031,31 @@ def quantize_fp8(X: torch.Tensor, block_rows: int = 1):
 def _matrices(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None):
     """(batch, rows, columns, leading dimension, stride) of a row-major matrix, or of a
     batch of them (3-D) any distance apart."""
-    if t.dim() != 3:
-        rows, cols, ld = _matrix(t, name, dtype)
-        return 1, rows, cols, ld, 0
-    if t.size(0) == 0:
+    shape = t.shape
+    if len(shape) != 3:
+        return 1, *_matrix(t, name, dtype), 0
+    batch = shape[0]
+    if batch == 0:
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        return 0, t.size(1), t.size(2), max(t.size(2), 1), 0
-    rows, cols, ld = _matrix(t[0], name, dtype)
-    return t.size(0), rows, cols, ld, t.stride(0) if t.size(0) > 1 else 0
+        return 0, shape[1], shape[2], max(shape[2], 1), 0
+    return batch, *_matrix(t[0], name, dtype), t.stride(0) if batch > 1 else 0
 
 
 def _fp8_weights(Wq: torch.Tensor, sw: torch.Tensor, offsets: Optional[torch.Tensor]):
-    """(experts, m, n, Wq, ldw, stride, sw, ldsw, stride, offsets): a layer's codes
-    and scales, or those of each expert with the offsets of their rows."""
-    experts, m, n, ldw, stride = _matrices(Wq, "Wq", E4M3)
-    if (Wq.dim() == 3) != (offsets is not None):
+    """(m, n, blocks of n, (Wq, ldw, stride, sw, ldsw, stride), experts, offsets): a layer's
+    codes and scales, or those of each expert with the offsets of their rows."""
+    if (len(Wq.shape) == 3) != (offsets is not None):
         raise ValueError("Wq is experts x m x n with offsets, and m x n without")
+    experts, m, n, ldw, stride = _matrices(Wq, "Wq", E4M3)
     if experts < 1:
         raise ValueError("Wq must have an expert")
-    want = (*Wq.shape[:-2], -(-m // _BLOCK), -(-n // _BLOCK))
-    if sw.shape != want:
-        raise ValueError(f"sw must have shape {want}, got {tuple(sw.shape)}")
-    _, _, _, ldsw, stride_s = _matrices(sw, "sw", torch.float32)
-    return (experts, m, n, Wq.data_ptr(), ldw, stride, sw.data_ptr(), ldsw, stride_s,
-            _vector(offsets, experts + 1, "offsets", torch.int32))
+    nb = (n + 127) // 128
+    es, mb, nbs, ldsw, stride_s = _matrices(sw, "sw", torch.float32)
+    if es != experts or nbs != nb or mb != (m + 127) // 128 or len(sw.shape) != len(Wq.shape):
+        raise ValueError(f"sw must have shape {(*Wq.shape[:-2], (m + 127) // 128, nb)}, got {tuple(sw.shape)}")
+    return (m, n, nb, (Wq.data_ptr(), ldw, stride, sw.data_ptr(), ldsw, stride_s), experts,
+            None if offsets is None else _vector(offsets, experts + 1, "offsets", torch.int32))
 
 
 def matmul_fp8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor,
@@ -1079,14 +1075,13 @@ def matmul_fp8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.T
     bfloat16 or float16), or ``out`` and its type. Asynchronous."""
     dev = _check_device(Xq, sx, Wq, sw, offsets, order, out, workspace)
     T, n, ldx = _matrix(Xq, "Xq", E4M3)
-    experts, m, nw, pw, ldw, stride, ps, ldsw, stride_s, po = _fp8_weights(Wq, sw, offsets)
+    m, nw, nb, weights, experts, po = _fp8_weights(Wq, sw, offsets)
     if nw != n:
         raise ValueError(f"Xq and Wq must have rows of one length, got {n} and {nw}")
     if sx.dtype != torch.float32:
         raise TypeError(f"sx must be torch.float32, got {sx.dtype}")
-    if sx.shape != (T, -(-n // _BLOCK)):
-        raise ValueError(f"sx must have shape {(T, -(-n // _BLOCK))}, got {tuple(sx.shape)}")
-    per_token = int(per_token)
+    if sx.shape != (T, nb):
+        raise ValueError(f"sx must have shape {(T, nb)}, got {tuple(sx.shape)}")
     if per_token < 1:
         raise ValueError("per_token must be positive")
     R, pr = T, None
@@ -1101,8 +1096,7 @@ def matmul_fp8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.T
     L = lib()
     ws, pws, nws = _scratch(L.bakron_matmul_fp8_workspace_bytes(code, T, R, experts, m, n), dev, workspace)
     _call("bakron_matmul_fp8", dev, L.bakron_matmul_fp8, code, T, R, experts, m, n, Xq.data_ptr(), ldx,
-          sx.data_ptr(), *sx.stride(), pw, ldw, stride, ps, ldsw, stride_s, po, pr, per_token, out.data_ptr(), ldy,
-          pws, nws)
+          sx.data_ptr(), *sx.stride(), *weights, po, pr, per_token, out.data_ptr(), ldy, pws, nws)
     return out
 
 
@@ -1117,14 +1111,14 @@ def matmul_fp8_grad(G: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor, offsets
     dev = _check_device(G, Wq, sw, offsets, workspace, out)
     code = _ft(G.dtype, "G")
     R, m, ldg = _matrix(G, "G")
-    experts, mw, n, pw, ldw, stride, ps, ldsw, stride_s, po = _fp8_weights(Wq, sw, offsets)
+    mw, n, _, weights, experts, po = _fp8_weights(Wq, sw, offsets)
     if mw != m:
         raise ValueError(f"G must have a column for each row of Wq, got {m} and {mw}")
     out, ldx = _output(out, R, n, G.dtype, "out", dev)
     L = lib()
     ws, pws, nws = _scratch(L.bakron_matmul_fp8_grad_workspace_bytes(code, R, experts, m, n), dev, workspace)
-    _call("bakron_matmul_fp8_grad", dev, L.bakron_matmul_fp8_grad, code, R, experts, m, n, G.data_ptr(), ldg, pw, ldw,
-          stride, ps, ldsw, stride_s, po, out.data_ptr(), ldx, pws, nws)
+    _call("bakron_matmul_fp8_grad", dev, L.bakron_matmul_fp8_grad, code, R, experts, m, n, G.data_ptr(), ldg, *weights,
+          po, out.data_ptr(), ldx, pws, nws)
     return out
 
 
@@ -1161,7 +1155,7 @@ def gather_tokens(X: torch.Tensor, order: torch.Tensor, per_token: int = 1,
     T, n, ldx = _matrix(X, "X")
     if order.dim() != 1:
         raise ValueError("order must be a vector")
-    R, per_token = order.size(0), int(per_token)
+    R = order.size(0)
     if per_token < 1:
         raise ValueError("per_token must be positive")
     po = _vector(order, R, "order", torch.int32)

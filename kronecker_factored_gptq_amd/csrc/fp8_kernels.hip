@@ -12,18 +12,62 @@ namespace bk {
 // all-zero block; code = x / s rounded to nearest even, the division correctly
 // rounded. The maximum is taken over the bits of |x|, in which a NaN is larger than
 // infinity: a block with either gets it as its scale.
+//
+// Bound by memory once a division is not the ten instructions of a general one: with r =
+// 1 / s correctly rounded, q = x r is within two units of x / s in the last place, q + r (x - q s)
+// within one, and the same once more is x / s correctly rounded (Markstein: a faithful quotient
+// and a correctly rounded reciprocal give it), the remainders being exact. They are while s >=
+// 2^-92: quotients below 2^-11 give the code 0 whatever their last bits, and above it q s
+// has no bit below 2^-57 s >= 2^-149. Other scales, those that are not finite among them, divide.
 // ---------------------------------------------------------------------------
-__device__ inline float block_scale(unsigned top) {
-  if (top == 0) return 1.0f;
-  const float s = __uint_as_float(top) / 448.0f;
-  return s < 0x1p-126f ? 0x1p-126f : s;
-}
+struct BlockScale {
+  float s, r;
+  bool fast;
+  __device__ inline BlockScale(float top) {
+    s = top / 448.0f;
+    s = top == 0.0f ? 1.0f : s < 0x1p-126f ? 0x1p-126f : s;
+    fast = s >= 0x1p-92f && s <= 0x1p126f;
+    r = 1.0f / s;
+  }
+  __device__ inline float over(float x) const {
+    const float q = x * r, u = __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+    return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-u, s, x), r, u), x);  // -0 stays -0
+  }
+  // four codes
+  __device__ inline int codes(const float* x) const {
+    float v[4];
+    if (fast) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = over(x[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = x[e] / s;
+    }
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    return __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+  }
+};
+// The largest |x| of eight elements, as float32 bits (16-bit ones two at a time).
 template <typename X> __device__ inline unsigned top8(const Eight<X>& t) {
   unsigned top = 0;
+  if constexpr (sizeof(X) == 4) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const unsigned a = __float_as_uint(to_f32(t.v[e])) & 0x7fffffffu;
-    top = a > top ? a : top;
+    for (int e = 0; e < 8; ++e) {
+      const unsigned a = __float_as_uint(to_f32(t.v[e])) & 0x7fffffffu;
+      top = a > top ? a : top;
+    }
+  } else {
+    typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+    unsigned w[4];
+    __builtin_memcpy(w, t.v, 16);
+    v2us m = __builtin_bit_cast(v2us, w[0] & 0x7fff7fffu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(v2us, w[i] & 0x7fff7fffu));
+    const unsigned short h = m[0] > m[1] ? m[0] : m[1];
+    X x;
+    __builtin_memcpy(&x, &h, 2);
+    top = __float_as_uint(to_f32(x));
   }
   return top;
 }
@@ -35,18 +79,38 @@ __device__ inline unsigned max_of_16(unsigned top) {
   }
   return top;
 }
-// eight codes of a row from column c on
-template <typename X>
-__device__ inline void store_codes(char* row, int64_t c, int64_t n, const Eight<X>& t, float s,
-                                   bool vec) {
-  int w[2];
+// The 128 columns of a block from c on, eight to each of 16 lanes: side by side where rows are
+// aligned to them (VEC), else 16 apart, so that a load of all lanes is still one piece of the row
+// (eight loads side by side a lane: 4003 x 11009 float32 90 us).
+template <typename X, bool VEC>
+__device__ inline Eight<X> load_block(const X* row, int64_t c, int64_t n, int l) {
+  if (VEC) return load8(row, c + 8 * l, n, true);
+  Eight<X> t;
+  __builtin_memset(&t, 0, sizeof t);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float a = to_f32(t.v[4 * i]) / s, b = to_f32(t.v[4 * i + 1]) / s;
-    const float d = to_f32(t.v[4 * i + 2]) / s, e = to_f32(t.v[4 * i + 3]) / s;
-    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(d, e, w[i], true);
+  for (int e = 0; e < 8; ++e)
+    if (c + 16 * e + l < n) t.v[e] = row[c + 16 * e + l];
+  return t;
+}
+// Their codes; without VEC they change lanes through LDS (`swap`: the 16 lanes' 128 bytes, in
+// one wave: no barrier), so that stores are of eight neighbouring codes all the same.
+template <typename X, bool VEC>
+__device__ inline void store_block(char* row, int64_t c, int64_t n, const Eight<X>& t, int l,
+                                   const BlockScale& f, bool vec, char* swap) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = to_f32(t.v[e]);
+  int w[2] = {f.codes(v), f.codes(v + 4)};
+  if (!VEC) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) swap[16 * e + l] = (char)(w[e / 4] >> 8 * (e % 4));
+    __builtin_amdgcn_wave_barrier();
+    const int2 x = *(const int2*)(swap + 8 * l);
+    __builtin_amdgcn_wave_barrier();
+    w[0] = x.x;
+    w[1] = x.y;
   }
+  c += 8 * l;
   if (vec && c + 8 <= n) {
     *(int2*)(row + c) = int2{w[0], w[1]};
   } else {
@@ -58,13 +122,14 @@ __device__ inline void store_codes(char* row, int64_t c, int64_t n, const Eight<
 
 // Blocks of 1 x 128: 16 lanes to kRun neighbouring blocks of a row, neighbouring groups of
 // lanes on neighbouring rows, so that their scales are stored side by side where the
-// scales' rows are. Bound by memory.
+// scales' rows are.
 constexpr int kRun = 4;
-template <typename X>
+template <typename X, bool VEC>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(
     int64_t rows, int64_t n, int64_t runs, const X* __restrict__ x, int64_t ldx, int64_t sX,
     char* __restrict__ q, int64_t ldq, int64_t sQ, float* __restrict__ s, int64_t srow,
-    int64_t sblock, int64_t sS, bool vec, bool vecq) {
+    int64_t sblock, int64_t sS, bool vecq) {
+  __shared__ __attribute__((aligned(16))) char swap[VEC ? 16 : 16 * kBlock];
   const int64_t at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   if (at >= rows * runs) return;  // whole groups of 16 lanes
   const int l = threadIdx.x & 15;
@@ -74,26 +139,27 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(
   s += blockIdx.y * sS + r * srow;
   Eight<X> t[kRun];
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) t[i] = load8(x, (run * kRun + i) * kBlock + 8 * l, n, vec);
+  for (int i = 0; i < kRun; ++i) t[i] = load_block<X, VEC>(x, (run * kRun + i) * kBlock, n, l);
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
     const int64_t b = run * kRun + i;
     if (b * kBlock >= n) break;
-    const float f = block_scale(max_of_16(top8(t[i])));
-    if (l == 0) s[b * sblock] = f;
-    store_codes(q, b * kBlock + 8 * l, n, t[i], f, vecq);
+    const BlockScale f(__uint_as_float(max_of_16(top8(t[i]))));
+    if (l == 0) s[b * sblock] = f.s;
+    store_block<X, VEC>(q, b * kBlock, n, t[i], l, f, vecq, swap + (VEC ? 0 : (threadIdx.x >> 4) * kBlock));
   }
 }
 
 // Blocks of 128 x 128, a workgroup each, held in registers between the maximum and the codes.
-template <typename X>
+template <typename X, bool VEC>
 __global__ __launch_bounds__(256) void quantize_blocks_kernel(
     int64_t rows, int64_t n, unsigned across, const X* __restrict__ x, int64_t ldx, int64_t sX,
     char* __restrict__ q, int64_t ldq, int64_t sQ, float* __restrict__ s, int64_t srow,
-    int64_t sblock, int64_t sS, bool vec, bool vecq) {
+    int64_t sblock, int64_t sS, bool vecq) {
   __shared__ unsigned red[4];
+  __shared__ __attribute__((aligned(16))) char swap[VEC ? 16 : 16 * kBlock];
   const int64_t a = blockIdx.x / across, b = blockIdx.x - a * across;
-  const int64_t c = b * kBlock + 8 * (threadIdx.x & 15);
+  const int l = threadIdx.x & 15;
   x += blockIdx.y * sX;
   q += blockIdx.y * sQ;
   Eight<X> t[8];
@@ -101,19 +167,21 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = a * kBlock + 16 * i + (threadIdx.x >> 4);
-    t[i] = load8(x + (r < rows ? r : rows - 1) * ldx, c, n, vec);
+    t[i] = load_block<X, VEC>(x + (r < rows ? r : rows - 1) * ldx, b * kBlock, n, l);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const unsigned u = top8(t[i]);  // rows past the last count as it, columns past n as zero
     top = u > top ? u : top;
   }
-  const float f = block_scale(max_of_256(top, red));
-  if (threadIdx.x == 0) s[blockIdx.y * sS + a * srow + b * sblock] = f;
+  const BlockScale f(__uint_as_float(max_of_256(top, red)));
+  if (threadIdx.x == 0) s[blockIdx.y * sS + a * srow + b * sblock] = f.s;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = a * kBlock + 16 * i + (threadIdx.x >> 4);
-    if (r < rows) store_codes(q + r * ldq, c, n, t[i], f, vecq);
+    if (r < rows)
+      store_block<X, VEC>(q + r * ldq, b * kBlock, n, t[i], l, f, vecq,
+                          swap + (VEC ? 0 : (threadIdx.x >> 4) * kBlock));
   }
 }
 
@@ -125,17 +193,22 @@ hipError_t launch_quantize_fp8(int64_t batch, int64_t rows, int64_t n, const X* 
   if (batch <= 0 || rows <= 0 || n <= 0) return hipSuccess;
   const bool vec = load8_ok(x, ldx) && load8_ok(x, sX), vecq = ((uintptr_t)q | ldq | sQ) % 8 == 0;
   const int64_t nb = (n + kBlock - 1) / kBlock;
+#define BK_QUANTIZE(KERNEL, GROUPS, COUNT)                                                        \
+  if (vec)                                                                                        \
+    hipLaunchKernelGGL((KERNEL<X, true>), dim3((unsigned)(GROUPS), (unsigned)batch), dim3(256), 0, \
+                       st, rows, n, COUNT, x, ldx, sX, (char*)q, ldq, sQ, s, srow, sblock, sS,    \
+                       vecq);                                                                     \
+  else                                                                                            \
+    hipLaunchKernelGGL((KERNEL<X, false>), dim3((unsigned)(GROUPS), (unsigned)batch), dim3(256),  \
+                       0, st, rows, n, COUNT, x, ldx, sX, (char*)q, ldq, sQ, s, srow, sblock, sS, \
+                       vecq)
   if (block_rows == 1) {
     const int64_t runs = (nb + kRun - 1) / kRun;
-    hipLaunchKernelGGL(quantize_rows_kernel<X>,
-                       dim3((unsigned)((rows * runs + 15) / 16), (unsigned)batch), dim3(256), 0, st,
-                       rows, n, runs, x, ldx, sX, (char*)q, ldq, sQ, s, srow, sblock, sS, vec, vecq);
+    BK_QUANTIZE(quantize_rows_kernel, (rows * runs + 15) / 16, runs);
   } else {
-    const int64_t na = (rows + kBlock - 1) / kBlock;
-    hipLaunchKernelGGL(quantize_blocks_kernel<X>, dim3((unsigned)(na * nb), (unsigned)batch),
-                       dim3(256), 0, st, rows, n, (unsigned)nb, x, ldx, sX, (char*)q, ldq, sQ, s,
-                       srow, sblock, sS, vec, vecq);
+    BK_QUANTIZE(quantize_blocks_kernel, (rows + kBlock - 1) / kBlock * nb, (unsigned)nb);
   }
+#undef BK_QUANTIZE
   return hipGetLastError();
 }
 

@@ -53,6 +53,29 @@ def quantized(X, rows):
     return q.to(F8).view(torch.uint8), s
 
 
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantize_any_scale(gpu_lib, rows):
+    """Blocks of every size from the smallest to the largest floats, with quotients at, and one step to
+    either side of, the middle between two codes."""
+    g = torch.Generator().manual_seed(7)
+    n = 128 * 254
+    e = torch.arange(254).repeat_interleave(128)
+    X = torch.ldexp(torch.rand(256, n, generator=g) + 1, (e - 126).expand(256, n).to(torch.int32))
+    X = X * torch.where(torch.rand(256, n, generator=g) < 0.5, -1.0, 1.0) * torch.rand(256, n, generator=g)
+    top = torch.zeros(256, 254)
+    top[:] = X.view(256, 254, 128).abs().amax(2) if rows == 1 else X.view(2, 128, 254, 128).abs().amax((1, 3)).repeat_interleave(128, 0)
+    s = torch.where(top == 0, torch.ones(()), (top / torch.full((), 448.0)).clamp(min=2.0 ** -126)).repeat_interleave(128, 1)
+    # middles: 1 + 1/16 and so on, times the scale, and its neighbours
+    mid = torch.ldexp(1 + (2 * torch.randint(0, 8, (256, n), generator=g) + 1) / 16.0, torch.randint(-9, 8, (256, n), generator=g, dtype=torch.int32)) * s
+    step = torch.randint(-2, 3, (256, n), generator=g).to(torch.int32)
+    near = (mid.view(torch.int32) + step).view(torch.float32)
+    X = torch.where((torch.rand(256, n, generator=g) < 0.7) & (near < top.repeat_interleave(128, 1)), near, X)
+    q, sc = gpu_lib.quantize_fp8(X.cuda(), rows)
+    qr, sr = quantized(X, rows)
+    assert torch.equal(sc.cpu(), sr)
+    assert torch.equal(q.cpu().contiguous().view(torch.uint8), qr)
+
+
 @pytest.mark.parametrize("a,n", [(1, 1), (1, 4096), (3, 17), (37, 1000), (5, 4099), (130, 256), (129, 385), (2, 20011),
                                  (256, 640), (300, 129)])
 @pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
@@ -79,6 +102,9 @@ def test_quantize_edge_values(gpu_lib):
     q, s = bk.quantize_fp8(X.cuda())
     assert s.item() == 1.0
     assert q.float().cpu().tolist() == [[448.0, 16.0, 20.0, 18.0, -20.0, 2.0 ** -9, 0.0, 2.0 ** -8, 0.0, 0.0, 1.0]]
+    X = torch.tensor([[0.0, -0.0, -1e-9, 1.0], [-0.0, -0.0, 0.0, -0.0]])  # the sign of zero, as the division's
+    q, s = bk.quantize_fp8(X.cuda())
+    assert q.cpu().view(torch.uint8).tolist() == [[0, 128, 128, 126], [128, 128, 0, 128]] and s[1].item() == 1.0
     X = torch.tensor([[1e-44, -1e-42, 3e-43, 0.0], [1e-38, -5e-39, 2e-40, 1e-45], [3.4e38, -1e38, 1.0, 0.0],
                       [6e-36, 5e-37, 0.0, -1e-45]])
     for rows in (1, 128):
