@@ -63,10 +63,16 @@ __global__ __launch_bounds__(kSortThreads) void place_routes_kernel(
   for (int e = tid; e < B; e += kSortThreads) {
     int before = 0, all = 0;
     if (gridDim.x > 1)
-      for (unsigned c = 0; c < gridDim.x; ++c) {
-        const int n = counts[c * (int64_t)B + e];
-        all += n;
-        before += c < blockIdx.x ? n : 0;
+      for (unsigned c0 = 0; c0 < gridDim.x; c0 += 16) {  // 16 loads on their way at once
+        int n[16];
+#pragma unroll
+        for (unsigned i = 0; i < 16; ++i)
+          n[i] = c0 + i < gridDim.x ? counts[(c0 + i) * (int64_t)B + e] : 0;
+#pragma unroll
+        for (unsigned i = 0; i < 16; ++i) {
+          all += n[i];
+          before += c0 + i < blockIdx.x ? n[i] : 0;
+        }
       }
     for (int w = 0; w < kSortWaves; ++w) {
       const int n = at[w * B + e];

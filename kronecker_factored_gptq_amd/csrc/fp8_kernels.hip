@@ -120,9 +120,9 @@ __device__ inline void store_block(char* row, int64_t c, int64_t n, const Eight<
   }
 }
 
-// Blocks of 1 x 128: 16 lanes to kRun neighbouring blocks of a row, neighbouring groups of
-// lanes on neighbouring rows, so that their scales are stored side by side where the
-// scales' rows are.
+// Blocks of 1 x 128: 16 lanes to kRun neighbouring blocks of a row, a workgroup to 16 rows, so that
+// their scales are stored side by side where the scales' rows are, and neighbouring workgroups
+// along the rows (8192 x 14336 bfloat16 71.6 us, 4.9 TB/s; rows first 80, a workgroup along one row 76).
 constexpr int kRun = 4;
 template <typename X, bool VEC>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(
@@ -130,10 +130,10 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(
     char* __restrict__ q, int64_t ldq, int64_t sQ, float* __restrict__ s, int64_t srow,
     int64_t sblock, int64_t sS, bool vecq) {
   __shared__ __attribute__((aligned(16))) char swap[VEC ? 16 : 16 * kBlock];
-  const int64_t at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  if (at >= rows * runs) return;  // whole groups of 16 lanes
+  const int64_t band = blockIdx.x / runs, run = blockIdx.x - band * runs;
+  const int64_t r = band * 16 + (threadIdx.x >> 4);
+  if (r >= rows) return;  // whole groups of 16 lanes
   const int l = threadIdx.x & 15;
-  const int64_t run = at / rows, r = at - run * rows;
   x += blockIdx.y * sX + r * ldx;
   q += blockIdx.y * sQ + r * ldq;
   s += blockIdx.y * sS + r * srow;
@@ -204,7 +204,7 @@ hipError_t launch_quantize_fp8(int64_t batch, int64_t rows, int64_t n, const X* 
                        vecq)
   if (block_rows == 1) {
     const int64_t runs = (nb + kRun - 1) / kRun;
-    BK_QUANTIZE(quantize_rows_kernel, (rows * runs + 15) / 16, runs);
+    BK_QUANTIZE(quantize_rows_kernel, (rows + 15) / 16 * runs, runs);
   } else {
     BK_QUANTIZE(quantize_blocks_kernel, (rows + kBlock - 1) / kBlock * nb, (unsigned)nb);
   }
