@@ -546,14 +546,30 @@ static hipError_t start_skinny_fp8(const Groups& groups, const Fp8Tokens& X, con
 static inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 static int64_t packed_ld(int64_t n) { return (n + kStepBytes - 1) / kStepBytes * kStepBytes; }
 static TilePlan fp8_plan(int es, int64_t R, int64_t m, int64_t n) {
-  TilePlan p = plan_tiles(m, R, (n + kStepBytes - 1) / kStepBytes, 1, false, true);
+  TilePlan p = plan_tiles(m, R, (n + kStepBytes - 1) / kStepBytes, 1, false, true,
+                          es == 4 ? &kCostsExact : &kCostsBlocks);
   if (es == 4 && p.tile == 256) p.tile = 128;
   return p;
 }
+// Of groups, whose sizes are not known here, `a` rows of the tiles' other operand and `steps`: tiles of
+// 64 below `few` rows each on average (64 experts of 2048 x 4096, us with 64 and 128: 8 rows each 129
+// and 136, 32 161 and 142, 128 233 and 179; 32 of 1024 x 2048: 64 rows 22 and 25, 128 33 and 28;
+// gradient of 32 of 4096 x 2048: 64 rows 108 and 112, 128 163 and 145), then 128 or 256 by the rounds of
+// tiles, half a round of them empty, if every group leaves half a tile empty; a round of 256 is
+// `ratio` as long as one of 128 and fills its ring for four steps more (64 experts, 128 and 256:
+// 192 rows 223 and 230, 256 271 and 239, 1024 824 and 748; 8 of 4096 x 1024, 1024 rows 83 and 90; gradient
+// 128 rows 145 and 227, 512 355 and 372).
+static TilePlan group_plan(int64_t R, int64_t experts, int64_t a, int64_t steps, int64_t few, double ratio) {
+  if (R < few * experts) return {64, 1};
+  auto time = [&](int64_t B, double at_once, double fill) {
+    const int64_t half = R / B + experts / 2;
+    const double tiles = (double)((a + B - 1) / B * (half > experts ? half : experts));
+    return (tiles / at_once + 0.5) * ((double)steps + fill);
+  };
+  return {time(256, 256, 6) * ratio < time(128, 512, 2) ? 256 : 128, 1};
+}
 static TilePlan fp8_plan(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool grouped) {
-  if (!grouped) return fp8_plan(es, R, m, n);
-  const int64_t each = R / experts;
-  return {each >= 128 ? (es == 4 || each < 256 ? 128 : 256) : 64, 1};
+  return grouped ? group_plan(R, experts, m, (n + 127) / 128, 32, es == 4 ? 1e9 : 1.39) : fp8_plan(es, R, m, n);
 }
 struct Fp8Offsets {
   size_t x, w, parts, total;
@@ -743,9 +759,8 @@ static hipError_t pack_rows(const char* p, int64_t ld, int64_t stride, int64_t p
 }
 
 static TilePlan fp8_grad_plan(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool grouped) {
-  if (!grouped) return plan_tiles(n, R, (m + 63) / 64, es == 4 ? 3 : 1, true, true);
-  const int64_t each = R / experts;
-  return {each >= 256 ? 256 : each >= 128 ? 128 : 64, 1};
+  return grouped ? group_plan(R, experts, n, (m + 63) / 64, 65, 1.61)
+                 : plan_tiles(n, R, (m + 63) / 64, es == 4 ? 3 : 1, false, true, &kCostsBlocks);
 }
 struct Fp8GradOffsets {
   size_t w, g, parts, total;

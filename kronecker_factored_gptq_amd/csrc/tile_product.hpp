@@ -668,6 +668,10 @@ struct PlanCosts {
 };
 constexpr PlanCosts kCostsOne = {{{0.15, 0.48, 0.61, 2.2}, {0.1, 0.26, 0.29, 1.5}}, 2.2, 0.02, 2.2};
 constexpr PlanCosts kCostsPairs = {{{0.28, 0.4, 0.5, 3}, {0.19, 0.175, 0.35, 1}}, 3, 0.02, 3.5};
+// Products with block scales (block_tile.hpp), fitted to 28 sizes of 1024 x 2048 to 14336 x 4096 with
+// 100 to 2048 rows: 8-bit and 16-bit instructions, and 8-bit codes on 16-bit ones.
+constexpr PlanCosts kCostsBlocks = {{{0.26, 0.47, 0.72, 3}, {0.15, 0.19, 0.5, 2.5}}, 6, 0.02, 4};
+constexpr PlanCosts kCostsExact = {{{0.4, 0.9, 1.2, 3}, {0.25, 0.36, 0.6, 2.5}}, 6, 0.02, 4};
 struct TilePlan {
   int tile, splits;
 };
@@ -690,8 +694,8 @@ inline bool plan_allowed(int64_t M, int64_t N, int64_t steps, int pairs, bool ma
 }
 // The estimate, for `steps` of all pairs; `joining`: the part of it that grows with n.
 inline double plan_us(int64_t M, int64_t N, int64_t steps, int pairs, bool kmajor, int tile, int64_t n,
-                      double* joining = nullptr) {
-  const PlanCosts& costs = pairs > 1 ? kCostsPairs : kCostsOne;
+                      double* joining = nullptr, const PlanCosts* own = nullptr) {
+  const PlanCosts& costs = own ? *own : pairs > 1 ? kCostsPairs : kCostsOne;
   const bool small = tile == 64;
   const TileCost& cost = costs.tile[small];
   const int64_t work = n * tiles_of(M, N, tile), slots = small ? 1024 : 512;
@@ -707,7 +711,7 @@ inline double plan_us(int64_t M, int64_t N, int64_t steps, int pairs, bool kmajo
 }
 // steps: of one pair.
 inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, int pairs, bool kmajor,
-                           bool may_split) {
+                           bool may_split, const PlanCosts* own = nullptr) {
   TilePlan best = {128, 1};
   if (M <= 0 || N <= 0) return best;
   const int64_t large = tiles_of(M, N, 256);
@@ -717,7 +721,7 @@ inline TilePlan plan_tiles(int64_t M, int64_t N, int64_t steps, int pairs, bool 
   for (int tile : {128, 64})
     for (int n = 1; plan_fits(M, N, steps, may_split, tile, n); n = plan_next(pairs, n)) {
       double joining;
-      const double t = plan_us(M, N, steps, pairs, kmajor, tile, n, &joining);
+      const double t = plan_us(M, N, steps, pairs, kmajor, tile, n, &joining, own);
       if (t < least) {
         least = t;
         best = {tile, n};
