@@ -1047,6 +1047,13 @@ def _fp8_weights(Wq: torch.Tensor, sw: torch.Tensor, offsets: Optional[torch.Ten
     codes and scales, or those of each expert with the offsets of their rows."""
     if (len(Wq.shape) == 3) != (offsets is not None):
         raise ValueError("Wq is experts x m x n with offsets, and m x n without")
+    if offsets is None:
+        m, n, ldw = _matrix(Wq, "Wq", E4M3)
+        mb, nbs, ldsw = _matrix(sw, "sw", torch.float32)
+        nb = (n + 127) // 128
+        if mb != (m + 127) // 128 or nbs != nb:
+            raise ValueError(f"sw must have shape {((m + 127) // 128, nb)}, got {tuple(sw.shape)}")
+        return m, n, nb, (Wq.data_ptr(), ldw, 0, sw.data_ptr(), ldsw, 0), 1, None
     experts, m, n, ldw, stride = _matrices(Wq, "Wq", E4M3)
     if experts < 1:
         raise ValueError("Wq must have an expert")
@@ -1055,7 +1062,7 @@ def _fp8_weights(Wq: torch.Tensor, sw: torch.Tensor, offsets: Optional[torch.Ten
     if es != experts or nbs != nb or mb != (m + 127) // 128 or len(sw.shape) != len(Wq.shape):
         raise ValueError(f"sw must have shape {(*Wq.shape[:-2], (m + 127) // 128, nb)}, got {tuple(sw.shape)}")
     return (m, n, nb, (Wq.data_ptr(), ldw, stride, sw.data_ptr(), ldsw, stride_s), experts,
-            None if offsets is None else _vector(offsets, experts + 1, "offsets", torch.int32))
+            _vector(offsets, experts + 1, "offsets", torch.int32))
 
 
 def matmul_fp8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor,

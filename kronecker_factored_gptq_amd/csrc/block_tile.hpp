@@ -16,7 +16,8 @@
 //
 // With Mul::kTransposed R is e4m3 codes k-major (k its rows, D's rows side by side, as a
 // layer's weights are for its input gradient) and C 16-bit along k: a step is 64 k, one unit of R and
-// two of C, so the ring holds three whole steps. R is read from LDS by the transposing
+// two of C, so the ring holds three whole steps (or two, DEEP, which lets three workgroups of 128 x
+// 128 share a CU: a wave's additions do not run beside its own matrix instructions). R is read from LDS by the transposing
 // 8-byte reads, 8 k of a column to a lane, and made 16-bit in registers, once for each
 // row of instructions: no 16-bit copy of the weights is written or read. Only R has scales.
 #pragma once
@@ -25,23 +26,26 @@
 
 namespace bk {
 
-template <class Mul, int B, int WR, int WC>
+template <class Mul, int B, int WR, int WC, int DEEP = Mul::kTransposed ? 3 : 2>
 struct BlockTile {
   typedef f32x4 acc_t;
   static constexpr int kWaves = WR * WC, kThreads = 64 * kWaves;
   static constexpr int FR = B / WR / 16, FC = B / WC / 16;
   static constexpr bool T = Mul::kTransposed;
-  static constexpr int kUnit = B * kStepBytes / 2, kUnits = 9;
+  static constexpr int kUnit = B * kStepBytes / 2;
   static constexpr int kStepUnits = T ? 3 : 4;
+  static constexpr int kDeep = DEEP;  // whole steps in the ring
+  static constexpr int kUnits = T ? 3 * kDeep : 9;
   static constexpr int LU = kUnit / 1024 / kWaves;  // a wave's loads to a unit
   static constexpr int kScaleSlot = kWaves * 256, kScaleSlots = 3;
   static constexpr int kLds = kUnits * kUnit + kScaleSlots * kScaleSlot;
   static constexpr int NB = FR < 4 ? FR : 4;                  // rows' fragments held
   static constexpr int P = FR == 8 ? (T ? 2 : 3) : FR == 4 ? 2 : 1;  // rows multiplied after the barrier
   static constexpr int kLoads = kStepUnits * LU + 1;          // a wave's loads to a step
-  static constexpr int kAhead = T ? kLoads : LU;              // in flight at a step's barrier
+  static constexpr int kAhead = T ? (kDeep - 2) * kLoads : LU;  // in flight at a step's barrier
   static constexpr int kEarly = kLoads / 3;                   // of them, those that go out first
   static constexpr int kLate = T ? 3 : 2;                     // products between a product and its sums' addition
+  static_assert(T ? kDeep == 2 || kDeep == 3 : kDeep == 2, "as the waits count");
   static_assert(LU * 1024 * kWaves == kUnit && kWaves % 2 == 0, "a unit's bytes divide over the waves");
   static_assert(FR % NB == 0 && P < FR && P <= NB, "rows' fragments go round");
   static_assert(B / WR >= 32 && B / WR <= 128 && B / WC <= B / 2, "a wave's rows and columns lie in one unit");
@@ -242,10 +246,8 @@ struct BlockTile {
     load_step(true);
     if (total > 1) load_step(true);
     if (total > 2) {
-      if (T)
-        load_step(true);
-      else
-        load_unit(R, 0);
+      if (T && kDeep > 2) load_step(true);
+      if (!T) load_unit(R, 0);
       wait_barrier<kLoads + kAhead>();
     } else {
       wait_barrier<0>();
@@ -412,7 +414,7 @@ struct BlockTile {
     };
     first_rows(no, no);
     int s = 0;
-    for (; s + 3 < total; ++s) {
+    for (; s + (T ? kDeep : 3) < total; ++s) {
       wait_barrier<kAhead>();
       advance();
       last_rows(yes, yes);

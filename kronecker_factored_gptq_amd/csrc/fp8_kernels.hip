@@ -679,11 +679,11 @@ struct Fp8Gradient {
   const char* p;
   int64_t ld, plane;  // bytes
 };
-template <class Mul, typename O, int B, int WR, int WC, bool ANY>
+template <class Mul, typename O, int B, int WR, int WC, bool ANY, int DEEP>
 __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_grad_kernel(
     Groups groups, Fp8Gradient G, Fp8Weights W, int64_t n, O* __restrict__ dX, int64_t ldx,
     bool vec, int splits, float* __restrict__ parts, int64_t ldp) {
-  typedef BlockTile<Mul, B, WR, WC> TP;
+  typedef BlockTile<Mul, B, WR, WC, DEEP> TP;
   extern __shared__ char lds[];
   const unsigned nr = (unsigned)((n + B - 1) / B);
   const unsigned nc = groups.offsets ? (unsigned)groups.tiles<B>() : (unsigned)((groups.R + B - 1) / B);
@@ -777,12 +777,12 @@ size_t matmul_fp8_grad_bytes(int es, int64_t R, int64_t experts, int64_t m, int6
   return fp8_grad_offsets(es, R, experts, m, n).total;
 }
 
-template <class Mul, typename O, int B, int WR, int WC, bool ANY = false>
+template <class Mul, typename O, int B, int WR, int WC, bool ANY = false, int DEEP = 3>
 static hipError_t start_fp8_grad(const Groups& groups, const Fp8Gradient& G, const Fp8Weights& W,
                                  int64_t n, O* dX, int64_t ldx, int splits, float* parts,
                                  hipStream_t s) {
-  typedef BlockTile<Mul, B, WR, WC> TP;
-  auto* k = matmul_fp8_grad_kernel<Mul, O, B, WR, WC, ANY>;
+  typedef BlockTile<Mul, B, WR, WC, DEEP> TP;
+  auto* k = matmul_fp8_grad_kernel<Mul, O, B, WR, WC, ANY, DEEP>;
   constexpr int lds = ANY ? TP::kAnyLds : TP::kLds;
   if (lds > 65536) {
     const hipError_t e =
@@ -837,8 +837,15 @@ hipError_t launch_matmul_fp8_grad(int64_t R, int64_t experts, int64_t m, int64_t
   const TilePlan plan = fp8_grad_plan(sizeof(G), R, experts, m, n, offsets != nullptr);
   if (plan.tile == 256)
     return start_fp8_grad<Mul, G, 256, 2, 4>(groups, x, W, n, dX, ldx, 1, parts, s);
-  if (plan.tile == 128)
+  if (plan.tile == 128) {
+    // more tiles than two a CU: three, with two steps in the ring (4096 tokens to 4 of 32 experts, 4096
+    // x 2048 bfloat16: 356 -> 338 us; with one tile a CU the shorter ring is slower: 777 x 4096 x 4096
+    // 44.5 and 50.3)
+    const int64_t tiles = (n + 127) / 128 * ((R + 127) / 128 + (offsets ? experts / 2 : 0)) * plan.splits;
+    if (tiles > 512)
+      return start_fp8_grad<Mul, G, 128, 2, 2, false, 2>(groups, x, W, n, dX, ldx, plan.splits, parts, s);
     return start_fp8_grad<Mul, G, 128, 2, 2>(groups, x, W, n, dX, ldx, plan.splits, parts, s);
+  }
   return start_fp8_grad<Mul, G, 64, 2, 2>(groups, x, W, n, dX, ldx, plan.splits, parts, s);
 }
 
