@@ -55,7 +55,7 @@ inline bool fp8_sizes_ok(int64_t T, int64_t R, int64_t experts, int64_t m, int64
          (T + experts * m) * (n + 128) / 4096 < kMaxGroups;  // rows laid out, 16 bytes a thread
 }
 inline bool fp8_grad_sizes_ok(int t, int64_t R, int64_t experts, int64_t m, int64_t n) {
-  return type_ok(t) && fp8_sizes_ok(0, R, experts, m, n) && R * ((n + 255) / 256) <= kMaxGroups &&
+  return type_ok(t) && fp8_sizes_ok(0, R, experts, m, n) &&
          (n + 63) / 64 * (R / 64 + experts + 1) <= kMaxGroups &&
          R + plane_groups(R, m) + plane_groups(experts * m, n) <= kMaxGroups;
 }

@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void gather_kernel(int64_t T, int64_t n, const
   const X* from = x + (has ? t : 0) * ldx;
   X* to = xs + r * lds;
   constexpr int E = 16 / sizeof(X);
-  int64_t c = 0;
+  int64_t c = 0;  // what is left for the loops below begins here
   if (vec) {
     for (c = lane * E; c + E <= n; c += 64 * E)
       *(v4i*)(to + c) = has ? *(const v4i*)(from + c) : v4i{0, 0, 0, 0};
@@ -189,7 +189,14 @@ __global__ __launch_bounds__(256) void gather_kernel(int64_t T, int64_t n, const
   }
   X zero;
   __builtin_memset(&zero, 0, sizeof zero);
-  for (c += lane; c < n; c += 64) to[c] = has ? from[c] : zero;
+  for (c += lane; c + 7 * 64 < n; c += 8 * 64) {  // eight on their way at once
+    X v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = has ? from[c + 64 * i] : zero;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) to[c + 64 * i] = v[i];
+  }
+  for (; c < n; c += 64) to[c] = has ? from[c] : zero;
 }
 template <typename X>
 hipError_t launch_gather_tokens(int64_t T, int64_t n, const X* x, int64_t ldx, int64_t k, int64_t R,
