@@ -735,27 +735,47 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_grad_kernel(
   store_tile(tp, r0, c0, n, c0 + cols, dX, ldx, vec, [](float a, int, int, int) { return a; });
 }
 
-// Codes whose rows are no multiple of 16 long or do not start on 16 bytes, and a 16-bit G
-// likewise, are copied to zero-padded lines first.
-template <int E>
-__global__ __launch_bounds__(256) void pack_rows_kernel(const char* __restrict__ p, int64_t ld,
-                                                        int64_t stride, int64_t per_batch,
-                                                        int64_t rows, int64_t bytes,
-                                                        char* __restrict__ to, int64_t ldp) {
-  const int64_t per = ldp / 16, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// The operands that the tiles cannot read as they are, laid out by one launch: a float32 G as
+// three bfloat16 planes, a 16-bit one whose rows are no multiple of 8 long in zero-padded lines; behind
+// it codes whose rows are no multiple of 16 long, in zero-padded lines (two launches: 333 x 1000 x
+// 1531 float32 26.7 us).
+struct Fp8Layout {
+  char* g;  // null: as it is
+  int64_t ldg, plane, blocks;
+  char* w;
+  int64_t ldw, rows;
+};
+template <typename G>
+__global__ __launch_bounds__(256) void grad_layout_kernel(int64_t R, int64_t m, int64_t n,
+                                                          const G* __restrict__ g, int64_t ldg,
+                                                          Fp8Weights W, Fp8Layout to, bool vec) {
+  if ((int64_t)blockIdx.x < to.blocks) {
+    const int64_t per = to.ldg / 16, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t r = at / per, c = (at - r * per) * 8;
+    if (r >= R) return;
+    const Eight<G> t = load8(g + r * ldg, c, m, vec);
+    char* p = to.g + r * to.ldg + c * 2;
+    if constexpr (sizeof(G) == 4) {
+      unsigned short w[3][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        unsigned short x[3];
+        split16<kBF16x3>(to_f32(t.v[e]), x);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) w[i][e] = x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *(v4i*)(p + i * to.plane) = __builtin_bit_cast(v4i, w[i]);
+    } else {
+      *(v4i*)p = __builtin_bit_cast(v4i, t);
+    }
+    return;
+  }
+  const int64_t per = to.ldw / 16, at = (int64_t)(blockIdx.x - to.blocks) * 256 + threadIdx.x;
   const int64_t r = at / per, k = (at - r * per) * 16;
-  if (r >= rows) return;
-  const int64_t z = r / per_batch;
-  *(v4i*)(to + r * ldp + k) = load_any<E>(p + z * stride + (r - z * per_batch) * ld, k, bytes);
-}
-template <int E>
-static hipError_t pack_rows(const char* p, int64_t ld, int64_t stride, int64_t per_batch,
-                            int64_t rows, int64_t bytes, char* to, int64_t ldp, hipStream_t s) {
-  const int64_t n = rows * (ldp / 16);
-  if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(pack_rows_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p, ld,
-                     stride, per_batch, rows, bytes, to, ldp);
-  return hipGetLastError();
+  if (r >= to.rows) return;
+  const int64_t z = r / W.m;
+  *(v4i*)(to.w + r * to.ldw + k) = load_any<1>(W.p + z * W.stride + (r - z * W.m) * W.ld, k, n);
 }
 
 static TilePlan fp8_grad_plan(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool grouped) {
@@ -811,24 +831,26 @@ hipError_t launch_matmul_fp8_grad(int64_t R, int64_t experts, int64_t m, int64_t
   Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
   const Fp8GradOffsets o = fp8_grad_offsets(sizeof(G), R, experts, m, n);
   char* b = (char*)ws;
-  hipError_t e = hipSuccess;
-  if (n % 16) {
-    e = pack_rows<1>(W.p, ldw, stride_w, m > 0 ? m : 1, experts * m, n, b + o.w, packed_ld(n), s);
-    if (e != hipSuccess) return e;
-    W.p = b + o.w;
-    W.ld = packed_ld(n);
-    W.stride = m * W.ld;
-  }
   Fp8Gradient x = {(const char*)g, ldg * (int64_t)sizeof(G), 0};
-  if (wide) {
-    const Planes planes = {b + o.g, plane_ld(m), R * plane_ld(m)};
-    e = launch_planes<float, kBF16x3>(R, m, (const float*)g, ldg, nullptr, nullptr, planes, s);
-    x = {planes.w, planes.ld, planes.plane};
-  } else if (m % 8) {
-    e = pack_rows<2>(x.p, x.ld, 0, R, R, m * 2, b + o.g, plane_ld(m), s);
-    x = {b + o.g, plane_ld(m), 0};
+  const bool lay_g = (wide || m % 8) && m > 0, lay_w = n % 16 && m > 0;
+  if (lay_g || lay_w) {
+    Fp8Layout to = {nullptr, plane_ld(m), R * plane_ld(m), 0, b + o.w, packed_ld(n), lay_w ? experts * m : 0};
+    if (lay_g) {
+      to.g = b + o.g;
+      to.blocks = (R * (to.ldg / 16) + 255) / 256;
+      x = {to.g, to.ldg, wide ? to.plane : 0};
+    }
+    const int64_t blocks = to.blocks + (to.rows * (to.ldw / 16) + 255) / 256;
+    hipLaunchKernelGGL(grad_layout_kernel<G>, dim3((unsigned)blocks), dim3(256), 0, s, R, m, n, g, ldg,
+                       W, to, load8_ok(g, ldg));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (lay_w) {
+      W.p = to.w;
+      W.ld = to.ldw;
+      W.stride = m * W.ld;
+    }
   }
-  if (e != hipSuccess) return e;
   float* parts = (float*)(b + o.parts);
   // 16-byte rows and 32-bit offsets
   if (((uintptr_t)W.p | W.ld | W.stride | (uintptr_t)x.p | x.ld | x.plane) % 16 != 0 ||
