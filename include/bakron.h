@@ -603,17 +603,19 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
  * bakron_matmul_fp8_grad: the input gradient, the tokens' rounding passed straight through,
  *   dX[r][j] = sum_i G[r][i] * sw[i / 128][j / 128] * Wq[i][j],
  * rows in groups as above (rows in no group are left as they were). G (R x m, ldg) and dX
- * (R x n, ldx) are of gtype: F32, BF16 or F16. For BF16 and F16 G is taken at 11 bits
- * (down to 2^-28 of the row's largest, and to 2^-39 of it below), all that they
- * have; F32 keeps its 24. Products are exact, sums float32, one rounding to gtype. The codes
- * are what the layer holds: there is no gradient with respect to them.
+ * (R x n, ldx) are of gtype: F32, BF16 or F16, and G is taken with all the bits it has (F32
+ * values below 2^-109 with those down to 2^-133).
+ * Products are exact, sums float32, one rounding to gtype. For F32 an infinity in G may make
+ * the results it enters NaN. The codes are what the layer holds: there is no gradient with
+ * respect to them.
  *
  * Outputs must not overlap the inputs (BAKRON_EINVAL; arrays are compared from their first
- * element to their last). Rows that start at multiples of 16 bytes with n (and, for
- * the gradient, m) a multiple of 16 are read fastest; any alignment and stride works. 1 <=
- * experts <= 1024; T, R < 2^24; m, n <= 2^20; around 2^36 elements of Xq and Wq, 2^35 of the
- * gradient's operands and 2^36 of Y and beyond, more than one launch holds, are
- * BAKRON_EINVAL. Asynchronous, deterministic.
+ * element to their last). Rows that start at multiples of 16 bytes with n a multiple of 16
+ * (and, for a 16-bit G, m one of 8) are read fastest; rows of other lengths are copied to the
+ * workspace first, and any alignment and stride works. The workspace queries give 0, and
+ * workspace may be NULL, where a call needs none. 1 <= experts <= 1024; T, R < 2^24; m, n <= 2^20;
+ * around 2^36 elements of Xq and Wq, 2^35 of the gradient's operands and 2^36 of Y or dX and beyond,
+ * more than one launch holds, are BAKRON_EINVAL. Asynchronous, deterministic.
  * ------------------------------------------------------------------------ */
 int bakron_quantize_fp8(int xtype, int64_t batch, int64_t rows, int64_t n,
                         const void *X, int64_t ldx, int64_t stride_x, int block_rows,

@@ -1,6 +1,7 @@
 // 8-bit floating point on gfx950: matrices quantised to e4m3 codes with a float32
-// scale for each block of 1 x 128 or 128 x 128, and the product of such tokens with
-// such weights, for one layer or for groups of tokens with weights of their own.
+// scale for each block of 1 x 128 or 128 x 128, the product of such tokens with such
+// weights, for one layer or for groups of tokens with weights of their own, and its input
+// gradient.
 #include "block_tile.hpp"
 #include "fp8_product.hpp"
 #include "launch.hpp"
@@ -150,7 +151,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(
   }
 }
 
-// Blocks of 128 x 128, a workgroup each, held in registers between the maximum and the codes.
+// Blocks of 128 x 128, a workgroup each, held in registers between the maximum and the codes
+// (8192 x 14336 bfloat16 75 us, 4003 x 11009 float32, unaligned rows, 46).
 template <typename X, bool VEC>
 __global__ __launch_bounds__(256) void quantize_blocks_kernel(
     int64_t rows, int64_t n, unsigned across, const X* __restrict__ x, int64_t ldx, int64_t sX,
@@ -216,7 +218,10 @@ hipError_t launch_quantize_fp8(int64_t batch, int64_t rows, int64_t n, const X* 
 // Y[r][i] = sum over blocks b of k of sx[t][b] sw[i / 128][b] sum_{j in b} Xq[t][j] Wq[i][j],
 // t the token of row r, W its group's: tiles of channels x rows. With `splits` ranges of the
 // steps (one layer only) their sums go to parts[range]. ANY: operands that the direct loads
-// cannot take.
+// cannot take. 8192 x 14336 x 4096 to bfloat16 461 to 485 us from card to card, 2.0 to 2.1e15
+// flop/s (a library's product without block scales reaches 2.6 here); to float32, on the
+// float16 instructions, 940. 4096 tokens to 8 of 64 experts of 2048 x 4096 375 to 419 us, 1.3 to 1.5e15
+// of the products asked for: groups end inside tiles.
 // ---------------------------------------------------------------------------
 template <class Mul, typename O, int B, int WR, int WC, bool ANY>
 __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
@@ -364,7 +369,8 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(Fp8Tokens X, Fp8Weights W
 // one layer and all of its rows, 16 NT at a time; its waves divide k between them, U blocks
 // a turn, straight from memory to registers with the next turn on its way, and their
 // sums meet in LDS (skinny_product.hpp, with the blocks' scales). Grid: channels x (tiles of
-// rows, or experts).
+// rows, or experts). One row: 4096 x 4096 5.9 us on the GPU, 14336 x 4096 13.9 (4.2 TB/s);
+// 256 rows of 64 experts of 2048 x 4096 102 us (5.3 TB/s).
 // ---------------------------------------------------------------------------
 template <class Mul, typename O, int RT, int NT, int U, bool ANY>
 __global__ __launch_bounds__(512) void skinny_fp8_kernel(Groups groups, Fp8Tokens X, Fp8Weights W,
@@ -673,7 +679,8 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
 // k-major and made 16-bit in registers (BlockTile, kTransposed). A bfloat16 or float16 G is
 // multiplied as it is, a float32 one as its three bfloat16 planes, one after the other
 // over all of k. With `splits` ranges of the steps (one layer only) their sums go to
-// parts[range].
+// parts[range]. 8192 x 4096 x 14336 bfloat16 860 to 895 us (1.1 PFLOP/s; a library's 16-bit product of
+// two matrices reaches 1.6); 4096 tokens to 4 of 32 experts of 4096 x 2048 330 to 340 us (0.82).
 // ---------------------------------------------------------------------------
 struct Fp8Gradient {
   const char* p;
