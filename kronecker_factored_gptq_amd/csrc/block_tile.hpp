@@ -17,9 +17,11 @@
 // With Mul::kTransposed R is e4m3 codes k-major (k its rows, D's rows side by side, as a
 // layer's weights are for its input gradient) and C 16-bit along k: a step is 64 k, one unit of R and
 // two of C, so the ring holds three whole steps (or two, DEEP, which lets three workgroups of 128 x
-// 128 share a CU: a wave's additions do not run beside its own matrix instructions). R is read from LDS by the transposing
-// 8-byte reads, 8 k of a column to a lane, and made 16-bit in registers, once for each
-// row of instructions: no 16-bit copy of the weights is written or read. Only R has scales.
+// 128 share a CU: a wave's additions do not run beside its own matrix instructions). R is read
+// from LDS by the transposing 8-byte reads, 8 k of a column to a lane, and made 16-bit in
+// registers, once for each row of instructions: no 16-bit copy of the weights is written or
+// read. Only R has scales.
+//
 // What bounds a large product (8192 x 14336 x 4096 e4m3, 256 x 256, 470 us): the matrix instructions
 // alone would keep their units busy for 0.48 of its cycles. Without the multiply-adds it took 420
 // us, without loads as well 352, without barriers as well 336: a wave's additions do not
@@ -142,16 +144,17 @@ struct BlockTile {
     }
   };
   // R of kTransposed: `krows` rows of k, `ld` bytes apart, each holding that k of the tile's
-  // `cols` columns from `p` on, readable up to a multiple of 16. A step's 64 k lie in LDS one after
-  // the other, the 16 bytes b of k at b ^ swap_at(k): the 16 k that two groups of 16 lanes
-  // read at one b then fall on different banks.
+  // `cols` columns from `p` on; what follows them in their last chunk makes columns that are not
+  // for storing, and of the last row no word is read that holds none of them. A step's 64 k lie
+  // in LDS one after the other, the 16 bytes b of k at b ^ swap_at(k): the 16 k that two groups
+  // of 16 lanes read at one b then fall on different banks.
   __device__ static inline int swap_at(int k) { return B == 256 ? k & 15 : B == 128 ? (k >> 1) & 7 : (k >> 2) & 3; }
   struct SideT {
     const char *p, *first;
     int64_t stride;
     v4i rsrc;
     int off[LU];
-    int krow, k, last, bytes;
+    int krow, k, last, bytes, bytes_last;
     __device__ inline void init(const char* p_, int64_t ld, int64_t krows, int cols, int s0) {
       const int lane = threadIdx.x & 63;
       constexpr int per = B / 16, lanes_k = 64 / per;  // chunks of a k; k of a wave load
@@ -164,10 +167,14 @@ struct BlockTile {
       krow = wave() * lanes_k + lane / per + last * 64 - (int)krows;  // >= 0 in the last step: past the last k
       stride = 64 * ld;
       bytes = 63 * (int)ld + (cols + 15) / 16 * 16;
+      bytes_last = ((int)(krows - 1) - last * 64) * (int)ld + (cols + 3) / 4 * 4;
       first = p_;
       k = last < 0 ? 0 : __builtin_amdgcn_readfirstlane(s0) % (last + 1);
       p = p_ + k * stride;
-      rsrc = buffer(p, bytes);
+      bytes = __builtin_amdgcn_readfirstlane(bytes);  // in next(): 8192 x 4096 x 14336 857 us, not 850
+      bytes_last = __builtin_amdgcn_readfirstlane(bytes_last);
+      last = __builtin_amdgcn_readfirstlane(last);
+      rsrc = buffer(p, k == last ? bytes_last : bytes);
     }
     __device__ inline void load(int, int j, unsigned lds) const {
       constexpr int lanes_k = 64 / (B / 16);
@@ -178,7 +185,7 @@ struct BlockTile {
       const bool wrap = Mul::kPlanes > 1 && k == last;
       k = wrap ? 0 : k + 1;
       p = wrap ? first : p + stride;
-      rsrc = buffer(p, bytes);
+      rsrc = buffer(p, k == last ? bytes_last : bytes);
     }
   };
   typedef typename std::conditional<T, SideT, Side>::type SideR;
@@ -187,10 +194,32 @@ struct BlockTile {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
   }
 
+  // Rows of a length that is no multiple of 16: what follows them in their last chunk came along and
+  // may be anything, a NaN for instance. It is made zero in LDS, in the units of one step from
+  // `first` on, byte `tail` of a row on. (Copied to zero-padded lines first, 1000 x 2000 x 4095
+  // bfloat16 takes 32 us in place of 21.)
+  __device__ static inline void zero_tail(char* lds, unsigned first, int tail) {
+    for (int row = threadIdx.x; row < 2 * B; row += kThreads) {
+      unsigned u = first + row / (B / 2);
+      u = u >= kUnits ? u - kUnits : u;
+      const int r = row % (B / 2);
+      v4i* at = (v4i*)(lds + u * kUnit + r * kStepBytes + chunk_at(r, tail / 16) * 16);
+      v4i x = *at;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int keep = tail % 16 - 4 * d;  // bytes of this word
+        x[d] &= keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << 8 * keep) - 1;
+      }
+      *at = x;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+
   // D's tile, its steps [s0, s1). `scale`: this wave's scales, `per` bytes from the block's
-  // pointer, which moves `stride` bytes a block of k.
+  // pointer, which moves `stride` bytes a block of k. `tail`: where rows end in the last of these
+  // steps, 0 at a multiple of 16 (zero_tail).
   __device__ inline void run(SideR& R, Side& C, const char* scale, int per, int64_t stride, int s0,
-                             int s1, char* lds) {
+                             int s1, char* lds, int tail = 0) {
     s0 = __builtin_amdgcn_readfirstlane(s0);
     const int total = __builtin_amdgcn_readfirstlane(s1) - s0;
     if (total <= 0) return;
@@ -258,6 +287,7 @@ struct BlockTile {
       wait_barrier<kLoads + kAhead>();
     } else {
       wait_barrier<0>();
+      if (!T && tail && total == 1) zero_tail(lds, 0, tail);
     }
 
     const int hr = w / WC * FR * 16 >= B / 2, hc = w % WC * FC * 16 >= B / 2;
@@ -433,6 +463,7 @@ struct BlockTile {
       else
         wait_barrier<0>();
       advance();
+      if (!T && tail && s + 2 == total) zero_tail(lds, step, tail);
       if (!T && s + 2 < total) load_step(false);
       last_rows(no, yes);
       first_rows(no, yes);

@@ -265,7 +265,8 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
   }
   typename TP::Side R, C;
   const int s0 = (int)((int64_t)total * range / splits), s1 = (int)((int64_t)total * (range + 1) / splits);
-  R.init(W.p + group * W.stride + r0 * W.ld, (int)((rows - 1) * W.ld + n), n, 0, s0,
+  const int64_t words = (n + 3) / 4 * 4;  // of the last row no word is read that holds none of it
+  R.init(W.p + group * W.stride + r0 * W.ld, (int)((rows - 1) * W.ld + words), n, 0, s0,
          [&](int row) { return (row < (int)rows ? row : (int)rows - 1) * (int)W.ld; });
   // the token of a tile's column: its offset in rows from `first`, -1 if none
   const int64_t first = X.order ? 0 : c0;
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
     return X.order ? (int)X.token(c0 + col) : col;
   };
   const int64_t last_row = X.order ? (X.T > 0 ? X.T - 1 : 0) : cols - 1;
-  C.init(X.p + first * X.ld, (int)(last_row * X.ld + n), n, 0, s0, [&](int col) {
+  C.init(X.p + first * X.ld, (int)(last_row * X.ld + words), n, 0, s0, [&](int col) {
     const int t = token(col);
     return t < 0 ? TP::kNone : t * (int)X.ld;
   });
@@ -289,7 +290,8 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
     scale = (const char*)(W.s + group * W.strides + r0 / kBlock * W.lds);
     per = (lane < last ? lane : last) * (int)W.lds * 4;
   }
-  tp.run(R, C, scale, per, (wave < B / 64 ? X.sb : 1) * 4, s0, s1, lds);
+  tp.run(R, C, scale, per, (wave < B / 64 ? X.sb : 1) * 4, s0, s1, lds,
+         n % 16 && s1 == total ? (int)(n % kStepBytes) : 0);
   if (splits > 1) {
     store_sums(tp, r0, c0, groups.R, parts + range * groups.R * ldp, ldp);
     return;
@@ -341,8 +343,8 @@ static hipError_t join_fp8(int64_t m, int64_t R, int splits, const float* parts,
   return hipGetLastError();
 }
 
-// Rows whose length is no multiple of 16 are copied to zero-padded lines first, 16 bytes a
-// thread: the tokens', and behind them every expert's.
+// Rows that do not start on 16 bytes, of a length that is no multiple of 16, are copied to
+// zero-padded lines first, 16 bytes a thread: the tokens', and behind them every expert's.
 __global__ __launch_bounds__(256) void pack_fp8_kernel(Fp8Tokens X, Fp8Weights W, int64_t experts,
                                                        int64_t n, char* __restrict__ px,
                                                        char* __restrict__ pw, int64_t ldp) {
@@ -616,12 +618,14 @@ static hipError_t start_fp8_tile(const Groups& groups, const Fp8Tokens& X, const
 }
 
 // Whether the direct loads can take the operands: rows on 16 bytes, and 32-bit offsets.
+static bool on_16(const Fp8Tokens& X, const Fp8Weights& W) {
+  return ((uintptr_t)X.p | X.ld | (uintptr_t)W.p | W.ld | W.stride) % 16 == 0;
+}
 static bool fp8_direct(const Fp8Tokens& X, const Fp8Weights& W, int64_t n) {
   const int64_t kMost = (int64_t)1 << 31;
   const int64_t reach = X.order ? X.T : 256;
-  return ((uintptr_t)X.p | X.ld | (uintptr_t)W.p | W.ld | W.stride | n) % 16 == 0 &&
-         W.ld <= kTileMaxLd && reach * X.ld + n < kMost && reach * X.st * 4 < kMost &&
-         W.lds * 8 < kMost;
+  return on_16(X, W) && W.ld <= kTileMaxLd && reach * X.ld + n + 16 < kMost &&
+         reach * X.st * 4 < kMost && W.lds * 8 < kMost;
 }
 
 template <typename O>
@@ -647,7 +651,7 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
     return n % 16 == 0 && fp8_direct(X, W, n) ? start_skinny_fp8<Mul, O, false>(groups, X, W, n, Y, ldy, s)
                                               : start_skinny_fp8<Mul, O, true>(groups, X, W, n, Y, ldy, s);
   const Fp8Offsets o = fp8_offsets(sizeof(O), T, R, experts, m, n);
-  if (n % 16) {
+  if (n % 16 && !on_16(X, W)) {
     const int64_t ld = packed_ld(n);
     char *px = (char*)ws + o.x, *pw = (char*)ws + o.w;
     hipLaunchKernelGGL(pack_fp8_kernel,
@@ -744,8 +748,8 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_grad_kernel(
 
 // The operands that the tiles cannot read as they are, laid out by one launch: a float32 G as
 // three bfloat16 planes, a 16-bit one whose rows are no multiple of 8 long in zero-padded lines; behind
-// it codes whose rows are no multiple of 16 long, in zero-padded lines (two launches: 333 x 1000 x
-// 1531 float32 26.7 us).
+// it codes whose rows are no multiple of 16 long and do not start on 16 bytes, in zero-padded lines
+// (two launches: 333 x 1000 x 1531 float32 26.7 us, one 24.9).
 struct Fp8Layout {
   char* g;  // null: as it is
   int64_t ldg, plane, blocks;
@@ -839,7 +843,8 @@ hipError_t launch_matmul_fp8_grad(int64_t R, int64_t experts, int64_t m, int64_t
   const Fp8GradOffsets o = fp8_grad_offsets(sizeof(G), R, experts, m, n);
   char* b = (char*)ws;
   Fp8Gradient x = {(const char*)g, ldg * (int64_t)sizeof(G), 0};
-  const bool lay_g = (wide || m % 8) && m > 0, lay_w = n % 16 && m > 0;
+  const bool lay_g = (wide || m % 8) && m > 0;
+  const bool lay_w = n % 16 && ((uintptr_t)W.p | W.ld | W.stride) % 16 && m > 0;
   if (lay_g || lay_w) {
     Fp8Layout to = {nullptr, plane_ld(m), R * plane_ld(m), 0, b + o.w, packed_ld(n), lay_w ? experts * m : 0};
     if (lay_g) {

@@ -225,6 +225,40 @@ def test_matmul_strides(gpu_lib, pad, first, T):
     assert (a - b).abs().max() <= 1e-5 * b.abs().max()
 
 
+@pytest.mark.parametrize("T,m,n", [(1, 70, 129), (40, 300, 255), (300, 200, 407), (90, 500, 1531), (700, 900, 130), (257, 140, 113),
+                                   (130, 260, 4097), (3600, 3600, 143), (3500, 3700, 17)])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_rows_end_inside_a_group_of_16(gpu_lib, T, m, n, t):
+    """Codes with rows on 16 bytes and of any length, as quantize_fp8 lays them out, NaN codes behind
+    each row: the product, by experts too, and the gradient."""
+    bk = gpu_lib
+    g = torch.Generator().manual_seed(T + m + n)
+    ld = (n + 15) // 16 * 16 + 16 * (T % 3)
+    xb, wb = codes(T, n, g, True), codes(m, n, g, True)
+    X, W = torch.full((T, ld), 0x7f, dtype=torch.uint8, device="cuda"), torch.full((m, ld), 0xff, dtype=torch.uint8, device="cuda")
+    X[:, :n], W[:, :n] = xb.cuda(), wb.cuda()
+    sx, sw = scales(T, blocks(n), g) * 0.05, scales(blocks(m), blocks(n), g) * 0.05
+    big = T * m > 1 << 22  # the reference on the GPU
+    u, v = (values(b, n).cuda() if big else values(b, n) for b in (xb, wb))
+    a, b = (s.cuda() if big else s for s in (sx, sw))
+    ref, S = expected(u, a, v, b)
+    Xv, Wv = X.view(F8)[:, :n], W.view(F8)[:, :n]
+    off = torch.tensor([0, T // 3, T], dtype=torch.int32).cuda()
+    both, scale2 = torch.stack([W, W])[:, :, :n].view(F8), torch.stack([sw, sw]).cuda()
+    assert both.stride(1) == ld
+    tol = tolerance(ref, S, n, TYPES[t], True)
+    for Y in (bk.matmul_fp8(Xv, sx.cuda(), Wv, sw.cuda(), out_dtype=TYPES[t]),
+              bk.matmul_fp8(Xv, sx.cuda(), both, scale2, offsets=off, order=torch.arange(T, dtype=torch.int32).cuda(), out_dtype=TYPES[t])):
+        assert ((Y.to(ref.device).double() - ref).abs() <= tol).all()
+    G = torch.randn(T, m, generator=g).to(TYPES[t])
+    V = (v.cpu() if big else v) * spread(sw, 128, m, n).double()
+    H, V = (G.double().cuda(), V.cuda()) if big else (G.double(), V)
+    ref, S = H @ V, H.abs() @ V.abs()
+    tol = S * (3 * m * 2.0 ** -23 + 3 * E32) + ref.abs() * half_step(TYPES[t]) * (1 + 2.0 ** -8) + smallest(TYPES[t])
+    for D in (bk.matmul_fp8_grad(G.cuda(), Wv, sw.cuda()), bk.matmul_fp8_grad(G.cuda(), both, scale2, offsets=off)):
+        assert ((D.to(ref.device).double() - ref).abs() <= tol).all()
+
+
 def test_matmul_empty(gpu_lib):
     bk = gpu_lib
     z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda").view(F8)
