@@ -613,11 +613,11 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
  * element to their last). Rows of codes that start at multiples of 16 bytes are read fastest
  * (and 16-bit ones of G, with m a multiple of 8; others are copied to the workspace first, as are
  * codes whose rows are neither aligned nor whole groups of 16), and any alignment and stride
- * works. Up to 3 bytes behind a row of codes may be read, in the aligned word that holds its
- * end; they do not matter. The workspace queries give 0, and workspace may be NULL, where a call
- * needs none. 1 <= experts <= 1024; T, R < 2^24; m, n <= 2^20; around 2^36 elements of Xq and Wq,
- * 2^35 of the gradient's operands and 2^36 of Y or dX and beyond,
- * more than one launch holds, are BAKRON_EINVAL. Asynchronous, deterministic.
+ * works. What lies between two rows of codes may be read, and up to 3 bytes behind the last, in
+ * the aligned word that holds its end; it does not matter. The workspace queries give 0, and
+ * workspace may be NULL, where a call needs none. 1 <= experts <= 1024; T, R < 2^24; m, n <= 2^20;
+ * around 2^36 elements of Xq and Wq, 2^35 of the gradient's operands and 2^36 of Y or dX and
+ * beyond, more than one launch holds, are BAKRON_EINVAL. Asynchronous, deterministic.
  * ------------------------------------------------------------------------ */
 int bakron_quantize_fp8(int xtype, int64_t batch, int64_t rows, int64_t n,
                         const void *X, int64_t ldx, int64_t stride_x, int block_rows,
