@@ -243,6 +243,18 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
   const int total = (int)((n + kStepBytes - 1) / kStepBytes);
   TP tp;
   tp.zero();
+  // Rows without a token are 0 whatever the weights hold (0 times a NaN code or a scale that is not
+  // finite is NaN): before the sums of any range of k leave.
+  auto clear = [&]() {
+    if (!X.order) return;
+#pragma unroll
+    for (int j = 0; j < TP::FC; ++j) {
+      const int col = tp.wave_c() + j * 16 + (lane & 15);
+      if (X.token(c0 + (col < (int)cols ? col : (int)cols - 1)) >= 0) continue;
+#pragma unroll
+      for (int i = 0; i < TP::FR; ++i) tp.acc[i][j] = f32x4{0, 0, 0, 0};
+    }
+  };
   if constexpr (ANY) {
     const char* w = W.p + group * W.stride + r0 * W.ld;
     const float* sw = W.s + group * W.strides + (r0 + tp.wave_r() < W.m ? r0 + tp.wave_r() : W.m - 1) / kBlock * W.lds;
@@ -260,6 +272,7 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
           const int64_t t = token(tp.wave_c() + j * 16 + (lane & 15));
           return t < 0 ? 0.0f : X.s[t * X.st + s * X.sb] * sw[s];
         });
+    clear();
     store_tile(tp, r0, c0, W.m, c0 + cols, Y, ldy, vec, [](float a, int, int, int) { return a; });
     return;
   }
@@ -292,17 +305,10 @@ __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
   }
   tp.run(R, C, scale, per, (wave < B / 64 ? X.sb : 1) * 4, s0, s1, lds,
          n % 16 && s1 == total ? (int)(n % kStepBytes) : 0);
+  clear();
   if (splits > 1) {
     store_sums(tp, r0, c0, groups.R, parts + range * groups.R * ldp, ldp);
     return;
-  }
-  if (X.order) {  // rows without a token are 0 whatever the weights' scales are
-#pragma unroll
-    for (int j = 0; j < TP::FC; ++j)
-      if (token(tp.wave_c() + j * 16 + (lane & 15)) < 0) {
-#pragma unroll
-        for (int i = 0; i < TP::FR; ++i) tp.acc[i][j] = f32x4{0, 0, 0, 0};
-      }
   }
   store_tile(tp, r0, c0, W.m, c0 + cols, Y, ldy, vec, [](float a, int, int, int) { return a; });
 }
