@@ -614,8 +614,12 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
  * (and 16-bit ones of G, with m a multiple of 8; others are copied to the workspace first, as are
  * codes whose rows are neither aligned nor whole groups of 16), and any alignment and stride
  * works. What lies between two rows of codes may be read, and up to 3 bytes behind the last, in
- * the aligned word that holds its end; it does not matter. The workspace queries give 0, and
- * workspace may be NULL, where a call needs none. 1 <= experts <= 1024; T, R < 2^24; m, n <= 2^20;
+ * the aligned word that holds its end; it does not matter. Of the two workspace queries of a call
+ * the first is for codes of any alignment, the aligned one for rows of Xq and Wq that all start at
+ * multiples of 16 bytes (the matrices, and the leading dimensions and stride_w of more than one row
+ * or expert), of which no copies are made: they differ where n is no multiple of 16, by a copy of all
+ * codes. Where a query gives 0 workspace may be NULL.
+ * 1 <= experts <= 1024; T, R < 2^24; m, n <= 2^20;
  * around 2^36 elements of Xq and Wq, 2^35 of the gradient's operands and 2^36 of Y or dX and
  * beyond, more than one launch holds, are BAKRON_EINVAL. Asynchronous, deterministic.
  * ------------------------------------------------------------------------ */
@@ -625,6 +629,8 @@ int bakron_quantize_fp8(int xtype, int64_t batch, int64_t rows, int64_t n,
                         float *s, int64_t s_row, int64_t s_block, int64_t stride_s, void *stream);
 size_t bakron_matmul_fp8_workspace_bytes(int ytype, int64_t T, int64_t R, int64_t experts,
                                          int64_t m, int64_t n);
+size_t bakron_matmul_fp8_aligned_workspace_bytes(int ytype, int64_t T, int64_t R, int64_t experts,
+                                                 int64_t m, int64_t n);
 int bakron_matmul_fp8(int ytype, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n,
                       const uint8_t *Xq, int64_t ldx,
                       const float *sx, int64_t sx_token, int64_t sx_block,
@@ -635,6 +641,8 @@ int bakron_matmul_fp8(int ytype, int64_t T, int64_t R, int64_t experts, int64_t 
                       void *workspace, size_t workspace_bytes, void *stream);
 size_t bakron_matmul_fp8_grad_workspace_bytes(int gtype, int64_t R, int64_t experts, int64_t m,
                                               int64_t n);
+size_t bakron_matmul_fp8_grad_aligned_workspace_bytes(int gtype, int64_t R, int64_t experts,
+                                                      int64_t m, int64_t n);
 int bakron_matmul_fp8_grad(int gtype, int64_t R, int64_t experts, int64_t m, int64_t n,
                            const void *G, int64_t ldg,
                            const uint8_t *Wq, int64_t ldw, int64_t stride_w,

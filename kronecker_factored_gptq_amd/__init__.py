@@ -161,13 +161,15 @@ def lib() -> ctypes.CDLL:
     L.bakron_quantize_fp8.argtypes = [_int, _i64, _i64, _i64, _vp, _i64, _i64, _int, _vp, _i64, _i64, _vp, _i64,
                                       _i64, _i64, _vp]
     L.bakron_quantize_fp8.restype = _int
-    L.bakron_matmul_fp8_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _i64, _i64]
-    L.bakron_matmul_fp8_workspace_bytes.restype = _sz
+    for f in (L.bakron_matmul_fp8_workspace_bytes, L.bakron_matmul_fp8_aligned_workspace_bytes):
+        f.argtypes = [_int, _i64, _i64, _i64, _i64, _i64]
+        f.restype = _sz
     L.bakron_matmul_fp8.argtypes = [_int, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
                                     _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
     L.bakron_matmul_fp8.restype = _int
-    L.bakron_matmul_fp8_grad_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _i64]
-    L.bakron_matmul_fp8_grad_workspace_bytes.restype = _sz
+    for f in (L.bakron_matmul_fp8_grad_workspace_bytes, L.bakron_matmul_fp8_grad_aligned_workspace_bytes):
+        f.argtypes = [_int, _i64, _i64, _i64, _i64]
+        f.restype = _sz
     L.bakron_matmul_fp8_grad.argtypes = [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
                                          _vp, _vp, _i64, _vp, _sz, _vp]
     L.bakron_matmul_fp8_grad.restype = _int
@@ -1065,6 +1067,11 @@ def _fp8_weights(Wq: torch.Tensor, sw: torch.Tensor, offsets: Optional[torch.Ten
             _vector(offsets, experts + 1, "offsets", torch.int32))
 
 
+def _fp8_rows(m: int, p: int, ldw: int, stride: int, *scales) -> int:
+    """A multiple of 16 where every row of a layer's codes starts at one."""
+    return p | (m > 1 and ldw) | stride
+
+
 def matmul_fp8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor,
                offsets: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None, per_token: int = 1,
                out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
@@ -1100,9 +1107,12 @@ def matmul_fp8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.T
     dtype = out_dtype if out is None else out.dtype
     code = _ft(dtype, "out_dtype")
     out, ldy = _output(out, R, m, dtype, "out", dev)
-    L = lib()
-    ws, pws, nws = _scratch(L.bakron_matmul_fp8_workspace_bytes(code, T, R, experts, m, n), dev, workspace)
-    _call("bakron_matmul_fp8", dev, L.bakron_matmul_fp8, code, T, R, experts, m, n, Xq.data_ptr(), ldx,
+    L, px = lib(), Xq.data_ptr()
+    query = L.bakron_matmul_fp8_workspace_bytes
+    if n % 16 and (px | (T > 1 and ldx) | _fp8_rows(m, *weights)) % 16 == 0:  # else they agree, or copies are made
+        query = L.bakron_matmul_fp8_aligned_workspace_bytes
+    ws, pws, nws = _scratch(query(code, T, R, experts, m, n), dev, workspace)
+    _call("bakron_matmul_fp8", dev, L.bakron_matmul_fp8, code, T, R, experts, m, n, px, ldx,
           sx.data_ptr(), *sx.stride(), *weights, po, pr, per_token, out.data_ptr(), ldy, pws, nws)
     return out
 
@@ -1123,7 +1133,10 @@ def matmul_fp8_grad(G: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor, offsets
         raise ValueError(f"G must have a column for each row of Wq, got {m} and {mw}")
     out, ldx = _output(out, R, n, G.dtype, "out", dev)
     L = lib()
-    ws, pws, nws = _scratch(L.bakron_matmul_fp8_grad_workspace_bytes(code, R, experts, m, n), dev, workspace)
+    query = L.bakron_matmul_fp8_grad_workspace_bytes
+    if n % 16 and _fp8_rows(m, *weights) % 16 == 0:
+        query = L.bakron_matmul_fp8_grad_aligned_workspace_bytes
+    ws, pws, nws = _scratch(query(code, R, experts, m, n), dev, workspace)
     _call("bakron_matmul_fp8_grad", dev, L.bakron_matmul_fp8_grad, code, R, experts, m, n, G.data_ptr(), ldg, *weights,
           po, out.data_ptr(), ldx, pws, nws)
     return out

@@ -60,6 +60,17 @@ inline bool fp8_grad_sizes_ok(int t, int64_t R, int64_t experts, int64_t m, int6
          R + plane_groups(R, m) + plane_groups(experts * m, n) <= kMaxGroups;
 }
 
+// a query's answer: room to align what the call needs, nothing for nothing
+inline size_t with_slack(size_t b) { return b ? b + kAlign : 0; }
+inline size_t fp8_query(int t, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n, bool aligned) {
+  if (!type_ok(t) || !fp8_sizes_ok(T, R, experts, m, n)) return 0;
+  return with_slack(matmul_fp8_bytes((int)type_size(t), T, R, experts, m, n, aligned));
+}
+inline size_t fp8_grad_query(int t, int64_t R, int64_t experts, int64_t m, int64_t n, bool aligned) {
+  if (!fp8_grad_sizes_ok(t, R, experts, m, n)) return 0;
+  return with_slack(matmul_fp8_grad_bytes((int)type_size(t), R, experts, m, n, aligned));
+}
+
 template <typename F> int by_type(int t, F f) {
   if (t == BAKRON_F32) return status(f((float*)nullptr));
   if (t == BAKRON_BF16) return status(f((BF16*)nullptr));
@@ -102,9 +113,11 @@ int bakron_quantize_fp8(int xtype, int64_t batch, int64_t rows, int64_t n, const
 
 size_t bakron_matmul_fp8_workspace_bytes(int ytype, int64_t T, int64_t R, int64_t experts, int64_t m,
                                          int64_t n) {
-  if (!type_ok(ytype) || !fp8_sizes_ok(T, R, experts, m, n)) return 0;
-  const size_t b = matmul_fp8_bytes((int)type_size(ytype), T, R, experts, m, n);
-  return b ? b + kAlign : 0;
+  return fp8_query(ytype, T, R, experts, m, n, false);
+}
+size_t bakron_matmul_fp8_aligned_workspace_bytes(int ytype, int64_t T, int64_t R, int64_t experts,
+                                                 int64_t m, int64_t n) {
+  return fp8_query(ytype, T, R, experts, m, n, true);
 }
 
 int bakron_matmul_fp8(int ytype, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n,
@@ -120,7 +133,9 @@ int bakron_matmul_fp8(int ytype, int64_t T, int64_t R, int64_t experts, int64_t 
   if (R == 0 || m == 0) return BAKRON_OK;
   const size_t es = type_size(ytype);
   const int64_t nb = blocks(n), mb = blocks(m);
-  const size_t need = matmul_fp8_bytes((int)es, T, R, experts, m, n);
+  const bool aligned = (T == 0 || fp8_rows_on_16(Xq, T > 1 ? ldx : 0, 0)) &&
+                       fp8_weights_on_16(Wq, experts, stride_w, m, ldw);
+  const size_t need = matmul_fp8_bytes((int)es, T, R, experts, m, n, aligned);
   if (need && (!workspace || (uintptr_t)workspace % kAlign || workspace_bytes < need))
     return BAKRON_EINVAL;
   if (!matrix_ok(Xq, T, n, ldx, 1) || !strided_ok(sx, T, sx_token, nb, sx_block) ||
@@ -143,9 +158,11 @@ int bakron_matmul_fp8(int ytype, int64_t T, int64_t R, int64_t experts, int64_t 
 
 size_t bakron_matmul_fp8_grad_workspace_bytes(int gtype, int64_t R, int64_t experts, int64_t m,
                                               int64_t n) {
-  if (!fp8_grad_sizes_ok(gtype, R, experts, m, n)) return 0;
-  const size_t b = matmul_fp8_grad_bytes((int)type_size(gtype), R, experts, m, n);
-  return b ? b + kAlign : 0;
+  return fp8_grad_query(gtype, R, experts, m, n, false);
+}
+size_t bakron_matmul_fp8_grad_aligned_workspace_bytes(int gtype, int64_t R, int64_t experts, int64_t m,
+                                                      int64_t n) {
+  return fp8_grad_query(gtype, R, experts, m, n, true);
 }
 
 int bakron_matmul_fp8_grad(int gtype, int64_t R, int64_t experts, int64_t m, int64_t n, const void* G,
@@ -157,7 +174,8 @@ int bakron_matmul_fp8_grad(int gtype, int64_t R, int64_t experts, int64_t m, int
   if (R == 0 || n == 0) return BAKRON_OK;
   const size_t es = type_size(gtype);
   const int64_t nb = blocks(n), mb = blocks(m);
-  const size_t need = matmul_fp8_grad_bytes((int)es, R, experts, m, n);
+  const size_t need = matmul_fp8_grad_bytes((int)es, R, experts, m, n,
+                                            fp8_weights_on_16(Wq, experts, stride_w, m, ldw));
   if (need && (!workspace || (uintptr_t)workspace % kAlign || workspace_bytes < need))
     return BAKRON_EINVAL;
   if (!matrix_ok(G, R, m, ldg, es) || !batch_ok(Wq, experts, stride_w, m, n, ldw, 1) ||
@@ -177,8 +195,7 @@ int bakron_matmul_fp8_grad(int gtype, int64_t R, int64_t experts, int64_t m, int
 
 size_t bakron_sort_tokens_workspace_bytes(int64_t T, int64_t k, int64_t experts) {
   if (T < 0 || k < 1 || T > kMaxRoutes / k || experts < 1 || experts > kMaxExperts) return 0;
-  const size_t b = sort_tokens_bytes(T * k, experts);
-  return b ? b + kAlign : 0;
+  return with_slack(sort_tokens_bytes(T * k, experts));
 }
 
 int bakron_sort_tokens(int64_t T, int64_t k, int64_t experts, const int64_t* ids, int64_t ld,

@@ -588,8 +588,8 @@ static TilePlan fp8_plan(int es, int64_t R, int64_t experts, int64_t m, int64_t 
 struct Fp8Offsets {
   size_t x, w, parts, total;
 };
-static Fp8Offsets fp8_offsets(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n) {
-  const bool skinny = fp8_skinny(R, experts, m, n), packs = n % 16 != 0 && !skinny;
+static Fp8Offsets fp8_offsets(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n, bool aligned) {
+  const bool skinny = fp8_skinny(R, experts, m, n), packs = n % 16 != 0 && !aligned && !skinny;
   Fp8Offsets o;
   o.x = 0;
   o.w = o.x + up256(packs ? (size_t)(T * packed_ld(n)) : 0);
@@ -598,8 +598,8 @@ static Fp8Offsets fp8_offsets(int es, int64_t T, int64_t R, int64_t experts, int
   o.total = o.parts + (experts == 1 && !skinny ? (size_t)split_words(m, R, fp8_plan(es, R, m, n).splits) * 4 : 0);
   return o;
 }
-size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n) {
-  return fp8_offsets(es, T, R, experts, m, n).total;
+size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n, bool aligned) {
+  return fp8_offsets(es, T, R, experts, m, n, aligned).total;
 }
 
 template <class Mul, typename O, int B, int WR, int WC, bool ANY = false>
@@ -625,7 +625,7 @@ static hipError_t start_fp8_tile(const Groups& groups, const Fp8Tokens& X, const
 
 // Whether the direct loads can take the operands: rows on 16 bytes, and 32-bit offsets.
 static bool on_16(const Fp8Tokens& X, const Fp8Weights& W) {
-  return ((uintptr_t)X.p | X.ld | (uintptr_t)W.p | W.ld | W.stride) % 16 == 0;
+  return fp8_rows_on_16(X.p, X.ld, 0) && fp8_rows_on_16(W.p, W.ld, W.stride);  // 0 where there is one row or expert
 }
 static bool fp8_direct(const Fp8Tokens& X, const Fp8Weights& W, int64_t n) {
   const int64_t kMost = (int64_t)1 << 31;
@@ -644,8 +644,8 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
   if (R <= 0 || m <= 0) return hipSuccess;
   typedef typename std::conditional<sizeof(O) == 4, MulFP8Exact, MulFP8>::type Mul;
   const Groups groups = {offsets, experts, R};
-  Fp8Tokens X = {(const char*)Xq, ldx, T, sx, sx_token, sx_block, order, per_token};
-  Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
+  Fp8Tokens X = {(const char*)Xq, T > 1 ? ldx : 0, T, sx, sx_token, sx_block, order, per_token};
+  Fp8Weights W = {(const char*)Wq, m > 1 ? ldw : 0, experts > 1 ? stride_w : 0, m, sw, ldsw, stride_sw};
   if (T == 0) {  // rows without a token read one all the same: readable memory of that size
     X.p = W.p;
     X.ld = W.ld;
@@ -656,8 +656,9 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
   if (fp8_skinny(R, experts, m, n))
     return n % 16 == 0 && fp8_direct(X, W, n) ? start_skinny_fp8<Mul, O, false>(groups, X, W, n, Y, ldy, s)
                                               : start_skinny_fp8<Mul, O, true>(groups, X, W, n, Y, ldy, s);
-  const Fp8Offsets o = fp8_offsets(sizeof(O), T, R, experts, m, n);
-  if (n % 16 && !on_16(X, W)) {
+  const bool aligned = on_16(X, W);
+  const Fp8Offsets o = fp8_offsets(sizeof(O), T, R, experts, m, n, aligned);
+  if (n % 16 && !aligned) {
     const int64_t ld = packed_ld(n);
     char *px = (char*)ws + o.x, *pw = (char*)ws + o.w;
     hipLaunchKernelGGL(pack_fp8_kernel,
@@ -802,16 +803,16 @@ static TilePlan fp8_grad_plan(int es, int64_t R, int64_t experts, int64_t m, int
 struct Fp8GradOffsets {
   size_t w, g, parts, total;
 };
-static Fp8GradOffsets fp8_grad_offsets(int es, int64_t R, int64_t experts, int64_t m, int64_t n) {
+static Fp8GradOffsets fp8_grad_offsets(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool aligned) {
   Fp8GradOffsets o;
   o.w = 0;
-  o.g = o.w + up256(n % 16 ? (size_t)(experts * m * packed_ld(n)) : 0);
+  o.g = o.w + up256(n % 16 && !aligned ? (size_t)(experts * m * packed_ld(n)) : 0);
   o.parts = o.g + up256(es == 4 ? (size_t)(3 * R * plane_ld(m)) : m % 8 ? (size_t)(R * plane_ld(m)) : 0);
   o.total = o.parts + (experts == 1 ? (size_t)split_words(n, R, fp8_grad_plan(es, R, 1, m, n, false).splits) * 4 : 0);
   return o;
 }
-size_t matmul_fp8_grad_bytes(int es, int64_t R, int64_t experts, int64_t m, int64_t n) {
-  return fp8_grad_offsets(es, R, experts, m, n).total;
+size_t matmul_fp8_grad_bytes(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool aligned) {
+  return fp8_grad_offsets(es, R, experts, m, n, aligned).total;
 }
 
 template <class Mul, typename O, int B, int WR, int WC, bool ANY = false, int DEEP = 3>
@@ -845,12 +846,13 @@ hipError_t launch_matmul_fp8_grad(int64_t R, int64_t experts, int64_t m, int64_t
   constexpr bool wide = sizeof(G) == 4;
   typedef MulWide<typename std::conditional<std::is_same<G, F16>::value, MmaF16, MmaBF16>::type, wide ? 3 : 1> Mul;
   const Groups groups = {offsets, experts, R};
-  Fp8Weights W = {(const char*)Wq, ldw, stride_w, m, sw, ldsw, stride_sw};
-  const Fp8GradOffsets o = fp8_grad_offsets(sizeof(G), R, experts, m, n);
+  Fp8Weights W = {(const char*)Wq, m > 1 ? ldw : 0, experts > 1 ? stride_w : 0, m, sw, ldsw, stride_sw};
+  const bool aligned = fp8_rows_on_16(W.p, W.ld, W.stride);
+  const Fp8GradOffsets o = fp8_grad_offsets(sizeof(G), R, experts, m, n, aligned);
   char* b = (char*)ws;
   Fp8Gradient x = {(const char*)g, ldg * (int64_t)sizeof(G), 0};
   const bool lay_g = (wide || m % 8) && m > 0;
-  const bool lay_w = n % 16 && ((uintptr_t)W.p | W.ld | W.stride) % 16 && m > 0;
+  const bool lay_w = n % 16 && !aligned && m > 0;
   if (lay_g || lay_w) {
     Fp8Layout to = {nullptr, plane_ld(m), R * plane_ld(m), 0, b + o.w, packed_ld(n), lay_w ? experts * m : 0};
     if (lay_g) {

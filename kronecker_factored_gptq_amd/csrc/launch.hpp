@@ -357,8 +357,17 @@ hipError_t launch_quantize_fp8(int64_t batch, int64_t rows, int64_t n, const X* 
                                int64_t sX, int block_rows, uint8_t* q, int64_t ldq, int64_t sQ,
                                float* s, int64_t srow, int64_t sblock, int64_t sS, hipStream_t st);
 // Y (R x m), its rows in groups with weights of their own where offsets is not null; ws
-// holds matmul_fp8_bytes (es: the element size of Y).
-size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n);
+// holds matmul_fp8_bytes (es: the element size of Y; aligned: fp8_rows_on_16 of the tokens, if there
+// are any, and of the weights: no copies). The leading dimension of a single row and the stride of a
+// single matrix say nothing, and count as 0.
+inline bool fp8_rows_on_16(const void* p, int64_t ld, int64_t stride) {
+  return ((uintptr_t)p | (uintptr_t)ld | (uintptr_t)stride) % 16 == 0;
+}
+inline bool fp8_weights_on_16(const void* p, int64_t experts, int64_t stride, int64_t m, int64_t ld) {
+  return fp8_rows_on_16(p, m > 1 ? ld : 0, experts > 1 ? stride : 0);
+}
+size_t matmul_fp8_bytes(int es, int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n,
+                        bool aligned);
 template <typename O>
 hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, int64_t n,
                              const uint8_t* Xq, int64_t ldx, const float* sx, int64_t sx_token,
@@ -366,8 +375,9 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
                              const float* sw, int64_t ldsw, int64_t stride_sw,
                              const int32_t* offsets, const int32_t* order, int64_t per_token, O* Y,
                              int64_t ldy, void* ws, hipStream_t s);
-// dX (R x n); ws holds matmul_fp8_grad_bytes (es: the element size of G).
-size_t matmul_fp8_grad_bytes(int es, int64_t R, int64_t experts, int64_t m, int64_t n);
+// dX (R x n); ws holds matmul_fp8_grad_bytes (es: the element size of G; aligned: fp8_rows_on_16 of
+// the weights).
+size_t matmul_fp8_grad_bytes(int es, int64_t R, int64_t experts, int64_t m, int64_t n, bool aligned);
 template <typename G>
 hipError_t launch_matmul_fp8_grad(int64_t R, int64_t experts, int64_t m, int64_t n, const G* g,
                                   int64_t ldg, const uint8_t* Wq, int64_t ldw, int64_t stride_w,
