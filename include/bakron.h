@@ -580,6 +580,9 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
  *          past n are not written).
  *   s      out: block (a, b) of matrix z at s[z * stride_s + a * s_row + b * s_block].
  *          For tokens s_row = 1, s_block = rows are read fastest by the product.
+ * batch < 2^16, rows < 2^24; a matrix of around 2^37 elements and beyond (2^38 in blocks of 128
+ * rows), more than one launch holds, is BAKRON_EINVAL. Outputs must not overlap the input or
+ * each other.
  *
  * bakron_matmul_fp8: row r of Y is a token times the weights of the row's group,
  *   Y[r][i] = sum_b sx[t][b] * sw[i / 128][b] * sum_{j in block b} Xq[t][j] * Wq[i][j],

@@ -90,7 +90,9 @@ int bakron_quantize_fp8(int xtype, int64_t batch, int64_t rows, int64_t n, const
   if (batch == 0 || rows == 0 || n == 0) return BAKRON_OK;
   const size_t es = type_size(xtype);
   const int64_t na = block_rows == 1 ? rows : blocks(rows), nb = blocks(n);
-  if (na > kMaxGroups / ((nb + 3) / 4) || (block_rows > 1 && na > kMaxGroups / nb)) return BAKRON_EINVAL;
+  // a workgroup takes 16 rows of four blocks, or one block of 128 rows
+  const int64_t down = block_rows == 1 ? (rows + 15) / 16 : na, across = block_rows == 1 ? (nb + 3) / 4 : nb;
+  if (down > kMaxGroups / across) return BAKRON_EINVAL;
   if (!batch_ok(X, batch, stride_x, rows, n, ldx, es) || !batch_ok(Xq, batch, stride_q, rows, n, ldq, 1) ||
       !strided_ok(s, na, s_row, nb, s_block) || stride_s < 0 || stride_s > (INT64_MAX / 16) / batch)
     return BAKRON_EINVAL;
