@@ -683,7 +683,7 @@ int bakron_matmul_fp8_grad(int gtype, int64_t R, int64_t experts, int64_t m, int
  * for dweights alone, and may be NULL without them.
  *
  * Element types F32, BF16 and F16. Outputs must not overlap the inputs or each other
- * (BAKRON_EINVAL). T < 2^24 for the last two, R <= 2^26 for the gather; more columns or choices than one
+ * (BAKRON_EINVAL). T < 2^24 for the last two, R <= 2^26 - 4 for the gather; more columns or choices than one
  * launch holds (T n around 2^35, T k around 2^26) are BAKRON_EINVAL. Asynchronous, deterministic.
  * ------------------------------------------------------------------------ */
 size_t bakron_sort_tokens_workspace_bytes(int64_t T, int64_t k, int64_t experts);

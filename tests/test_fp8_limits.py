@@ -13,6 +13,13 @@ def at(k):
     return ctypes.c_void_p(0x1000000 * k)
 
 
+def test_the_largest_gather():
+    """R <= 2^26 - 4: a wave to a row, four to a workgroup, fewer than 2^24 workgroups. No columns: nothing is launched."""
+    gather = lambda R: bk.lib().bakron_gather_tokens(bk.F32, 5, 0, at(1), 1, 1, R, at(2), at(3), 1, None)
+    assert gather((1 << 26) - 4) == bk.OK
+    assert gather((1 << 26) - 3) == gather(1 << 26) == bk.EINVAL
+
+
 @pytest.mark.parametrize("rows,n,block_rows", [(((1 << 24) - 1), 8 * 1024 * 128, 1), (1 << 23, 128 * 128 + 1, 1),
                                                ((1 << 24) - 1, 1 << 24, 128), (1 << 24, 1, 1)])
 def test_quantize_beyond_one_launch(rows, n, block_rows):
