@@ -596,12 +596,13 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
  *            order of bakron_sort_tokens, so that no sorted copy of the tokens is needed. A
  *            row whose order names no token (below 0, or its t not below T) becomes 0.
  *   ytype    the type of Y (R x m, ldy >= m): F32, BF16 or F16.
- * For BF16 and F16 the products of a block are added by the 8-bit instructions, which cut
- * each of eight neighbouring products below 2^-13 of the largest of the eight before they
- * add them: 7 * 2^-13 of sum_j |Xq Wq| at most, 1.5e-5 of the result for Gaussian codes,
- * nothing where the codes' exponents differ by at most 3 in either operand. For F32 products
- * are exact and added in float32. Blocks are scaled and added in float32 in either case,
- * and Y is rounded once.
+ * For F32, and for few rows of any type, products are exact and added in float32. Few: up to 64
+ * of one layer (16 where m n > 2^24, 8 where m n > 2^26), up to 8 an expert on average where n >=
+ * 2048. For BF16 and F16 beyond that the products of a block are added by the 8-bit instructions, at
+ * twice the rate, which cut each of eight neighbouring products below 2^-13 of the largest of the
+ * eight before they add them: 7 * 2^-13 of sum_j |Xq Wq| at most, 1.5e-5 of the result for Gaussian
+ * codes, nothing where the codes' exponents differ by at most 3 in either operand; a caller who needs
+ * more takes F32. Blocks are scaled and added in float32 in any case, and Y is rounded once.
  *
  * bakron_matmul_fp8_grad: the input gradient, the tokens' rounding passed straight through,
  *   dX[r][j] = sum_i G[r][i] * sw[i / 128][j / 128] * Wq[i][j],

@@ -376,11 +376,13 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(Fp8Tokens X, Fp8Weights W
 // Few rows: bound by reading the weights once. A workgroup of 8 waves takes 16 RT channels of
 // one layer and all of its rows, 16 NT at a time; its waves divide k between them, U blocks
 // a turn, straight from memory to registers with the next turn on its way, and their
-// sums meet in LDS (skinny_product.hpp, with the blocks' scales). Grid: channels x (tiles of
-// rows, or experts). One row: 4096 x 4096 5.9 us on the GPU, 14336 x 4096 13.9 (4.2 TB/s);
-// 256 rows of 64 experts of 2048 x 4096 102 us (5.3 TB/s).
+// sums meet in LDS (skinny_product.hpp, with the blocks' scales). Every result type takes the
+// float16 instructions, exact products and float32 sums: the 8-bit ones' coarser sums (MulFP8) would buy
+// 0 to 4 % here (14336 x 4096, one row: 14.1 and 14.7 us; 256 rows of 64 experts of 2048 x 4096 104.0 and
+// 106.2). Grid: channels x (tiles of rows, or experts). One row: 4096 x 4096 5.9 us on the GPU,
+// 14336 x 4096 13.9 (4.2 TB/s); 256 rows of 64 experts of 2048 x 4096 102 us (5.3 TB/s).
 // ---------------------------------------------------------------------------
-template <class Mul, typename O, int RT, int NT, int U, bool ANY>
+template <typename O, int RT, int NT, int U, bool ANY>
 __global__ __launch_bounds__(512) void skinny_fp8_kernel(Groups groups, Fp8Tokens X, Fp8Weights W,
                                                          int64_t n, O* __restrict__ Y, int64_t ldy,
                                                          bool vec) {
@@ -464,7 +466,7 @@ __global__ __launch_bounds__(512) void skinny_fp8_kernel(Groups groups, Fp8Token
           const float f = has[j] ? t.f[u][j] * t.w[u] : 0.0f;
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            const f32x4 p = Mul::block(t.a[u][i][0], t.a[u][i][1], t.b[u][j][0], t.b[u][j][1]);
+            const f32x4 p = MulFP8Exact::block(t.a[u][i][0], t.a[u][i][1], t.b[u][j][0], t.b[u][j][1]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               acc[i][j][e] = __builtin_fmaf(has[j] ? p[e] : 0.0f, f, acc[i][j][e]);
@@ -526,7 +528,7 @@ static bool fp8_skinny(int64_t R, int64_t experts, int64_t m, int64_t n) {
   if (experts == 1) return R <= (m * n <= (1 << 24) ? 64 : m * n <= (1 << 26) ? 16 : 8);
   return R <= 8 * experts && n >= 2048;
 }
-template <class Mul, typename O, bool ANY>
+template <typename O, bool ANY>
 static hipError_t start_skinny_fp8(const Groups& groups, const Fp8Tokens& X, const Fp8Weights& W,
                                    int64_t n, O* Y, int64_t ldy, hipStream_t s) {
   const bool vec = vec4_ok(Y, ldy);
@@ -539,7 +541,7 @@ static hipError_t start_skinny_fp8(const Groups& groups, const Fp8Tokens& X, con
   const int rt = work >= 64 * 192 ? 4 : work >= 32 * 192 ? 2 : 1;
 #define BK_SKINNY(RT, NT, U)                                                                   \
   hipLaunchKernelGGL(                                                                          \
-      (skinny_fp8_kernel<Mul, O, RT, NT, U, ANY>),                                             \
+      (skinny_fp8_kernel<O, RT, NT, U, ANY>),                                             \
       dim3((unsigned)((W.m + 16 * RT - 1) / (16 * RT)),                                        \
            (unsigned)(groups.offsets ? groups.count : (groups.R + 16 * NT - 1) / (16 * NT))),  \
       dim3(512), 0, s, groups, X, W, n, Y, ldy, vec)
@@ -654,8 +656,8 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
     X.sb = 1;
   }
   if (fp8_skinny(R, experts, m, n))
-    return n % 16 == 0 && fp8_direct(X, W, n) ? start_skinny_fp8<Mul, O, false>(groups, X, W, n, Y, ldy, s)
-                                              : start_skinny_fp8<Mul, O, true>(groups, X, W, n, Y, ldy, s);
+    return n % 16 == 0 && fp8_direct(X, W, n) ? start_skinny_fp8<O, false>(groups, X, W, n, Y, ldy, s)
+                                              : start_skinny_fp8<O, true>(groups, X, W, n, Y, ldy, s);
   const bool aligned = on_16(X, W);
   const Fp8Offsets o = fp8_offsets(sizeof(O), T, R, experts, m, n, aligned);
   if (n % 16 && !aligned) {

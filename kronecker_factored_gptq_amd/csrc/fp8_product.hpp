@@ -30,7 +30,7 @@ struct MulFP8 {
 };
 // e4m3 codes as float16 (exact: 4 of its 11 bits, 2^-9 to 448) on the float16 instructions,
 // whose products are exact and whose sums are float32: for float32 results, which the
-// other would leave at 1.5e-5. Half its rate.
+// other would leave at 1.5e-5, and for few rows, which wait for memory. Half its rate.
 __device__ inline v8h fp8_to_f16(int lo, int hi) {
   typedef _Float16 v2h __attribute__((ext_vector_type(2)));
   const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
