@@ -602,15 +602,18 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
  * twice the rate, which cut each of eight neighbouring products below 2^-13 of the largest of the
  * eight before they add them: 7 * 2^-13 of sum_j |Xq Wq| at most, 1.5e-5 of the result for Gaussian
  * codes, nothing where the codes' exponents differ by at most 3 in either operand; a caller who needs
- * more takes F32. Blocks are scaled and added in float32 in any case, and Y is rounded once.
+ * more takes F32. Blocks are scaled and added in float32 in any case, and Y is rounded once. A block's
+ * factor is the float32 product of its two scales: below 2^-126 it has fewer bits (it is a multiple
+ * of 2^-149), from 2^128 on it is infinite, and NaN times a block whose sum is 0.
  *
  * bakron_matmul_fp8_grad: the input gradient, the tokens' rounding passed straight through,
  *   dX[r][j] = sum_i G[r][i] * sw[i / 128][j / 128] * Wq[i][j],
  * rows in groups as above (rows in no group are left as they were). G (R x m, ldg) and dX
  * (R x n, ldx) are of gtype: F32, BF16 or F16, and G is taken with all the bits it has (F32
  * values below 2^-109 with those down to 2^-133).
- * Products are exact, sums float32, one rounding to gtype. For F32 an infinity in G may make
- * the results it enters NaN. The codes are what the layer holds: there is no gradient with
+ * Products are exact, sums float32, one rounding to gtype. The sums are taken before they are
+ * scaled: values of G from about 2^113 on (448 * 64 of them below 2^128) may overflow there whatever the
+ * scale. For F32 an infinity in G may make the results it enters NaN. The codes are what the layer holds: there is no gradient with
  * respect to them.
  *
  * Outputs must not overlap the inputs (BAKRON_EINVAL; arrays are compared from their first
