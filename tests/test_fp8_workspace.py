@@ -160,6 +160,9 @@ def test_the_binding_takes_no_copies(gpu_lib, T, R, E, m, n):
         torch.cuda.synchronize()
         split = bk.lib().bakron_matmul_fp8_aligned_workspace_bytes(bk.BF16, T, R, E, m, n)
         grad = bk.lib().bakron_matmul_fp8_grad_aligned_workspace_bytes(bk.BF16, R, E, m, n)
-        assert torch.cuda.max_memory_allocated() - before <= own + max(split, grad) + 4096
+        # the allocator counts whole blocks: two of them, each up to 1 MiB larger than asked for, since what is left of a
+        # block beyond that is split off; a copy of the codes is 16 MiB (4096 rows of 4096 bytes) or more in every case here
+        assert E * m * (n // 128 * 128) >= 15 << 20
+        assert torch.cuda.max_memory_allocated() - before <= own + max(split, grad) + (2 << 20)
         if E > 1:
             assert max(split, grad) == 0
