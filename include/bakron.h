@@ -616,17 +616,18 @@ int bakron_cross_entropy_grad(int xtype, int64_t T, int64_t d, int64_t V,
  * scale. For F32 an infinity in G may make the results it enters NaN. The codes are what the layer holds: there is no gradient with
  * respect to them.
  *
- * Outputs must not overlap the inputs (BAKRON_EINVAL; arrays are compared from their first
- * element to their last). Rows of codes that start at multiples of 16 bytes are read fastest
- * (and 16-bit ones of G, with m a multiple of 8; others are copied to the workspace first, as are
- * codes whose rows are neither aligned nor whole groups of 16), and any alignment and stride
- * works. What lies between two rows of codes may be read, and up to 3 bytes behind the last, in
- * the aligned word that holds its end; it does not matter. Of the two workspace queries of a call
- * the first is for codes of any alignment, the aligned one for rows of Xq and Wq that all start at
- * multiples of 16 bytes (the matrices, and the leading dimensions and stride_w of more than one row
- * or expert), of which no copies are made: they differ where n is no multiple of 16, by a copy of all
- * codes. Where a query gives 0 workspace may be NULL.
- * 1 <= experts <= 1024; T, R < 2^24; m, n <= 2^20;
+ * Outputs must not overlap the inputs (BAKRON_EINVAL; arrays are compared from their first element
+ * to their last). Any alignment and stride works. Rows of codes that start at multiples of 16
+ * bytes are read fastest, and of a 16-bit G rows that do, with m a multiple of 8. Codes whose rows
+ * are neither aligned nor whole groups of 16 are copied to the workspace first, as is G where it
+ * is F32 or m no multiple of 8; the other unaligned ones, and tokens of 2^31 bytes and more under
+ * an order, go through registers, in two to seven times the time where there are many rows. What
+ * lies between two rows of codes may be read, and up to 3 bytes behind the last, in the aligned
+ * word that holds its end; it does not matter. Of the two workspace queries of a call the first is
+ * for codes of any alignment, the aligned one for rows of Xq and Wq that all start at multiples of
+ * 16 bytes (the matrices, and the leading dimensions and stride_w of more than one row or expert),
+ * of which no copies are made: they differ where n is no multiple of 16, by a copy of all codes.
+ * Where a query gives 0 workspace may be NULL. 1 <= experts <= 1024; T, R < 2^24; m, n <= 2^20;
  * around 2^36 elements of Xq and Wq, 2^35 of the gradient's operands and 2^36 of Y or dX and
  * beyond, more than one launch holds, are BAKRON_EINVAL. Asynchronous, deterministic.
  * ------------------------------------------------------------------------ */

@@ -152,7 +152,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(
 }
 
 // Blocks of 128 x 128, a workgroup each, held in registers between the maximum and the codes
-// (8192 x 14336 bfloat16 75 us, 4003 x 11009 float32, unaligned rows, 46).
+// (8192 x 14336 bfloat16 75 us; 4003 x 11009 float32, unaligned rows, 55 from memory, 46 where the
+// last-level cache holds some of them).
 template <typename X, bool VEC>
 __global__ __launch_bounds__(256) void quantize_blocks_kernel(
     int64_t rows, int64_t n, unsigned across, const X* __restrict__ x, int64_t ldx, int64_t sX,
@@ -218,10 +219,11 @@ hipError_t launch_quantize_fp8(int64_t batch, int64_t rows, int64_t n, const X* 
 // Y[r][i] = sum over blocks b of k of sx[t][b] sw[i / 128][b] sum_{j in b} Xq[t][j] Wq[i][j],
 // t the token of row r, W its group's: tiles of channels x rows. With `splits` ranges of the
 // steps (one layer only) their sums go to parts[range]. ANY: operands that the direct loads
-// cannot take. 8192 x 14336 x 4096 to bfloat16 461 to 485 us from card to card, 2.0 to 2.1e15
+// cannot take (8192 x 14336 x 4096 to bfloat16 1457 us with one operand off 16 bytes, 1922 with both).
+// 8192 x 14336 x 4096 to bfloat16 456 to 487 us from card to card, 2.0 to 2.1e15
 // flop/s (a library's product without block scales reaches 2.6 here); to float32, on the
-// float16 instructions, 940. 4096 tokens to 8 of 64 experts of 2048 x 4096 375 to 419 us, 1.3 to 1.5e15
-// of the products asked for: groups end inside tiles.
+// float16 instructions, 940 to 990. 4096 tokens to 8 of 64 experts of 2048 x 4096 375 to 433 us, 1.3 to
+// 1.5e15 of the products asked for: groups end inside tiles.
 // ---------------------------------------------------------------------------
 template <class Mul, typename O, int B, int WR, int WC, bool ANY>
 __global__ __launch_bounds__(64 * WR * WC) void matmul_fp8_kernel(
@@ -378,9 +380,10 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(Fp8Tokens X, Fp8Weights W
 // a turn, straight from memory to registers with the next turn on its way, and their
 // sums meet in LDS (skinny_product.hpp, with the blocks' scales). Every result type takes the
 // float16 instructions, exact products and float32 sums: the 8-bit ones' coarser sums (MulFP8) would buy
-// 0 to 4 % here (14336 x 4096, one row: 14.1 and 14.7 us; 256 rows of 64 experts of 2048 x 4096 104.0 and
-// 106.2). Grid: channels x (tiles of rows, or experts). One row: 4096 x 4096 5.9 us on the GPU,
-// 14336 x 4096 13.9 (4.2 TB/s); 256 rows of 64 experts of 2048 x 4096 102 us (5.3 TB/s).
+// 0 to 4 % here (14336 x 4096, one row: 14.1 and 14.7 us a call; 256 rows of 64 experts of 2048 x 4096
+// 104.0 and 106.2). Grid: channels x (tiles of rows, or experts). One row: 4096 x 4096 5.8 us on the GPU,
+// 14336 x 4096 14.7 us a call among others (4.0 TB/s); 256 rows of 64 experts of 2048 x 4096 102 to 110
+// us from card to card (4.9 to 5.3 TB/s).
 // ---------------------------------------------------------------------------
 template <typename O, int RT, int NT, int U, bool ANY>
 __global__ __launch_bounds__(512) void skinny_fp8_kernel(Groups groups, Fp8Tokens X, Fp8Weights W,
@@ -520,10 +523,13 @@ __global__ __launch_bounds__(512) void skinny_fp8_kernel(Groups groups, Fp8Token
 }
 
 // Whether the kernel above takes a call. Of one layer as many rows as the int8 product's takes
-// (4096 x 4096, 64 rows: 12.6 us against 14.6 of tiles). Of experts, whose number of rows each is
+// (4096 x 4096, 64 rows: 12.9 us against 15.4 of tiles; 14336 x 4096, 16 and 32 rows: 14.8 and 22.9 against
+// 18.2 and 20.8). Of experts, whose number of rows each is
 // not known here, up to 8 on average where k is long enough for eight waves: 2048 x 4096 of 64
-// experts, f16, 1 / 4 / 8 / 16 rows each on average 46 / 104 / 116 / 162 us against 39 / 143 / 129 / 133 of
-// tiles; 4096 x 1024 of 16, 2 / 8 / 32 rows: 19 / 21 / 33 against 14.7 / 15.6 / 17.6.
+// experts, f16, 1 / 4 / 8 / 16 rows each on average 80 / 106 / 119 / 167 us against 96 / 143 / 129 / 132 of
+// tiles; 4096 x 1024 of 16, 2 / 8 / 32 rows: 20 / 22 / 45 against 14.9 / 15.8 / 20.3. One expert with far
+// more than the average is gone through 16 rows at a time by its own workgroups alone: all of 512 rows
+// to one of the 64 take 320 us, even ones 118.
 static bool fp8_skinny(int64_t R, int64_t experts, int64_t m, int64_t n) {
   if (experts == 1) return R <= (m * n <= (1 << 24) ? 64 : m * n <= (1 << 26) ? 16 : 8);
   return R <= 8 * experts && n >= 2048;
@@ -533,8 +539,9 @@ static hipError_t start_skinny_fp8(const Groups& groups, const Fp8Tokens& X, con
                                    int64_t n, O* Y, int64_t ldy, hipStream_t s) {
   const bool vec = vec4_ok(Y, ldy);
   // rows at a time; channels a workgroup, more where that leaves nearly every CU one: the rows
-  // are then read less often (14336 x 4096, one row: 13.9 us with 64 channels, 15.1 with 16; 4096 x
-  // 14336 30.8 and 12.8; 64 experts of 2048 x 4096, 256 rows: 104 with 64, 116 with 32, 122 with 16)
+  // are then read less often (measured on the 8-bit instructions: 14336 x 4096, one row: 13.9 us with 64
+  // channels, 15.1 with 16; 4096 x 14336 30.8 and 12.8; 64 experts of 2048 x 4096, 256 rows: 104 with
+  // 64, 116 with 32, 122 with 16)
   const int64_t each = (groups.R + groups.count - 1) / groups.count;
   const int nt = each > 32 ? 4 : each > 16 ? 2 : 1;
   const int64_t work = W.m * (groups.offsets ? groups.count : (groups.R + 16 * nt - 1) / (16 * nt));
@@ -625,7 +632,8 @@ static hipError_t start_fp8_tile(const Groups& groups, const Fp8Tokens& X, const
   return join_fp8(W.m, groups.R, splits, parts, ldp, Y, ldy, vec, s);
 }
 
-// Whether the direct loads can take the operands: rows on 16 bytes, and 32-bit offsets.
+// Whether the direct loads can take the operands: rows on 16 bytes, and 32-bit offsets, which an order
+// needs to all tokens (8192 rows of 500000 tokens of 4096 bytes 143 us, of 530000, beyond 2 GiB, 719).
 static bool on_16(const Fp8Tokens& X, const Fp8Weights& W) {
   return fp8_rows_on_16(X.p, X.ld, 0) && fp8_rows_on_16(W.p, W.ld, W.stride);  // 0 where there is one row or expert
 }
@@ -692,8 +700,9 @@ hipError_t launch_matmul_fp8(int64_t T, int64_t R, int64_t experts, int64_t m, i
 // k-major and made 16-bit in registers (BlockTile, kTransposed). A bfloat16 or float16 G is
 // multiplied as it is, a float32 one as its three bfloat16 planes, one after the other
 // over all of k. With `splits` ranges of the steps (one layer only) their sums go to
-// parts[range]. 8192 x 4096 x 14336 bfloat16 860 to 895 us (1.1 PFLOP/s; a library's 16-bit product of
-// two matrices reaches 1.6); 4096 tokens to 4 of 32 experts of 4096 x 2048 330 to 340 us (0.82).
+// parts[range]. 8192 x 4096 x 14336 bfloat16 860 to 935 us from card to card (1.0 to 1.1 PFLOP/s; a
+// library's 16-bit product of two matrices reaches 1.6); 4096 tokens to 4 of 32 experts of 4096 x 2048 330 to
+// 350 us (0.82). ANY: G or codes off 16 bytes (2740 us and more for the former).
 // ---------------------------------------------------------------------------
 struct Fp8Gradient {
   const char* p;
